@@ -36,12 +36,19 @@ SOURCES = {
     "kvc_gather.hip": [],
     "kvc_refresh.hip": ["-ffp-contract=off"],  # fp64 cosine: one operation at a time
     "kvc_noalloc.hip": [],
+    "kvc_cache_host.cpp": [],
+    "kvc_q8.hip": ["-ffp-contract=off"],       # scales and codes: one rounding at a time
+    "kvc_q8_attend.hip": [],
+    "kvc_pages.hip": [],
 }
 EXPORTS = ["kvc_score_window", "kvc_mass_segment", "kvc_select", "kvc_gather_compact",
            "kvc_gather_paged", "kvc_qc_trigger", "kvc_partial_init", "kvc_partial_append",
            "kvc_full_sync", "kvc_compress_event", "kvc_compress_event_noalloc",
            "kvc_workspace_bytes", "kvc_segment_capacity",
-           "kvc_check_params", "kvc_strerror", "kvc_abi_version"]
+           "kvc_check_params", "kvc_strerror", "kvc_abi_version",
+           "kvc_q8_store", "kvc_q8_load", "kvc_q8_append", "kvc_q8_attend",
+           "kvc_q8_attend_workspace_bytes", "kvc_pages_alloc", "kvc_pages_fork",
+           "kvc_pages_free", "kvc_pages_copy", "kvc_pages_compact", "kvc_pages_workspace_bytes"]
 
 
 def _compile(src: str, extra: list) -> str:

@@ -5,7 +5,7 @@
 #include <math.h>
 #include <string.h>
 
-#include "kvc_internal.h"
+#include "kvc_host.h"
 
 namespace kvc {
 
@@ -145,35 +145,6 @@ static int derive(const kvc_params* p, Derived* d) {
   return KVC_OK;
 }
 
-struct Range {
-  const void* p;
-  size_t n;
-};
-
-static bool overlap(Range a, Range b) {
-  if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = uintptr_t(a.p), b0 = uintptr_t(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-// Every output must be disjoint from every input and from every other output.
-static bool any_alias(const Range* in, int n_in, const Range* out, int n_out) {
-  for (int i = 0; i < n_out; ++i) {
-    for (int j = 0; j < n_in; ++j)
-      if (overlap(out[i], in[j])) return true;
-    for (int j = i + 1; j < n_out; ++j)
-      if (overlap(out[i], out[j])) return true;
-  }
-  return false;
-}
-
-static bool aligned(const void* p, size_t a) { return (uintptr_t(p) & (a - 1)) == 0; }
-
-static int launch_status(hipError_t e) {
-  if (e != hipSuccess) return KVC_EDEVICE;
-  return hipGetLastError() == hipSuccess ? KVC_OK : KVC_EDEVICE;
-}
-
 }  // namespace kvc
 
 using namespace kvc;
@@ -187,7 +158,7 @@ const char* kvc_strerror(int status) {
     case KVC_OK: return "ok";
     case KVC_NOOP: return "no eviction needed: T <= budget (identity copy enqueued)";
     case KVC_EINVAL: return "invalid argument: shape or parameter out of range, NULL pointer, or aliasing outputs";
-    case KVC_EALIGN: return "misaligned pointer: bf16 tensors need 16-byte alignment";
+    case KVC_EALIGN: return "misaligned pointer: bf16 and 8-bit arrays need 16-byte alignment";
     case KVC_EWORKSPACE: return "workspace missing or smaller than kvc_workspace_bytes()";
     case KVC_EUNSUPPORTED: return "unsupported variant: head_dim must be 64 or 128 and group <= 64";
     case KVC_EDEVICE: return "HIP runtime reported a launch error";

@@ -1,0 +1,556 @@
+// Page tables on gfx950: allocation, forks, frees, copies and compaction of the
+// pages of a paged cache, all decided on the device.
+//
+// A page is free when its count is zero, and new pages are the lowest free
+// ones: there is no free list to keep in step, and the same calls give the
+// same tables.  Finding them takes two small launches: workgroups count the
+// free (or live) pages of their tiles, then rank them by the tile counts before
+// them and write them down in order.  A last launch applies the decisions,
+// table rows by some workgroups and page bytes by others.  Counts change by
+// integer atomics, whose order does not matter to the result.  The page copies
+// are bound by HBM, the rest by launch latency.
+#include "kvc_pages.h"
+
+namespace kvc {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kThreads = 256;
+constexpr int kPerLane = kPageTile / kThreads;  // pages a lane looks at
+enum { kRefused = 0, kShared = 1, kCopied = 2 };  // what a fork pair does
+
+__device__ __forceinline__ int below(uint64_t mask, int lane) {
+  return __popcll(mask & ((uint64_t(1) << lane) - 1));
+}
+
+// Sum over the workgroup, in every thread.
+__device__ __forceinline__ int block_sum(int x, int* sh) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return sh[0] + sh[1] + sh[2] + sh[3];
+}
+
+// Exclusive prefix sum over the workgroup's threads; *total in every thread.
+__device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int incl = x;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int y = __shfl_up(incl, off);
+    if (lane >= off) incl += y;
+  }
+  __syncthreads();
+  if (lane == 63) sh[wave] = incl;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) base += w < wave ? sh[w] : 0;
+  *total = sh[0] + sh[1] + sh[2] + sh[3];
+  return base + incl - x;
+}
+
+// One tile's pages in order: wave w has its w-th quarter, 64 pages a step.
+// Bit i of the result: the lane's page of step i has a count above zero.
+__device__ __forceinline__ uint32_t tile_live(const int32_t* refs, int n, int tile, int* first) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  *first = tile * kPageTile + wave * (kPageTile / 4) + lane;
+  int r[kPerLane];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int id = *first + i * 64;
+    r[i] = id < n ? refs[id] : 0;
+  }
+  uint32_t live = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) live |= r[i] > 0 ? 1u << i : 0u;
+  return live;
+}
+
+__device__ __forceinline__ int tile_size(int n, int tile) {
+  const int left = n - tile * kPageTile;
+  return left < kPageTile ? left : kPageTile;
+}
+
+// Live pages of each tile, by the first n_tiles workgroups of a launch.
+__device__ __forceinline__ void count_tile(const Pages& t, int tile, int32_t* count, int* sh) {
+  int first;
+  const uint32_t live = tile_live(t.refs, t.n, tile, &first);
+  const int total = block_sum(__popc(live), sh);
+  if (threadIdx.x == 0) count[tile] = total;
+}
+
+// Live pages before this tile, and in all tiles.
+__device__ __forceinline__ int live_before(const int32_t* count, int n_tiles, int tile, int* sh,
+                                           int* all) {
+  int before = 0, sum = 0;
+  for (int i = threadIdx.x; i < n_tiles; i += kThreads) {
+    const int x = count[i];
+    sum += x;
+    before += i < tile ? x : 0;
+  }
+  before = block_sum(before, sh);
+  *all = block_sum(sum, sh);
+  return before;
+}
+
+// Writes the tile's free pages to list[rank]; the number of free pages to
+// meta[0].
+__device__ __forceinline__ void list_free(const Pages& t, int tile, int n_tiles,
+                                          const int32_t* count, int32_t* list, int32_t* meta,
+                                          int* sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int all, first;
+  const uint32_t live = tile_live(t.refs, t.n, tile, &first);
+  const int before = live_before(count, n_tiles, tile, sh, &all);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i)
+    mine += __popcll(__ballot(first + i * 64 < t.n && !(live >> i & 1)));
+  __syncthreads();
+  if (lane == 0) sh[wave] = mine;
+  __syncthreads();
+  int rank = tile * kPageTile - before;
+  for (int w = 0; w < wave; ++w) rank += sh[w];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const bool free = first + i * 64 < t.n && !(live >> i & 1);
+    const uint64_t m = __ballot(free);
+    if (free) list[rank + below(m, lane)] = first + i * 64;
+    rank += __popcll(m);
+  }
+  if (tile == 0 && threadIdx.x == 0) meta[0] = t.n - all;
+}
+
+__device__ __forceinline__ bool is_page(const Pages& t, int32_t p) {
+  return uint32_t(p) < uint32_t(t.n);
+}
+
+// --- alloc -------------------------------------------------------------------
+
+// Entries that a sequence's want covers, or -1 when it is refused.
+__device__ __forceinline__ int wanted(const Pages& t, int32_t want) {
+  if (want < 0 || int64_t(want) > int64_t(t.tb) * t.bs) return -1;
+  return int((int64_t(want) + t.bs - 1) / t.bs);
+}
+
+__global__ __launch_bounds__(kThreads) void k_alloc_count(Pages t, int n_tiles, const int32_t* want,
+                                                          int32_t* count, int32_t* need) {
+  __shared__ int sh[4];
+  if (int(blockIdx.x) < n_tiles) return count_tile(t, blockIdx.x, count, sh);
+  const int b = int(blockIdx.x) - n_tiles;
+  const int entries = wanted(t, want[b]);
+  const int32_t* row = t.table + size_t(b) * t.tb;
+  int miss = 0;
+  for (int j = threadIdx.x; j < entries; j += kThreads) miss += is_page(t, row[j]) ? 0 : 1;
+  miss = block_sum(miss, sh);
+  if (threadIdx.x == 0) need[b] = miss;
+}
+
+__global__ __launch_bounds__(kThreads) void k_alloc_list(Pages t, int n_tiles, const int32_t* count,
+                                                         int32_t* list, int32_t* meta,
+                                                         const int32_t* need, int32_t* offset) {
+  __shared__ int sh[4];
+  if (int(blockIdx.x) < n_tiles) return list_free(t, blockIdx.x, n_tiles, count, list, meta, sh);
+  // Requests before each sequence's; a sum past 2^31 - 1 stays there.
+  int64_t base = 0;
+  for (int b0 = 0; b0 < t.B; b0 += kThreads) {
+    const int b = b0 + int(threadIdx.x);
+    int total;
+    const int off = block_scan(b < t.B ? need[b] : 0, sh, &total);
+    const int64_t at = base + off;
+    if (b < t.B) offset[b] = at < 0x7fffffff ? int32_t(at) : 0x7fffffff;
+    base += total;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_alloc_apply(Pages t, const int32_t* want,
+                                                          const int32_t* list, const int32_t* meta,
+                                                          const int32_t* need, const int32_t* offset,
+                                                          int32_t* status) {
+  __shared__ int sh[4];
+  const int b = blockIdx.x;
+  const int entries = wanted(t, want[b]), n = need[b], off = offset[b];
+  const bool fits = int64_t(off) + n <= meta[0];
+  if (threadIdx.x == 0) status[b] = entries < 0 ? 2 : (n == 0 || fits ? 0 : 1);
+  if (n == 0 || !fits) return;
+  int32_t* row = t.table + size_t(b) * t.tb;
+  int rank = off;
+  for (int j0 = 0; j0 < entries; j0 += kThreads) {
+    const int j = j0 + int(threadIdx.x);
+    const bool miss = j < entries && !is_page(t, row[j]);
+    int total;
+    const int at = block_scan(miss ? 1 : 0, sh, &total);
+    if (miss) {
+      const int32_t p = list[rank + at];
+      row[j] = p;
+      t.refs[p] = 1;
+    }
+    rank += total;
+  }
+}
+
+// --- copies ------------------------------------------------------------------
+
+// One chunk of page `from` to page `to`, in the buffer the chunk belongs to.
+__device__ __forceinline__ void copy_chunk(const Buffers& f, uint32_t chunk, int from, int to) {
+  int i = 0;
+  while (i + 1 < f.n && chunk >= f.b[i + 1].first) ++i;
+  const int64_t at = int64_t(chunk - f.b[i].first) * kCopyChunk;
+  const int64_t left = f.b[i].bytes - at;
+  const int size = int(left < kCopyChunk ? left : kCopyChunk);
+  const char* src = f.b[i].base + int64_t(from) * f.b[i].bytes + at;
+  char* dst = f.b[i].base + int64_t(to) * f.b[i].bytes + at;
+  if (f.b[i].unit == 16) {
+    const u32x4* a = reinterpret_cast<const u32x4*>(src);
+    u32x4* z = reinterpret_cast<u32x4*>(dst);
+    const int n = size / 16, e = threadIdx.x;
+    u32x4 x, y;
+    if (e < n) x = a[e];
+    if (e + kThreads < n) y = a[e + kThreads];
+    if (e < n) z[e] = x;
+    if (e + kThreads < n) z[e + kThreads] = y;
+  } else if (f.b[i].unit >= 4) {
+    for (int e = threadIdx.x; e < size / 4; e += kThreads)
+      reinterpret_cast<uint32_t*>(dst)[e] = reinterpret_cast<const uint32_t*>(src)[e];
+  } else {
+    for (int e = threadIdx.x; e < size; e += kThreads) dst[e] = src[e];
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_pages_copy(int n, int n_pairs, const int32_t* src,
+                                                         const int32_t* dst, Buffers f) {
+  const uint64_t items = uint64_t(n_pairs) * f.chunks;
+  for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = int(it / f.chunks);
+    const int32_t from = src[i], to = dst[i];
+    if (uint32_t(from) < uint32_t(n) && uint32_t(to) < uint32_t(n) && from != to)
+      copy_chunk(f, uint32_t(it % f.chunks), from, to);
+  }
+}
+
+// --- fork --------------------------------------------------------------------
+
+__device__ __forceinline__ bool is_seq(const Pages& t, int32_t b) {
+  return uint32_t(b) < uint32_t(t.B);
+}
+
+__device__ __forceinline__ int length_of(const Pages& t, int b) {
+  const int len = t.seq_len[b], cap = t.tb * t.bs;
+  return len < 0 ? 0 : (len < cap ? len : cap);
+}
+
+// Tile counts, and in the last workgroup what every pair does and which of the
+// new pages it takes.
+__global__ __launch_bounds__(kThreads) void k_fork_plan(Pages t, int n_tiles, int n_pairs,
+                                                        const int32_t* src, const int32_t* dst,
+                                                        int32_t* count, int32_t* mark,
+                                                        int32_t* kind, int32_t* rank,
+                                                        int32_t* from) {
+  __shared__ int sh[4];
+  if (int(blockIdx.x) < n_tiles) return count_tile(t, blockIdx.x, count, sh);
+  // mark[b]: the first pair whose dst is b
+  for (int b = threadIdx.x; b < t.B; b += kThreads)
+    __hip_atomic_store(&mark[b], 0x7fffffff, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  for (int i = threadIdx.x; i < n_pairs; i += kThreads)
+    if (is_seq(t, dst[i])) atomicMin(&mark[dst[i]], i);
+  __syncthreads();
+  int base = 0;
+  for (int i0 = 0; i0 < n_pairs; i0 += kThreads) {
+    const int i = i0 + int(threadIdx.x);
+    int what = kRefused, page = -1;
+    if (i < n_pairs) {
+      const int32_t a = src[i], z = dst[i];
+      auto first = [&](int b) {
+        return __hip_atomic_load(&mark[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      };
+      if (is_seq(t, a) && is_seq(t, z) && first(z) == i && first(a) == 0x7fffffff) {
+        const int len = length_of(t, a), whole = len / t.bs;
+        what = kShared;
+        if (len % t.bs) {
+          page = t.table[size_t(a) * t.tb + whole];
+          if (is_page(t, page)) what = kCopied;
+        }
+      }
+    }
+    int total;
+    const int r = base + block_scan(what == kCopied ? 1 : 0, sh, &total);
+    if (i < n_pairs) {
+      kind[i] = what;
+      rank[i] = r;
+      from[i] = page;
+    }
+    base += total;
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void k_list(Pages t, int n_tiles, const int32_t* count,
+                                                   int32_t* list, int32_t* meta) {
+  __shared__ int sh[4];
+  list_free(t, blockIdx.x, n_tiles, count, list, meta, sh);
+}
+
+// The first n_rows workgroups write one pair's table row each, the others copy
+// page chunks.
+__global__ __launch_bounds__(kThreads) void k_fork_apply(Pages t, int n_pairs, int n_rows,
+                                                         const int32_t* src, const int32_t* dst,
+                                                         const int32_t* kind, const int32_t* rank,
+                                                         const int32_t* from, const int32_t* list,
+                                                         const int32_t* meta, int32_t* status,
+                                                         Buffers f) {
+  const int n_free = meta[0];
+  if (int(blockIdx.x) < n_rows) {
+    const int i = blockIdx.x, what = kind[i];
+    const bool fits = what != kCopied || rank[i] < n_free;
+    if (threadIdx.x == 0) status[i] = what == kRefused ? 2 : (fits ? 0 : 1);
+    if (what == kRefused || !fits) return;
+    const int a = src[i], z = dst[i], len = length_of(t, a), whole = len / t.bs;
+    const int32_t* ra = t.table + size_t(a) * t.tb;
+    int32_t* rz = t.table + size_t(z) * t.tb;
+    for (int j = threadIdx.x; j < t.tb; j += kThreads) {
+      const int32_t was = rz[j];
+      int32_t now = j < whole ? ra[j] : -1;
+      if (is_page(t, now)) {
+        atomicAdd(&t.refs[now], 1);
+      } else {
+        now = -1;
+      }
+      if (j == whole && what == kCopied) {
+        now = list[rank[i]];
+        t.refs[now] = 1;
+      }
+      if (is_page(t, was)) atomicSub(&t.refs[was], 1);
+      rz[j] = now;
+    }
+    if (threadIdx.x == 0) t.seq_len[z] = len;
+    return;
+  }
+  const uint64_t items = uint64_t(n_pairs) * f.chunks;
+  for (uint64_t it = blockIdx.x - n_rows; it < items; it += gridDim.x - n_rows) {
+    const int i = int(it / f.chunks);
+    if (kind[i] == kCopied && rank[i] < n_free)
+      copy_chunk(f, uint32_t(it % f.chunks), from[i], list[rank[i]]);
+  }
+}
+
+// --- free --------------------------------------------------------------------
+
+__global__ __launch_bounds__(kThreads) void k_pages_free(Pages t, const int32_t* ids) {
+  const int32_t b = ids[blockIdx.x];
+  if (!is_seq(t, b)) return;
+  int32_t* row = t.table + size_t(b) * t.tb;
+  // the exchange hands each entry to one workgroup where an id is named twice
+  for (int j = threadIdx.x; j < t.tb; j += kThreads) {
+    int32_t p = row[j];
+    if (is_page(t, p)) {
+      p = atomicExch(&row[j], -1);
+      if (is_page(t, p)) atomicSub(&t.refs[p], 1);
+    } else if (p != -1) {
+      row[j] = -1;
+    }
+  }
+  if (threadIdx.x == 0) t.seq_len[b] = 0;
+}
+
+// --- compact -----------------------------------------------------------------
+
+__global__ __launch_bounds__(kThreads) void k_compact_count(Pages t, int32_t* count) {
+  __shared__ int sh[4];
+  count_tile(t, blockIdx.x, count, sh);
+}
+
+// Free pages below n_live ("holes") and live ones at or past it ("movers"), each
+// in ascending order: there are as many of one as of the other.  place[p]: p
+// itself, -1 where it is free, -2 - m for the m-th mover.
+__global__ __launch_bounds__(kThreads) void k_compact_list(Pages t, int n_tiles,
+                                                           const int32_t* count, int32_t* holes,
+                                                           int32_t* movers, int32_t* place,
+                                                           int32_t* meta, int32_t* n_live_out) {
+  __shared__ int sh[4];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tile = blockIdx.x;
+  int n_live, first;
+  const uint32_t live = tile_live(t.refs, t.n, tile, &first);
+  const int before = live_before(count, n_tiles, tile, sh, &n_live);
+  // live pages below n_live: whole tiles, then the start of the one it cuts
+  const int cut = n_live / kPageTile;
+  int part = 0;
+  for (int i = threadIdx.x; i < cut; i += kThreads) part += count[i];
+  for (int id = cut * kPageTile + int(threadIdx.x); id < n_live; id += kThreads)
+    part += t.refs[id] > 0 ? 1 : 0;
+  const int low = block_sum(part, sh);
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) mine += __popcll(__ballot(live >> i & 1));
+  __syncthreads();
+  if (lane == 0) sh[wave] = mine;
+  __syncthreads();
+  int rank = before;  // live pages before this step
+  for (int w = 0; w < wave; ++w) rank += sh[w];
+#pragma unroll
+  for (int i = 0; i < kPerLane; ++i) {
+    const int id = first + i * 64;
+    const bool on = live >> i & 1;
+    const uint64_t m = __ballot(on);
+    const int r = rank + below(m, lane);
+    if (id < t.n) {
+      int32_t to = on ? id : -1;
+      if (on && id >= n_live) {
+        movers[r - low] = id;
+        to = -2 - (r - low);
+      }
+      if (!on && id < n_live) holes[id - r] = id;
+      place[id] = to;
+    }
+    rank += __popcll(m);
+  }
+  if (tile == 0 && threadIdx.x == 0) {
+    meta[0] = n_live;
+    meta[1] = n_live - low;  // moves
+    *n_live_out = n_live;
+  }
+}
+
+// Workgroups below n_rows rewrite tables and counts, the others move pages.
+__global__ __launch_bounds__(kThreads) void k_compact_apply(Pages t, int n_rows,
+                                                            const int32_t* holes,
+                                                            const int32_t* movers,
+                                                            const int32_t* place,
+                                                            const int32_t* meta,
+                                                            int32_t* table_out, int32_t* refs_out,
+                                                            int32_t* remap, Buffers f) {
+  const int n_live = meta[0], moves = meta[1];
+  if (int(blockIdx.x) < n_rows) {
+    const size_t entries = size_t(t.B) * t.tb, total = entries + size_t(t.n);
+    for (size_t e = size_t(blockIdx.x) * kThreads + threadIdx.x; e < total;
+         e += size_t(n_rows) * kThreads) {
+      const bool entry = e < entries;
+      const int32_t p = entry ? t.table[e] : int32_t(e - entries);
+      int32_t to = -1;
+      if (is_page(t, p)) {
+        to = place[p];
+        if (to <= -2) to = holes[-2 - to];
+      }
+      if (entry) {
+        table_out[e] = to;
+      } else {
+        remap[p] = to;
+        // counts: a page that stays or moves brings its own; what nobody
+        // comes to is free
+        if (to >= 0) refs_out[to] = t.refs[p];
+        if (p >= n_live) refs_out[p] = 0;
+      }
+    }
+    return;
+  }
+  const uint64_t items = uint64_t(moves) * f.chunks;
+  for (uint64_t it = blockIdx.x - n_rows; it < items; it += gridDim.x - n_rows) {
+    const int i = int(it / f.chunks);
+    copy_chunk(f, uint32_t(it % f.chunks), movers[i], holes[i]);
+  }
+}
+
+int tiles_of(const Pages& t) { return (t.n + kPageTile - 1) / kPageTile; }
+
+unsigned copy_blocks(uint64_t items) {
+  return unsigned(items < 8192 ? items : 8192);
+}
+
+}  // namespace
+
+PagesWs pages_ws(const Pages& t, int n_pairs) {
+  PagesWs w{};
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = (off + n + 63) & ~size_t(63);  // 256 bytes
+    return at;
+  };
+  w.meta = take(64);
+  w.count = take(size_t(tiles_of(t)));
+  w.list = take(size_t(t.n));
+  w.movers = take(size_t(t.n));
+  w.place = take(size_t(t.n));
+  w.need = take(size_t(t.B));
+  w.offset = take(size_t(t.B));
+  w.kind = take(size_t(n_pairs));
+  w.rank = take(size_t(n_pairs));
+  w.from = take(size_t(n_pairs));
+  w.total = off;
+  return w;
+}
+
+hipError_t launch_pages_alloc(const Pages& t, const int32_t* want, int32_t* status, int32_t* ws,
+                              hipStream_t s) {
+  const PagesWs w = pages_ws(t, 0);
+  const int tiles = tiles_of(t);
+  k_alloc_count<<<unsigned(tiles + t.B), kThreads, 0, s>>>(t, tiles, want, ws + w.count, ws + w.need);
+  k_alloc_list<<<unsigned(tiles + 1), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list,
+                                                        ws + w.meta, ws + w.need, ws + w.offset);
+  k_alloc_apply<<<unsigned(t.B), kThreads, 0, s>>>(t, want, ws + w.list, ws + w.meta, ws + w.need,
+                                                   ws + w.offset, status);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_fork(const Pages& t, int n_pairs, const int32_t* src, const int32_t* dst,
+                             const Buffers* groups, int n_groups, int32_t* status, int32_t* ws,
+                             hipStream_t s) {
+  const PagesWs w = pages_ws(t, n_pairs);
+  const int tiles = tiles_of(t);
+  k_fork_plan<<<unsigned(tiles + 1), kThreads, 0, s>>>(t, tiles, n_pairs, src, dst, ws + w.count,
+                                                       ws + w.need, ws + w.kind, ws + w.rank,
+                                                       ws + w.from);
+  k_list<<<unsigned(tiles), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list, ws + w.meta);
+  for (int gr = 0; gr < n_groups; ++gr) {
+    const int rows = gr == 0 ? n_pairs : 0;
+    const unsigned blocks = unsigned(rows) + copy_blocks(uint64_t(n_pairs) * groups[gr].chunks);
+    if (blocks == 0) continue;
+    k_fork_apply<<<blocks, kThreads, 0, s>>>(t, n_pairs, rows, src, dst, ws + w.kind, ws + w.rank,
+                                             ws + w.from, ws + w.list, ws + w.meta, status,
+                                             groups[gr]);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_free(const Pages& t, int n_ids, const int32_t* ids, hipStream_t s) {
+  k_pages_free<<<unsigned(n_ids), kThreads, 0, s>>>(t, ids);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_copy(int n_blocks, int n_pairs, const int32_t* src, const int32_t* dst,
+                             const Buffers* groups, int n_groups, hipStream_t s) {
+  for (int gr = 0; gr < n_groups; ++gr) {
+    const unsigned blocks = copy_blocks(uint64_t(n_pairs) * groups[gr].chunks);
+    if (blocks == 0) continue;
+    k_pages_copy<<<blocks, kThreads, 0, s>>>(n_blocks, n_pairs, src, dst, groups[gr]);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_compact(const Pages& t, const Buffers* groups, int n_groups,
+                                int32_t* table_out, int32_t* refs_out, int32_t* remap,
+                                int32_t* n_live, int32_t* ws, hipStream_t s) {
+  const PagesWs w = pages_ws(t, 0);
+  const int tiles = tiles_of(t);
+  k_compact_count<<<unsigned(tiles), kThreads, 0, s>>>(t, ws + w.count);
+  k_compact_list<<<unsigned(tiles), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list,
+                                                      ws + w.movers, ws + w.place, ws + w.meta,
+                                                      n_live);
+  const size_t entries = size_t(t.B) * t.tb + size_t(t.n);
+  for (int gr = 0; gr < n_groups; ++gr) {
+    size_t rows = gr == 0 ? (entries + 4 * kThreads - 1) / (4 * kThreads) : 0;
+    if (rows > 2048) rows = 2048;
+    const unsigned blocks =
+        unsigned(rows) + copy_blocks(uint64_t(t.n / 2) * groups[gr].chunks);  // at most n/2 moves
+    if (blocks == 0) continue;
+    k_compact_apply<<<blocks, kThreads, 0, s>>>(t, int(rows), ws + w.list, ws + w.movers,
+                                                ws + w.place, ws + w.meta, table_out, refs_out,
+                                                remap, groups[gr]);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace kvc

@@ -1,0 +1,73 @@
+// 8-bit paged cache: declarations shared by its kernels and host code, and the
+// device code that turns values into codes and back.
+#pragma once
+
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// Quotient by a divisor known at launch: q = (mulhi(x, m) + x) >> s, exact for
+// 0 <= x < 2^31 (m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d)).
+struct FastDiv {
+  uint32_t d, m, s;
+};
+
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < d) ++s;
+  const uint64_t m = ((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1;
+  return FastDiv{d, uint32_t(m), s};
+}
+
+__host__ __device__ __forceinline__ uint32_t quot(FastDiv f, uint32_t x) {
+  return uint32_t(((uint64_t(x) * f.m) >> 32) + x) >> f.s;
+}
+
+// A cache after validation.
+struct Q8 {
+  int B, H, D, bs, tb, cap, fmt;
+  uint32_t n_blocks;
+  FastDiv div;  // by bs
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  const int32_t* table;
+  const int32_t* seq_len;
+};
+
+__device__ __forceinline__ int q8_len(const Q8& c, int b) {
+  const int len = c.seq_len[b];
+  return len < 0 ? 0 : (len < c.cap ? len : c.cap);
+}
+
+// Page of logical block j of sequence b, or -1.
+__device__ __forceinline__ int q8_page(const Q8& c, int b, int j) {
+  const int32_t p = c.table[size_t(b) * c.tb + j];
+  return uint32_t(p) < c.n_blocks ? p : -1;
+}
+
+// Keys per workgroup of the attention: 256 up to 64 pieces of a sequence, then
+// twice as many until 2048.  It depends on the sequence's own length only, so
+// a head's sums are taken in the same order whatever else is in the launch.
+__host__ __device__ inline int q8_chunk(int len) {
+  int c = 256;
+  while (c < 2048 && len > 64 * c) c *= 2;
+  return c;
+}
+// The most pieces that any length up to cap is cut into.
+inline int q8_max_pieces(int cap) {
+  if (cap <= 64 * 256) return cap > 0 ? (cap + 255) / 256 : 1;
+  const int n = (cap + 2047) / 2048;
+  return n > 64 ? n : 64;
+}
+
+hipError_t launch_q8_store(const Q8& c, int T, int TS, const int32_t* kept, int n_kept,
+                           const void* k, const void* v, hipStream_t s);
+hipError_t launch_q8_load(const Q8& c, int T, int TS, void* k_out, void* v_out, hipStream_t s);
+hipError_t launch_q8_append(const Q8& c, int W, const void* k_new, const void* v_new,
+                            hipStream_t s);
+hipError_t launch_q8_attend(const Q8& c, int G, int W, float c_log2, const void* q, void* out,
+                            float* lse, float* part, hipStream_t s);
+
+}  // namespace kvc

@@ -10,6 +10,7 @@ Tensor conventions (see include/kvc.h for the full layouts):
   bf16 data     torch.bfloat16 (or torch.uint16 / torch.int16 bit views)
   u64 credit    torch.int64 holding the unsigned bit pattern
   i32 indices   torch.int32
+  8-bit codes   torch.float8_e4m3fn or torch.int8 (the dtype is the format)
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20   # KVC_NOALLOC_SCRATCH_BYTES
 POOL_AVG, POOL_MAX = 0, 1
 AGG_SUM, AGG_MAX = 0, 1
 QUOTA_MASS, QUOTA_UNIFORM = 0, 1
+Q8_E4M3, Q8_INT8 = 0, 1
 
 
 class KvcError(RuntimeError):
@@ -49,6 +51,29 @@ class _CParams(ctypes.Structure):
         ("seg_fixed", ctypes.c_int32), ("quota_mode", ctypes.c_int32),
         ("valid_len", ctypes.c_void_p),
     ]
+
+
+class _CQ8Cache(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("table_blocks", ctypes.c_int32),
+        ("max_len", ctypes.c_int32), ("format", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("n_blocks", ctypes.c_int64),
+        ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p),
+    ]
+
+
+class _CPageTable(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("table_blocks", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("n_blocks", ctypes.c_int32),
+        ("table", ctypes.c_void_p), ("seq_len", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+    ]
+
+
+class _CPageBuffer(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
 
 
 @dataclass
@@ -144,6 +169,18 @@ def lib() -> ctypes.CDLL:
                                vp, vp, ctypes.c_int32, vp, vp],
         "kvc_full_sync": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, vp, vp,
                           ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
+        "kvc_q8_store": [vp, ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, vp],
+        "kvc_q8_load": [vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
+        "kvc_q8_append": [vp, ctypes.c_int32, vp, vp, vp],
+        "kvc_q8_attend": [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, sz,
+                          vp],
+        "kvc_q8_attend_workspace_bytes": [vp, ctypes.c_int32, ctypes.c_int32],
+        "kvc_pages_alloc": [vp, vp, vp, vp, sz, vp],
+        "kvc_pages_fork": [vp, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp, vp, sz, vp],
+        "kvc_pages_free": [vp, ctypes.c_int32, vp, vp],
+        "kvc_pages_copy": [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp],
+        "kvc_pages_compact": [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, sz, vp],
+        "kvc_pages_workspace_bytes": [vp, ctypes.c_int32],
         "kvc_workspace_bytes": [P],
         "kvc_segment_capacity": [P],
         "kvc_check_params": [P],
@@ -154,7 +191,9 @@ def lib() -> ctypes.CDLL:
         fn = getattr(L, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    L.kvc_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("kvc_workspace_bytes", "kvc_q8_attend_workspace_bytes",
+                 "kvc_pages_workspace_bytes"):
+        getattr(L, name).restype = ctypes.c_size_t
     L.kvc_strerror.restype = ctypes.c_char_p
     if L.kvc_abi_version() != ABI_VERSION:
         raise RuntimeError(f"{LIB_PATH} has ABI version {L.kvc_abi_version()}, this binding "
@@ -484,3 +523,285 @@ def full_sync(part_pos, k_part, v_part, k_full, v_full, t_from: int, stream=None
         int(t_from), TS, _ptr(k_full, _BF16_LIKE, (NH, TS, d), "k_full"),
         _ptr(v_full, _BF16_LIKE, (NH, TS, d), "v_full"), _stream(stream))
     _check(rc, "kvc_full_sync")
+
+
+# ---------------------------------------------------------------------------
+# 8-bit paged cache and page tables (include/kvc.h documents each call)
+# ---------------------------------------------------------------------------
+
+_Q8_FORMAT = {torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8}
+
+
+class _On:
+    """Device and stream of a call on tensors of `device`: the given stream or
+    that device's current one.  Inside, the device is current and so is the
+    stream, so that what is allocated belongs to it."""
+
+    def __init__(self, device, stream):
+        self.raw = torch.cuda.current_stream(device) if stream is None else stream
+        if self.raw.device != device:
+            raise ValueError(f"stream on {self.raw.device}, tensors on {device}")
+        here = stream is None and torch.cuda.current_device() == device.index
+        self.ctx = None if here else torch.cuda.stream(self.raw)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.raw.cuda_stream
+
+    def __exit__(self, *a):
+        if self.ctx is not None:
+            self.ctx.__exit__(*a)
+
+
+def _one_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
+
+
+def _opt_ws(ws, n, device):
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace: contiguous uint8 tensor on the cache's GPU expected")
+    return ws
+
+
+class Q8Cache:
+    """An 8-bit paged cache: k_pool, v_pool [n_blocks, kv_heads, block_size, d]
+    (torch.float8_e4m3fn or torch.int8), k_scale, v_scale fp32 [n_blocks,
+    kv_heads], table int32 [n_seqs, table_blocks], seq_len int32 [n_seqs].
+    A handle that the calls below share: the tensors are checked once, here,
+    and kept; change their contents freely, not the handle.  max_len bounds
+    seq_len (0: the table's room) and sizes the launches."""
+
+    def __init__(self, k_pool, v_pool, k_scale, v_scale, table, seq_len, max_len: int = 0):
+        if k_pool.dtype not in _Q8_FORMAT:
+            raise TypeError(f"k_pool: dtype {k_pool.dtype} not in {tuple(_Q8_FORMAT)}")
+        if k_pool.dim() != 4 or table.dim() != 2:
+            raise ValueError("k_pool: 4 dimensions expected, table: 2")
+        n, H, bs, d = k_pool.shape
+        B, tb = table.shape
+        c = _CQ8Cache(n_seqs=B, kv_heads=H, head_dim=d, block_size=bs, table_blocks=tb,
+                      max_len=int(max_len), format=_Q8_FORMAT[k_pool.dtype], reserved=0, n_blocks=n)
+        c.k_pool = _ptr(k_pool, (k_pool.dtype,), (n, H, bs, d), "k_pool")
+        c.v_pool = _ptr(v_pool, (k_pool.dtype,), (n, H, bs, d), "v_pool")
+        c.k_scale = _ptr(k_scale, (torch.float32,), (n, H), "k_scale")
+        c.v_scale = _ptr(v_scale, (torch.float32,), (n, H), "v_scale")
+        c.table = _ptr(table, (torch.int32,), (B, tb), "table")
+        c.seq_len = _ptr(seq_len, (torch.int32,), (B,), "seq_len")
+        self.device = k_pool.device
+        _one_device(self.device, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, table=table,
+                    seq_len=seq_len)
+        self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
+        self.table, self.seq_len = table, seq_len
+        self.heads, self.head_dim = B * H, d
+        self._c, self._ref = c, ctypes.addressof(c)
+
+    def attend_workspace_bytes(self, group: int, window: int = 1) -> int:
+        n = int(lib().kvc_q8_attend_workspace_bytes(self._ref, int(group), int(window)))
+        if n == ctypes.c_size_t(-1).value:
+            raise KvcError(-1, "kvc_q8_attend_workspace_bytes")
+        return n
+
+
+def q8_store(cache: Q8Cache, k, v, kept=None, T: int = 0, stream=None):
+    """Writes rows of k, v (bf16 [heads, t_stride, d], T of them valid, 0 = all)
+    into the cache's pages: the rows kept (int32 [heads, n_kept]), or the last
+    seq_len.  Returns the cache."""
+    if k.dim() != 3:
+        raise ValueError("k: 3 dimensions expected")
+    shp = (cache.heads, k.shape[1], cache.head_dim)
+    n_kept = 0 if kept is None else kept.shape[1]
+    _one_device(cache.device, k=k, v=v, kept=kept)
+    with _On(cache.device, stream) as s:
+        rc = lib().kvc_q8_store(cache._ref, int(T) or shp[1], shp[1],
+                                _ptr(kept, (torch.int32,), (cache.heads, n_kept), "kept"), n_kept,
+                                _ptr(k, _BF16_LIKE, shp, "k"), _ptr(v, _BF16_LIKE, shp, "v"), s)
+    _check(rc, "kvc_q8_store")
+    return cache
+
+
+def q8_load(cache: Q8Cache, T: int, k_out=None, v_out=None, want_v: bool = True, stream=None):
+    """The last T positions as bf16 rows, left-padded with zeros: returns (k, v),
+    [heads, t_stride >= T, d] (want_v false and v_out None: (k, None))."""
+    _one_device(cache.device, k_out=k_out, v_out=v_out)
+    with _On(cache.device, stream) as s:
+        if k_out is None:
+            k_out = torch.empty((cache.heads, T, cache.head_dim), dtype=torch.bfloat16,
+                                device=cache.device)
+        if v_out is None and want_v:
+            v_out = torch.empty_like(k_out)
+        shp = (cache.heads, k_out.shape[1], cache.head_dim)
+        rc = lib().kvc_q8_load(cache._ref, int(T), shp[1], _ptr(k_out, _BF16_LIKE, shp, "k_out"),
+                               _ptr(v_out, _BF16_LIKE, shp, "v_out"), s)
+    _check(rc, "kvc_q8_load")
+    return k_out, v_out
+
+
+def q8_append(cache: Q8Cache, k_new, v_new, stream=None):
+    """Appends k_new, v_new (bf16 [heads, window, d]) as the last `window`
+    positions of every sequence (seq_len counts them already).  Returns the
+    cache."""
+    if k_new.dim() != 3:
+        raise ValueError("k_new: 3 dimensions expected")
+    shp = (cache.heads, k_new.shape[1], cache.head_dim)
+    _one_device(cache.device, k_new=k_new, v_new=v_new)
+    with _On(cache.device, stream) as s:
+        rc = lib().kvc_q8_append(cache._ref, shp[1], _ptr(k_new, _BF16_LIKE, shp, "k_new"),
+                                 _ptr(v_new, _BF16_LIKE, shp, "v_new"), s)
+    _check(rc, "kvc_q8_append")
+    return cache
+
+
+def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, scale: float = 0.0,
+              ws=None, stream=None):
+    """Attention of the last `window` positions' queries q (bf16 [heads, group,
+    window, d]) over the cache.  Returns out (bf16, like q), or (out, lse) with
+    want_lse or an lse tensor (fp32 [heads, group, window])."""
+    if q.dim() != 4:
+        raise ValueError("q: 4 dimensions expected")
+    _, G, W, _ = q.shape
+    shp = (cache.heads, G, W, cache.head_dim)
+    _one_device(cache.device, q=q, out=out, lse=lse)
+    with _On(cache.device, stream) as s:
+        if out is None:
+            out = torch.empty(shp, dtype=q.dtype, device=cache.device)
+        if lse is None and want_lse:
+            lse = torch.empty(shp[:3], dtype=torch.float32, device=cache.device)
+        need = cache.attend_workspace_bytes(G, W)
+        ws = _opt_ws(ws, need, cache.device)
+        rc = lib().kvc_q8_attend(cache._ref, G, W, float(scale), _ptr(q, _BF16_LIKE, shp, "q"),
+                                 _ptr(out, _BF16_LIKE, shp, "out"),
+                                 _ptr(lse, (torch.float32,), shp[:3], "lse"), ws.data_ptr(),
+                                 ws.numel(), s)
+    _check(rc, "kvc_q8_attend")
+    return out if lse is None else (out, lse)
+
+
+class PageTable:
+    """Who owns which page: table int32 [n_seqs, table_blocks], seq_len int32
+    [n_seqs], refs int32 [n_blocks], pages of block_size positions.  A handle
+    like Q8Cache."""
+
+    def __init__(self, table, seq_len, refs, block_size: int):
+        if table.dim() != 2 or refs.dim() != 1:
+            raise ValueError("table: 2 dimensions expected, refs: 1")
+        B, tb = table.shape
+        c = _CPageTable(n_seqs=B, table_blocks=tb, block_size=int(block_size),
+                        n_blocks=refs.shape[0])
+        c.table = _ptr(table, (torch.int32,), (B, tb), "table")
+        c.seq_len = _ptr(seq_len, (torch.int32,), (B,), "seq_len")
+        c.refs = _ptr(refs, (torch.int32,), (refs.shape[0],), "refs")
+        self.device = table.device
+        _one_device(self.device, seq_len=seq_len, refs=refs)
+        self.table, self.seq_len, self.refs = table, seq_len, refs
+        self.block_size, self.n_blocks = int(block_size), refs.shape[0]
+        self._c, self._ref = c, ctypes.addressof(c)
+
+    def workspace_bytes(self, n_pairs: int = 0) -> int:
+        n = int(lib().kvc_pages_workspace_bytes(self._ref, int(n_pairs)))
+        if n == 0:
+            raise KvcError(-1, "kvc_pages_workspace_bytes")
+        return n
+
+
+class PageBuffers:
+    """Tensors indexed by page in their first dimension (pools, scales): what a
+    page id stands for in every one of them."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self._c = (_CPageBuffer * max(1, len(self.tensors)))()
+        self.n_blocks = self.tensors[0].shape[0] if self.tensors else 0
+        self.device = self.tensors[0].device if self.tensors else None
+        for i, t in enumerate(self.tensors):
+            self._c[i].base = _ptr(t, (t.dtype,), (self.n_blocks,) + tuple(t.shape[1:]),
+                                   f"buffer {i}")
+            self._c[i].page_bytes = t[:1].numel() * t.element_size()
+            _one_device(self.device, **{f"buffer {i}": t})
+        self._ref = ctypes.addressof(self._c)
+
+    def _for(self, n_blocks: int, device):
+        if self.tensors and (self.n_blocks != n_blocks or self.device != device):
+            raise ValueError(f"buffers of {self.n_blocks} pages on {self.device}, the table has "
+                             f"{n_blocks} on {device}")
+        return self._ref, len(self.tensors)
+
+
+def pages_alloc(pages: PageTable, want_len, status=None, ws=None, stream=None):
+    """Gives every sequence pages for want_len (int32 [n_seqs]) positions.
+    Returns status (int32 [n_seqs]: 0 served, 1 no room, 2 refused)."""
+    B = pages.table.shape[0]
+    _one_device(pages.device, want_len=want_len, status=status)
+    with _On(pages.device, stream) as s:
+        if status is None:
+            status = torch.empty((B,), dtype=torch.int32, device=pages.device)
+        ws = _opt_ws(ws, pages.workspace_bytes(), pages.device)
+        rc = lib().kvc_pages_alloc(pages._ref, _ptr(want_len, (torch.int32,), (B,), "want_len"),
+                                   _ptr(status, (torch.int32,), (B,), "status"), ws.data_ptr(),
+                                   ws.numel(), s)
+    _check(rc, "kvc_pages_alloc")
+    return status
+
+
+def pages_fork(pages: PageTable, src, dst, bufs: PageBuffers, status=None, ws=None, stream=None):
+    """Sequence dst[i] becomes a copy of src[i] (int32 [n_pairs]).  Returns status
+    (int32 [n_pairs])."""
+    n = src.shape[0]
+    ref, n_bufs = bufs._for(pages.n_blocks, pages.device)
+    _one_device(pages.device, src=src, dst=dst, status=status)
+    with _On(pages.device, stream) as s:
+        if status is None:
+            status = torch.empty((n,), dtype=torch.int32, device=pages.device)
+        ws = _opt_ws(ws, pages.workspace_bytes(n), pages.device)
+        rc = lib().kvc_pages_fork(pages._ref, n, _ptr(src, (torch.int32,), (n,), "src"),
+                                  _ptr(dst, (torch.int32,), (n,), "dst"), ref, n_bufs,
+                                  _ptr(status, (torch.int32,), (n,), "status"), ws.data_ptr(),
+                                  ws.numel(), s)
+    _check(rc, "kvc_pages_fork")
+    return status
+
+
+def pages_free(pages: PageTable, ids, stream=None):
+    """Frees the sequences ids (int32 [n])."""
+    _one_device(pages.device, ids=ids)
+    with _On(pages.device, stream) as s:
+        rc = lib().kvc_pages_free(pages._ref, ids.shape[0],
+                                  _ptr(ids, (torch.int32,), (ids.shape[0],), "ids"), s)
+    _check(rc, "kvc_pages_free")
+
+
+def pages_copy(src, dst, bufs: PageBuffers, stream=None):
+    """Copies page src[i] to page dst[i] (int32 [n_pairs]) in every buffer."""
+    n = src.shape[0]
+    _one_device(src.device, dst=dst)
+    ref, n_bufs = bufs._for(bufs.n_blocks, src.device)
+    with _On(src.device, stream) as s:
+        rc = lib().kvc_pages_copy(max(1, bufs.n_blocks), n, _ptr(src, (torch.int32,), (n,), "src"),
+                                  _ptr(dst, (torch.int32,), (n,), "dst"), ref, n_bufs, s)
+    _check(rc, "kvc_pages_copy")
+
+
+def pages_compact(pages: PageTable, bufs: PageBuffers, out=None, ws=None, stream=None):
+    """Moves the live pages to the front of every buffer.  Returns dict(table,
+    refs, remap, n_live): new tensors (or those of `out`), the handle's own are
+    left as they were."""
+    ref, n_bufs = bufs._for(pages.n_blocks, pages.device)
+    o = dict(out or {})
+    _one_device(pages.device, **o)
+    n, shp = pages.n_blocks, tuple(pages.table.shape)
+    with _On(pages.device, stream) as s:
+        for name, shape in (("table", shp), ("refs", (n,)), ("remap", (n,)), ("n_live", (1,))):
+            if o.get(name) is None:
+                o[name] = torch.empty(shape, dtype=torch.int32, device=pages.device)
+        ws = _opt_ws(ws, pages.workspace_bytes(), pages.device)
+        rc = lib().kvc_pages_compact(pages._ref, ref, n_bufs,
+                                     _ptr(o["table"], (torch.int32,), shp, "table"),
+                                     _ptr(o["refs"], (torch.int32,), (n,), "refs"),
+                                     _ptr(o["remap"], (torch.int32,), (n,), "remap"),
+                                     _ptr(o["n_live"], (torch.int32,), (1,), "n_live"),
+                                     ws.data_ptr(), ws.numel(), s)
+    _check(rc, "kvc_pages_compact")
+    return o

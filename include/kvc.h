@@ -80,6 +80,9 @@ enum kvc_status {
                              scratch than KVC_NOALLOC_SCRATCH_BYTES          */
 };
 
+/* 8-bit formats of a paged cache. */
+enum { KVC_Q8_E4M3 = 0, KVC_Q8_INT8 = 1 };
+
 /* Scratch held on each GPU by kvc_compress_event_noalloc (64 MiB). */
 #define KVC_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 
@@ -311,7 +314,175 @@ int kvc_compress_event_noalloc(const kvc_params* p, const void* q_win, const voi
                                void* v_out, uint64_t* credit_out, int32_t* kept_out,
                                float* u_out, void* stream);
 
-/* Workspace bytes any entry point above needs for these parameters (0 when
+/* ---------------------------------------------------------------------------
+ * 8-bit paged cache: the compacted (or whole) cache held as 8-bit codes with
+ * one fp32 scale for each (page, KV head), in the pages of kvc_gather_paged.
+ * The value of a code is code * scale of its page and head.
+ *   KVC_Q8_E4M3  codes are OCP e4m3 (4 significant bits, largest value 448);
+ *                kvc_q8_store and kvc_q8_append give a page the smallest
+ *                scale 2^e, e >= -126, with max|x| <= 448 * 2^e: coding again
+ *                under a larger scale only shifts exponents
+ *   KVC_Q8_INT8  codes -127..127; scale = max(max|x| / 127, 2^-126) and
+ *                code = rint(x * (1 / scale)), both in fp32
+ * kvc_q8_load and kvc_q8_attend take any finite non-negative scale.
+ *
+ * Layout: k_pool, v_pool 8-bit [n_blocks][kv_heads][block_size][head_dim]
+ * (16-byte aligned), k_scale, v_scale f32 [n_blocks][kv_heads], table i32
+ * [n_seqs][table_blocks], seq_len i32 [n_seqs] (device arrays).  Head n =
+ * b * kv_heads + h of the bf16 arrays is head h of sequence b; its position
+ * t lives in page table[b][t / block_size], row t % block_size.  A table
+ * entry outside [0, n_blocks) names no page: its positions are not attended,
+ * load as zeros and are not written.  seq_len is taken as clamped to [0, cap]
+ * with cap = min(max_len, table_blocks * block_size) (max_len 0: the second).
+ * Rows of a page at or past seq_len are neither read nor written; their codes
+ * may be anything.  Preconditions (not checked): the codes of attended
+ * positions are finite, and a page that is written belongs to one entry of
+ * the table. */
+typedef struct kvc_q8_cache {
+  int32_t n_seqs;        /* B sequences; 0 = nothing to do                   */
+  int32_t kv_heads;      /* H KV heads, n_seqs * kv_heads < 2^24             */
+  int32_t head_dim;      /* d, 64 or 128                                     */
+  int32_t block_size;    /* positions per page, 1..4096                      */
+  int32_t table_blocks;  /* table entries per sequence (>= 1),
+                            table_blocks * block_size <= 2^30                */
+  int32_t max_len;       /* 0, or a bound on seq_len that sizes the launches */
+  int32_t format;        /* KVC_Q8_E4M3 or KVC_Q8_INT8                       */
+  int32_t reserved;      /* 0                                                */
+  int64_t n_blocks;      /* pages in the pools, n_blocks * kv_heads *
+                            block_size < 2^32 - 1                            */
+  void* k_pool;
+  void* v_pool;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  const int32_t* seq_len;
+} kvc_q8_cache;
+
+/* Step 5 into 8-bit pages: writes slots 0..L-1 of every sequence and the
+ * scales of their pages.  k, v: bf16 [n_seqs * kv_heads][t_stride][d], rows
+ * 0..T-1 valid, T 1..2^27.  With kept (i32 [n_seqs * kv_heads][n_kept], as the event
+ * writes it) slot j of head n is row kept[n][j] (zeros where it is outside
+ * [0, T)) and L = min(seq_len, n_kept); kept NULL (n_kept 0) stores the last L
+ * = min(seq_len, T) rows: slot j is row T - L + j, the left-padded layout of
+ * kvc_params.valid_len.  A page's scale covers the slots written to it; rows
+ * past L in the last page are left as they were.  Precondition: the rows are
+ * finite.  No workspace. */
+int kvc_q8_store(const kvc_q8_cache* c, int32_t T, int32_t t_stride, const int32_t* kept,
+                 int32_t n_kept, const void* k, const void* v, void* stream);
+
+/* The cache as bf16 rows, for the event's scores or to move it: row T - L + t
+ * of k_out, v_out (bf16 [n_seqs * kv_heads][t_stride][d]) receives position t,
+ * L = seq_len, for the last min(L, T) positions; rows 0..T-L-1 are zeros
+ * (left padding), rows >= T untouched; T 1..2^27.  Each value is code * scale in fp32,
+ * rounded once.  k_out or v_out may be NULL (not loaded).  No workspace. */
+int kvc_q8_load(const kvc_q8_cache* c, int32_t T, int32_t t_stride, void* k_out, void* v_out,
+                void* stream);
+
+/* Appends: the last `window` positions of every sequence (seq_len counts them
+ * already) receive k_new, v_new (bf16 [n_seqs * kv_heads][window][d]); new row
+ * w goes to position seq_len - window + w (skipped where negative).  A page
+ * whose first row is new takes its scale from the new rows.  One that holds
+ * earlier rows keeps its scale unless the new rows alone need a larger one;
+ * then its earlier rows are coded again under the larger scale (e4m3: code *
+ * old / new rounded to nearest even; int8: rint(code * (old * (1 / new)))).
+ * The same call repeated changes nothing.  No workspace. */
+int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const void* k_new, const void* v_new,
+                  void* stream);
+
+/* Attention of the last `window` positions' queries over the cache.  q, out:
+ * bf16 [n_seqs * kv_heads][group][window][d] (the layout of q_win); query w
+ * sits at position seq_len - window + w and attends to the positions up to
+ * its own:  out = sum_t softmax_t(scale * <q, k[t]>) * v[t], in fp32 (the
+ * weights enter the matrix products as fp16).  scale 0 => 1/sqrt(d), otherwise
+ * finite and positive.  lse: optional f32 [n_seqs * kv_heads][group][window],
+ * log(sum_t exp(scale * <q, k[t]>)).  A query that attends to nothing gives
+ * zeros and lse = -inf.  group 1..64, window >= 1, group * window <= 4096.
+ * A head's results depend on its own length, queries and pages alone.
+ * ws: at least kvc_q8_attend_workspace_bytes(c, group, window), 256-byte
+ * aligned (may be NULL when that is 0). */
+int kvc_q8_attend(const kvc_q8_cache* c, int32_t group, int32_t window, float scale,
+                  const void* q, void* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes kvc_q8_attend needs; (size_t)-1 for invalid arguments (the
+ * device pointers are not looked at).  Pure host function. */
+size_t kvc_q8_attend_workspace_bytes(const kvc_q8_cache* c, int32_t group, int32_t window);
+
+/* ---------------------------------------------------------------------------
+ * Pages: who owns which page of a pool, kept on the device.  refs[p] counts
+ * the table entries that name page p; a page with refs <= 0 is free.  A new
+ * page is always the lowest free one, so the same calls give the same tables.
+ * The calls change table, seq_len and refs in place (kvc_pages_compact writes
+ * new ones); table entries outside [0, n_blocks) name no page.  Precondition
+ * (not checked): refs agrees with the tables of all its users.
+ * Requests that need new pages are served in order; from the first that does
+ * not fit on, none gets a page.  status (i32, device): 0 served, 1 no room,
+ * 2 refused; a request with status 1 or 2 changed nothing. */
+typedef struct kvc_page_table {
+  int32_t n_seqs;        /* sequences, 0..2^20 (0 = nothing to allocate or
+                            free; forks and compactions need at least one)   */
+  int32_t table_blocks;  /* entries per sequence (>= 1), table_blocks *
+                            block_size <= 2^30                               */
+  int32_t block_size;    /* positions per page, 1..4096                      */
+  int32_t n_blocks;      /* pages in the pool, 1..2^24                       */
+  int32_t* table;        /* i32 [n_seqs][table_blocks]                       */
+  int32_t* seq_len;      /* i32 [n_seqs]                                     */
+  int32_t* refs;         /* i32 [n_blocks]                                   */
+} kvc_page_table;
+
+/* An array indexed by page: page p is the page_bytes bytes at base + p *
+ * page_bytes (a pool, bf16 or 8-bit, or the scales of one). */
+typedef struct kvc_page_buffer {
+  void* base;
+  int64_t page_bytes;
+} kvc_page_buffer;
+
+/* Gives every sequence b pages for its positions 0..want_len[b]-1: entries
+ * among its first ceil(want_len[b] / block_size) that name no page receive
+ * one, all or none per sequence.  want_len: i32 [n_seqs], 0 = leave alone,
+ * negative or past the table: status 2.  seq_len is not changed.
+ * status: i32 [n_seqs]. */
+int kvc_pages_alloc(const kvc_page_table* t, const int32_t* want_len, int32_t* status, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* Forks: for each pair i, sequence dst[i] gives up the pages it holds and
+ * becomes a copy of src[i]: it shares the floor(len / block_size) full pages,
+ * and an open last page is copied to a new page in all n_bufs buffers (host
+ * array; n_bufs 0..4096).  Pages given up are free from the next call on.
+ * src, dst: i32 [n_pairs] on the device.  Status 2: an id out of range, src
+ * = dst, dst named by an earlier pair, or src named as dst by any pair.
+ * status: i32 [n_pairs]. */
+int kvc_pages_fork(const kvc_page_table* t, int32_t n_pairs, const int32_t* src,
+                   const int32_t* dst, const kvc_page_buffer* bufs, int32_t n_bufs,
+                   int32_t* status, void* ws, size_t ws_bytes, void* stream);
+
+/* Frees the sequences ids[0..n_ids-1] (i32 on the device; out of range:
+ * skipped, named twice: freed once): their pages lose one count each, their
+ * entries become -1, their lengths 0.  No workspace. */
+int kvc_pages_free(const kvc_page_table* t, int32_t n_ids, const int32_t* ids, void* stream);
+
+/* Copies page src[i] to page dst[i] in every buffer, i < n_pairs (i32 on the
+ * device; a pair with an id outside [0, n_blocks) is skipped).  Precondition:
+ * the destinations are distinct and none of them is a source.  No
+ * workspace. */
+int kvc_pages_copy(int32_t n_blocks, int32_t n_pairs, const int32_t* src, const int32_t* dst,
+                   const kvc_page_buffer* bufs, int32_t n_bufs, void* stream);
+
+/* Compacts the pool: with n_live pages in use, those at or past n_live move,
+ * in ascending order, to the free pages below it, in all buffers.  table_out
+ * (i32 [n_seqs][table_blocks]) and refs_out (i32 [n_blocks]) receive the new
+ * tables and counts, remap (i32 [n_blocks]) the new id of every page (-1: it
+ * was free), n_live (i32 [1]) the count; t's own arrays are read only, and
+ * swapping them is the caller's.  Other tables that name these pages follow by
+ * remap. */
+int kvc_pages_compact(const kvc_page_table* t, const kvc_page_buffer* bufs, int32_t n_bufs,
+                      int32_t* table_out, int32_t* refs_out, int32_t* remap, int32_t* n_live,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes kvc_pages_alloc, kvc_pages_fork (with up to n_pairs pairs)
+ * and kvc_pages_compact need; 0 for invalid arguments.  Pure host function. */
+size_t kvc_pages_workspace_bytes(const kvc_page_table* t, int32_t n_pairs);
+
+/* Workspace bytes any entry point that takes a kvc_params needs for these parameters (0 when
  * the parameters are invalid).  Pure host function. */
 size_t kvc_workspace_bytes(const kvc_params* p);
 

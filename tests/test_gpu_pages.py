@@ -1,0 +1,164 @@
+"""Page tables on the GPU against the oracle: tables, counts, lengths, statuses
+and page bytes equal."""
+import numpy as np
+import pytest
+import torch
+
+from eviction_window_qk_amd import kvc
+from oracle import pages as op
+import q8_utils as u
+
+pytestmark = pytest.mark.gpu
+
+# B, table_blocks, block_size, n_blocks
+SHAPES = [(1, 1, 1, 1), (3, 4, 16, 9), (20, 13, 24, 150), (64, 40, 16, 2000), (300, 20, 8, 4097),
+          (50, 300, 1, 9000)]
+
+
+def _buffers(seed, n, widths=((4, 16), (3,), (2, 2, 2))):
+    rng = u.rng_of(seed, n)
+    bufs = [torch.from_numpy(rng.integers(0, 256, (n,) + w).astype(np.uint8)).cuda() for w in widths]
+    bufs.append(torch.from_numpy(rng.standard_normal((n, 5)).astype(np.float32)).cuda())
+    bufs.append(torch.from_numpy(rng.integers(0, 256, (n, 5000)).astype(np.uint8)).cuda())
+    return bufs
+
+
+def _host(bufs):
+    return [b.cpu().numpy().copy() for b in bufs]
+
+
+def _check_copies(bufs, before, copies):
+    for b, was in zip(bufs, before):
+        want = was.copy()
+        for a, z in copies:
+            want[z] = was[a]
+        np.testing.assert_array_equal(b.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(s) for s in SHAPES])
+def test_alloc(shape):
+    B, tb, bs, n = shape
+    print(f"[case] alloc {shape}", flush=True)
+    t = u.random_pages(1, B, tb, bs, n)
+    g = u.pages_to_gpu(t)
+    rng = u.rng_of(2, B)
+    for step in range(4):
+        want = np.minimum(t.lens + rng.integers(0, 2 * bs * (step + 1) + 1, B), tb * bs).astype(np.int32)
+        if step == 1:
+            want[:: 3] = 0
+            want[1:: 7] = -5
+            want[2:: 11] = tb * bs + 1
+        if step == 3:
+            want[:] = tb * bs
+        st = kvc.pages_alloc(g, torch.from_numpy(want).cuda())
+        ref = op.alloc(t, want)
+        np.testing.assert_array_equal(st.cpu().numpy(), ref)
+        u.same_pages(g, t)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(s) for s in SHAPES])
+def test_fork_and_free(shape):
+    B, tb, bs, n = shape
+    print(f"[case] fork {shape}", flush=True)
+    t = u.random_pages(3, B, tb, bs, n)
+    g = u.pages_to_gpu(t)
+    tensors = _buffers(4, n)
+    bufs = kvc.PageBuffers(tensors)
+    rng = u.rng_of(5, B)
+    for step in range(4):
+        pairs = int(rng.integers(1, B + 3))
+        src = rng.integers(-1, B + 1, pairs).astype(np.int32)
+        dst = rng.integers(-1, B + 1, pairs).astype(np.int32)
+        before = _host(tensors)
+        st = kvc.pages_fork(g, torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), bufs)
+        ref, copies = op.fork(t, src, dst)
+        np.testing.assert_array_equal(st.cpu().numpy(), ref)
+        u.same_pages(g, t)
+        _check_copies(tensors, before, copies)
+        ids = rng.integers(-2, B + 2, max(1, B // 3)).astype(np.int32)
+        ids[-1] = ids[0]                                   # named twice
+        kvc.pages_free(g, torch.from_numpy(ids).cuda())
+        op.release(t, ids)
+        u.same_pages(g, t)
+
+
+def test_many_children_of_one_prompt():
+    """Every child shares the whole pages and owns its open one."""
+    B, tb, bs, n = 40, 6, 16, 60
+    t = op.Pages(np.full((B, tb), -1), np.zeros(B), np.zeros(n), bs)
+    t.table[0, :4] = [50, 3, 7, 59]
+    t.lens[0] = 50
+    t.refs[[50, 3, 7, 59]] = 1
+    g = u.pages_to_gpu(t)
+    tensors = _buffers(6, n)
+    before = _host(tensors)
+    src = np.zeros(39, np.int32)
+    dst = np.arange(1, 40, dtype=np.int32)
+    st = kvc.pages_fork(g, torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), kvc.PageBuffers(tensors))
+    ref, copies = op.fork(t, src, dst)
+    assert st.cpu().numpy().tolist() == ref.tolist() and (ref == 0).all()
+    assert t.refs[50] == 40 and len(copies) == 39
+    u.same_pages(g, t)
+    _check_copies(tensors, before, copies)
+
+
+def test_forks_past_the_free_pages():
+    B, tb, bs, n = 12, 3, 8, 6
+    t = op.Pages(np.full((B, tb), -1), np.zeros(B), np.zeros(n), bs)
+    t.table[0, :2], t.lens[0] = [5, 2], 13                 # open page
+    t.table[1, :1], t.lens[1] = [0], 8                     # whole page
+    t.refs[[5, 2, 0]] = 1
+    g = u.pages_to_gpu(t)
+    tensors = _buffers(7, n)
+    before = _host(tensors)
+    src = np.array([0, 0, 1, 0, 0, 1], np.int32)
+    dst = np.array([2, 3, 4, 5, 6, 7], np.int32)
+    st = kvc.pages_fork(g, torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), kvc.PageBuffers(tensors))
+    ref, copies = op.fork(t, src, dst)
+    assert ref.tolist() == [0, 0, 0, 0, 1, 0] and st.cpu().numpy().tolist() == ref.tolist()
+    u.same_pages(g, t)
+    _check_copies(tensors, before, copies)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(s) for s in SHAPES])
+@pytest.mark.parametrize("fill", [0.0, 0.5, 1.0])
+def test_compact(shape, fill):
+    B, tb, bs, n = shape
+    print(f"[case] compact {shape} {fill}", flush=True)
+    t = u.random_pages(8, B, tb, bs, n, fill=fill)
+    t.table[0, -1] = n + 5                                  # names no page
+    g = u.pages_to_gpu(t)
+    tensors = _buffers(9, n)
+    before = _host(tensors)
+    got = kvc.pages_compact(g, kvc.PageBuffers(tensors))
+    table, refs, remap, live, copies = op.compact(t)
+    np.testing.assert_array_equal(got["table"].cpu().numpy(), table)
+    np.testing.assert_array_equal(got["refs"].cpu().numpy(), refs)
+    np.testing.assert_array_equal(got["remap"].cpu().numpy(), remap)
+    assert int(got["n_live"][0]) == live
+    u.same_pages(g, t)                                      # the old arrays stay
+    _check_copies(tensors, before, copies)
+
+
+def test_copy_pages_skips_bad_ids_and_takes_many_buffers():
+    n = 30
+    rng = u.rng_of(10)
+    tensors = [torch.from_numpy(rng.integers(0, 256, (n, 7 + i % 40)).astype(np.uint8)).cuda() for i in range(130)]
+    before = _host(tensors)
+    src = np.array([3, -1, 5, 29, 31, 3], np.int32)
+    dst = np.array([10, 11, 40, 12, 13, 14], np.int32)
+    kvc.pages_copy(torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), kvc.PageBuffers(tensors))
+    _check_copies(tensors, before, [(3, 10), (29, 12), (3, 14)])
+
+
+def test_empty_requests():
+    t = u.random_pages(11, 3, 2, 4, 5)
+    g = u.pages_to_gpu(t)
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    bufs = kvc.PageBuffers([])
+    kvc.pages_free(g, none)
+    assert kvc.pages_fork(g, none, none, bufs).numel() == 0
+    kvc.pages_copy(none, none, bufs)
+    one = torch.tensor([0], dtype=torch.int32, device="cuda")
+    kvc.pages_copy(one, one, bufs)                          # no buffers: nothing to copy
+    u.same_pages(g, t)

@@ -1,0 +1,262 @@
+"""The 8-bit paged cache on the GPU against the oracle: codes, scales and loaded
+rows bit for bit, the attention within a derived bound."""
+import numpy as np
+import pytest
+import torch
+
+from eviction_window_qk_amd import kvc
+from oracle import q8 as oq
+import q8_utils as u
+
+pytestmark = pytest.mark.gpu
+
+FMTS = [oq.E4M3, oq.INT8]
+
+# (B, H, d, block_size, lengths, T)
+STORE = [
+    (1, 1, 64, 16, [1], 1),
+    (3, 2, 128, 16, [0, 1, 37], 40),
+    (2, 3, 128, 1, [5, 3], 7),
+    (2, 2, 64, 24, [24, 49], 50),
+    (2, 1, 128, 64, [64, 100], 130),
+    (1, 2, 128, 100, [257], 300),
+    (2, 1, 128, 128, [128, 129], 140),
+    (1, 2, 64, 256, [300], 300),
+    (1, 1, 128, 512, [700], 700),
+    (2, 1, 64, 4096, [4100, 9], 4200),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("case", STORE, ids=[f"{i}" for i in range(len(STORE))])
+def test_store_and_load(case, fmt):
+    B, H, d, bs, lens, T = case
+    print(f"[case] store {case} {u.NAMES[fmt]}", flush=True)
+    for kept_rows in (0, 1):
+        c = u.random_cache(1, B, H, d, bs, lens, fmt, holes=0.0)
+        k, v = u.random_rows(2, B * H, T + 3, d), u.random_rows(3, B * H, T + 3, d)
+        k[0, T // 2] = 0
+        kept = None
+        if kept_rows:
+            rng = u.rng_of(4, T)
+            kept = np.sort(rng.integers(-1, T + 2, (B * H, max(1, T - 1))).astype(np.int32), axis=1)
+        g = u.to_gpu(c)
+        kvc.q8_store(g, u.dev_bf16(k), u.dev_bf16(v), T=T,
+                     kept=None if kept is None else torch.from_numpy(kept).cuda())
+        oq.store(c, k, v, T, kept)
+        torch.cuda.synchronize()
+        u.same_cache(g, c)
+        for rows in (1, T, T + 5):
+            gk, gv = kvc.q8_load(g, rows)
+            if kept is not None and kept.shape[1] < max(lens):
+                continue            # rows past the kept ones hold poison
+            rk, rv = oq.load(c, rows)
+            np.testing.assert_array_equal(gk.view(torch.int16).cpu().numpy().view(np.uint16), rk)
+            np.testing.assert_array_equal(gv.view(torch.int16).cpu().numpy().view(np.uint16), rv)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+def test_store_extreme_values(fmt):
+    """Zero pages, the smallest and largest bf16 magnitudes, exact scale borders."""
+    B, H, d, bs, T = 6, 1, 64, 8, 8
+    c = u.random_cache(5, B, H, d, bs, [8] * B, fmt)
+    x = np.zeros((B, T, d), np.uint16)
+    x[1, :, :] = 0x0001                       # smallest subnormal
+    x[2, :, ::2] = 0x7F7F                     # largest finite
+    x[2, :, 1::2] = 0x8080                    # -2^-126
+    x[3] = u.synth.f32_to_bf16_bits(np.tile(np.float32([448.0, -447.0, 1.0, 0.0] * 16), (T, 1)))
+    x[4] = u.synth.f32_to_bf16_bits(np.tile(np.float32([450.0, 3.5, 17.0, -2.0] * 16), (T, 1)))
+    x[5] = u.random_rows(6, T, d)
+    g = u.to_gpu(c)
+    kvc.q8_store(g, u.dev_bf16(x), u.dev_bf16(x[::-1].copy()))
+    oq.store(c, x, x[::-1].copy(), T)
+    torch.cuda.synchronize()
+    u.same_cache(g, c)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+def test_every_code_rounds_to_nearest_even(fmt):
+    """All bf16 values of one binade range under a scale of one, ties among them."""
+    d, bs = 64, 64
+    vals = np.arange(0x3A00, 0x43E0, dtype=np.uint16)          # 2^-11 .. 448
+    vals = vals[u.synth.bf16_bits_to_f32(vals) <= (448 if fmt == oq.E4M3 else 127)]
+    x = np.zeros((1, bs, d), np.uint16)
+    x.reshape(-1)[: vals.size] = vals
+    x.reshape(-1)[-1] = u.synth.f32_to_bf16_bits(np.float32([448.0 if fmt == oq.E4M3 else 127.0]))[0]
+    c = u.random_cache(7, 1, 1, d, bs, [bs], fmt)
+    g = u.to_gpu(c)
+    neg = np.where(x == 0, x, x | 0x8000)
+    kvc.q8_store(g, u.dev_bf16(x), u.dev_bf16(neg))
+    oq.store(c, x, neg, bs)
+    torch.cuda.synchronize()
+    assert float(g.k_scale[int(c.table[0, 0]), 0]) == 1.0
+    u.same_cache(g, c)
+
+
+APPEND = [
+    # B, H, d, bs, lengths after, W
+    (4, 2, 128, 16, [1, 16, 17, 40], 1),
+    (3, 1, 64, 24, [2, 24, 50], 1),
+    (4, 2, 128, 16, [0, 3, 18, 35], 5),
+    (2, 1, 64, 1, [9, 3], 4),
+    (2, 2, 128, 256, [300, 255], 40),
+    (1, 1, 128, 64, [200], 150),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("case", APPEND, ids=[f"{i}" for i in range(len(APPEND))])
+@pytest.mark.parametrize("loud", [0.02, 1.0, 300.0])
+def test_append(case, fmt, loud):
+    """New rows smaller than the page's scale holds, about as large, and far larger."""
+    B, H, d, bs, lens, W = case
+    print(f"[case] append {case} {u.NAMES[fmt]} x{loud}", flush=True)
+    c = u.random_cache(8, B, H, d, bs, lens, fmt)
+    c.ks = np.where(np.isnan(c.ks), 1.0, c.ks).astype(np.float32)
+    c.vs = np.where(np.isnan(c.vs), 1.0, c.vs).astype(np.float32)
+    f = lambda s: u.synth.f32_to_bf16_bits((u.synth.bf16_bits_to_f32(u.random_rows(s, B * H, W, d)) * loud).astype(np.float32))
+    k, v = f(9), f(10)
+    g = u.to_gpu(c)
+    kvc.q8_append(g, u.dev_bf16(k), u.dev_bf16(v))
+    oq.append(c, k, v)
+    torch.cuda.synchronize()
+    u.same_cache(g, c)
+    kvc.q8_append(g, u.dev_bf16(k), u.dev_bf16(v))      # again: nothing changes
+    torch.cuda.synchronize()
+    u.same_cache(g, c)
+
+
+ATTEND = [
+    # B, H, G, W, d, bs, lengths, holes
+    (1, 1, 1, 1, 64, 16, [1], 0.0),
+    (4, 2, 4, 1, 128, 16, [0, 1, 33, 300], 0.0),
+    (3, 1, 7, 1, 128, 24, [31, 32, 257], 0.0),
+    (2, 2, 16, 1, 64, 1, [100, 64], 0.0),
+    (2, 1, 17, 1, 128, 64, [255, 513], 0.0),
+    (3, 2, 4, 5, 64, 24, [0, 3, 700], 0.3),
+    (2, 1, 9, 9, 128, 100, [90, 411], 0.0),
+    (1, 1, 64, 1, 128, 16, [1000], 0.0),
+    (2, 1, 1, 40, 64, 32, [39, 600], 0.5),
+    (1, 2, 4, 1, 128, 4096, [5000], 0.0),
+    (3, 1, 2, 2, 128, 16, [50, 60, 70], 1.0),
+    (1, 1, 3, 1, 128, 128, [16500], 0.0),
+    (1, 1, 2, 1, 64, 48, [140001], 0.02),
+]
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("case", ATTEND, ids=[f"{i}" for i in range(len(ATTEND))])
+def test_attend(case, fmt):
+    B, H, G, W, d, bs, lens, holes = case
+    print(f"[case] attend {case} {u.NAMES[fmt]}", flush=True)
+    c = u.random_cache(11, B, H, d, bs, lens, fmt, holes=holes)
+    q = u.random_rows(12, B * H, G, W, d)
+    g = u.to_gpu(c)
+    out, lse = kvc.q8_attend(g, u.dev_bf16(q), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("spread", [6.0, 14.0])
+def test_attend_scales_far_apart(fmt, spread):
+    """Page scales over many powers of two, zero scales, large scores."""
+    B, H, G, W, d, bs = 2, 2, 5, 1, 128, 8
+    c = u.random_cache(13, B, H, d, bs, [400, 77], fmt, scale_spread=spread, poison=False)
+    c.ks = np.minimum(c.ks, np.float32(0.05))
+    c.vs[u.rng_of(14).random(c.vs.shape) < 0.2] = 0.0
+    q = u.random_rows(15, B * H, G, W, d)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True, scale=0.25)
+    torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse, scale=0.25)
+
+
+def test_attend_query_range():
+    """Queries from the smallest to large magnitudes, and a zero row."""
+    B, H, G, W, d, bs = 1, 1, 6, 1, 128, 16
+    c = u.random_cache(16, B, H, d, bs, [200], oq.E4M3)
+    q = u.random_rows(17, 1, G, W, d)
+    f = u.synth.bf16_bits_to_f32(q)
+    for i, s in enumerate([0.0, 2.0 ** -130, 2.0 ** -40, 1.0, 2.0 ** 6, 2.0 ** -3]):
+        f[0, i] *= np.float32(s)
+    f[0, 3, 0, ::7] *= np.float32(2.0 ** -30)       # far below the row's largest
+    q = u.synth.f32_to_bf16_bits(f)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse)
+
+
+def test_max_len_bounds_the_length():
+    c = u.random_cache(18, 2, 2, 64, 16, [300, 40], oq.INT8, poison=False)
+    g = u.to_gpu(c, max_len=100)
+    c2 = oq.Cache(c.k, c.v, c.ks, c.vs, c.table, c.lens, c.fmt, max_len=100)
+    q = u.random_rows(19, 4, 3, 1, 64)
+    out, lse = kvc.q8_attend(g, u.dev_bf16(q), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c2, q, out, lse)
+    gk, _ = kvc.q8_load(g, 120)
+    np.testing.assert_array_equal(gk.view(torch.int16).cpu().numpy().view(np.uint16), oq.load(c2, 120)[0])
+
+
+def test_a_head_alone_gives_the_bits_it_has_in_a_batch():
+    lens = [700, 33, 20000, 512]
+    c = u.random_cache(20, 4, 2, 128, 16, lens, oq.E4M3)
+    g = u.to_gpu(c)
+    q = u.dev_bf16(u.random_rows(21, 8, 4, 2, 128))
+    out, lse = kvc.q8_attend(g, q, want_lse=True)
+    for b in range(4):
+        tb = -(-lens[b] // 16)
+        alone = kvc.Q8Cache(g.k_pool, g.v_pool, g.k_scale, g.v_scale,
+                            g.table[b:b + 1, :tb].contiguous(), g.seq_len[b:b + 1].contiguous())
+        o, l = kvc.q8_attend(alone, q[2 * b:2 * b + 2].contiguous(), want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[2 * b:2 * b + 2].view(torch.int16))
+        assert torch.equal(l, lse[2 * b:2 * b + 2])
+
+
+def test_untouched_rows_and_pages():
+    """Rows past the length, pages of nobody and k/v rows >= T of a load stay."""
+    c = u.random_cache(22, 2, 2, 64, 16, [20, 5], oq.INT8)
+    g = u.to_gpu(c)
+    out_k = torch.full((4, 30, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out_v = out_k.clone()
+    kvc.q8_load(g, 24, k_out=out_k, v_out=out_v)
+    assert bool((out_k[:, 24:] == 7.0).all()) and bool((out_v[:, 24:] == 7.0).all())
+    u.same_cache(g, c)
+    only_k, none = kvc.q8_load(g, 24, want_v=False)
+    assert none is None and torch.equal(only_k.view(torch.int16), out_k[:, :24].contiguous().view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """A pool of more than 2^32 bytes: the last pages hold the sequence."""
+    H, bs, d = 8, 64, 128
+    n = (1 << 32) // (H * bs * d) + 40                         # 4.3 GB of codes
+    k = torch.zeros((n, H, bs, d), dtype=torch.int8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.ones((n, H), device="cuda")
+    vs = torch.ones((n, H), device="cuda")
+    table = torch.tensor([[n - 1, n - 7, n - 3]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([150], dtype=torch.int32, device="cuda")
+    rows_k, rows_v = u.random_rows(23, H, 150, d), u.random_rows(24, H, 150, d)
+    g = kvc.Q8Cache(k, v, ks, vs, table, lens)
+    kvc.q8_store(g, u.dev_bf16(rows_k), u.dev_bf16(rows_v))
+    ids = [n - 1, n - 7, n - 3]
+    small = oq.Cache(np.zeros((3, H, bs, d), np.uint8), np.zeros((3, H, bs, d), np.uint8),
+                     np.ones((3, H), np.float32), np.ones((3, H), np.float32), [[0, 1, 2]], [150], oq.INT8)
+    oq.store(small, rows_k, rows_v, 150)
+    np.testing.assert_array_equal(bits8_of(g.k_pool, ids), small.k)
+    np.testing.assert_array_equal(bits8_of(g.v_pool, ids), small.v)
+    q = u.random_rows(25, H, 4, 1, d)
+    out, lse = kvc.q8_attend(g, u.dev_bf16(q), want_lse=True)
+    u.check_attention(small, q, out, lse)
+    new = u.random_rows(26, H, 1, d)
+    lens += 1
+    kvc.q8_append(g, u.dev_bf16(new), u.dev_bf16(new))
+    small.lens = np.array([151])
+    oq.append(small, new, new)
+    np.testing.assert_array_equal(bits8_of(g.k_pool, ids), small.k)
+    got, _ = kvc.q8_load(g, 151)
+    np.testing.assert_array_equal(got.view(torch.int16).cpu().numpy().view(np.uint16), oq.load(small, 151)[0])
+
+
+def bits8_of(pool, ids):
+    return u.bits8(pool[torch.tensor(ids, device="cuda")].contiguous())
