@@ -38,7 +38,7 @@ SOURCES = {
     "kvc_noalloc.hip": [],
     "kvc_cache_host.cpp": [],
     "kvc_q8.hip": ["-ffp-contract=off"],       # scales and codes: one rounding at a time
-    "kvc_q8_attend.hip": [],
+    "kvc_q8_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "kvc_pages.hip": [],
 }
 EXPORTS = ["kvc_score_window", "kvc_mass_segment", "kvc_select", "kvc_gather_compact",

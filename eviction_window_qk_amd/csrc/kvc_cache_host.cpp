@@ -99,10 +99,10 @@ void q8_ranges(const kvc_q8_cache* c, Range* r) {
 bool too_many(uint64_t units) { return units > 0xffffff00ull; }
 
 size_t attend_ws(const Q8& d, int rows) {
-  const int pieces = q8_max_pieces(d.cap);
+  const int pieces = q8_max_pieces(d.cap, rows);
   if (pieces == 1) return 0;
   const size_t n = size_t(d.B) * d.H * rows * pieces;
-  return (n * (d.D + 4) * 4 + 255) & ~size_t(255);
+  return (n * (d.D + 2) * 4 + 255) & ~size_t(255);
 }
 
 int attend_shape(const kvc_q8_cache* c, int32_t group, int32_t window, Q8* d) {

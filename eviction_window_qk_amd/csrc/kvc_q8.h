@@ -23,6 +23,12 @@ __host__ __device__ __forceinline__ uint32_t quot(FastDiv f, uint32_t x) {
   return uint32_t(((uint64_t(x) * f.m) >> 32) + x) >> f.s;
 }
 
+// The same for any 32-bit x.
+__device__ __forceinline__ uint32_t quot32(FastDiv f, uint32_t x) {
+  const uint32_t hi = __umulhi(x, f.m);
+  return f.s == 0 ? x : (((x - hi) >> 1) + hi) >> (f.s - 1);
+}
+
 // A cache after validation.
 struct Q8 {
   int B, H, D, bs, tb, cap, fmt;
@@ -47,17 +53,23 @@ __device__ __forceinline__ int q8_page(const Q8& c, int b, int j) {
   return uint32_t(p) < c.n_blocks ? p : -1;
 }
 
-// Keys per workgroup of the attention: 256 up to 64 pieces of a sequence, then
-// twice as many until 2048.  It depends on the sequence's own length only, so
-// a head's sums are taken in the same order whatever else is in the launch.
-__host__ __device__ inline int q8_chunk(int len) {
-  int c = 256;
+// Keys per workgroup of the attention, for a sequence of len keys and R query
+// rows: pieces of at most 512 (1024 for more than 16 rows, whose partial sums
+// weigh twice as much), at most 1024 and 2048 past 64 such pieces; equal
+// pieces, in multiples of the workgroup's 128-key stride.  256 heads of 1100
+// keys took 24 us so, 29 with 256 or 1024.  It depends on the sequence's own
+// length and rows only, so a head's sums are taken in the same order whatever
+// else is in the launch.
+__host__ __device__ inline int q8_chunk(int len, int rows) {
+  int c = rows <= 16 ? 512 : 1024;
   while (c < 2048 && len > 64 * c) c *= 2;
-  return c;
+  const int pieces = (len + c - 1) / c;
+  return pieces > 1 ? ((len + pieces - 1) / pieces + 127) & ~127 : c;
 }
 // The most pieces that any length up to cap is cut into.
-inline int q8_max_pieces(int cap) {
-  if (cap <= 64 * 256) return cap > 0 ? (cap + 255) / 256 : 1;
+inline int q8_max_pieces(int cap, int rows) {
+  const int base = q8_chunk(1, rows);
+  if (cap <= 64 * base) return cap > 0 ? (cap + base - 1) / base : 1;
   const int n = (cap + 2047) / 2048;
   return n > 64 ? n : 64;
 }

@@ -2,16 +2,18 @@
 //
 // For every (sequence, KV head) the G query heads' W queries form the R = G*W
 // rows of two products against the same keys and values:
-//   s = c * ks * <q, code_k>, p = 2^(s - m), l = sum p, out = sum p * vs * code_v / l
-// with c = scale * log2(e), ks and vs the page scales, m a running maximum.
-// Each cached byte is read once for all R rows; with the few rows of a decode
-// step the bound is HBM: 2*d bytes per key.
+//   x = c * ks * <q, code_k> + log2 vs,  w = 2^(x - m),
+//   l = sum w / vs,  out = sum w * code_v / l
+// with c = scale * log2(e), ks and vs the page scales, m a running maximum of
+// x.  Each cached byte is read once for all R rows; with the few rows of a
+// decode step the bound is HBM: 2*d bytes per key.
 //
 // Both products run on fp16 matrix instructions, 16x16x32: e4m3 and int8 codes
 // are exact in fp16, so is a bf16 query scaled by a power of two (elements
 // below 2^-29 of the row's largest lose bits), and the weights keep 11 bits.
-// A weight carries its page's value scale, w = 2^(s + log2 vs - m2) with a
-// maximum m2 of its own, so that it stays in (0, 1] whatever the scales are.
+// A weight carries its page's value scale inside the exponent, so one exp2 a
+// score gives a number in (0, 1] whatever the scales are; the denominator
+// takes the scale out again, in fp32.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P': the lane that
 // holds eight scores of a query row (keys 4g..4g+3 of two 16-key tiles, g its
@@ -24,6 +26,8 @@
 // four waves of a workgroup take the 32-key tiles of a piece in turn, and
 // their sums meet in LDS.  A second kernel joins the pieces where there are
 // several.
+#include <type_traits>
+
 #include "kvc_q8.h"
 
 namespace kvc {
@@ -35,7 +39,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kThreads = 256;
+constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr int kMaxChunk = 2048;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
@@ -47,8 +51,8 @@ struct Args {
   const uint16_t* q;
   uint16_t* out;
   float* lse;
-  float* part;  // [n][row][piece][D] sums, then [n][row][piece][4] (m, l, m2, -)
-  float* stat;
+  float* part;  // [n][row][piece][D] sums
+  float* stat;  // [n][row][piece][2] m, l
 };
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -90,27 +94,45 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
 
-// One output value from its sums: the weights were relative to 2^m2 and carried
-// the value scales, l is relative to 2^m.
+// Maximum over the workgroup, in every thread.
+__device__ __forceinline__ float block_max(float x, float* sh) {
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) x = fmaxf(x, __shfl_xor(x, off));
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
+  __syncthreads();
+  x = sh[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) x = fmaxf(x, sh[w]);
+  return x;
+}
+
+// One output value from its sums, relative to 2^m.
 __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, float sum,
-                                       float l, float m, float m2) {
-  A.out[row * D + dim] = to_bf16(l == 0.0f ? 0.0f : sum * (fast_exp2(m2 - m) / l));
+                                       float l, float m) {
+  A.out[row * D + dim] = to_bf16(l == 0.0f ? 0.0f : sum / l);
   if (A.lse && dim == 0)
     A.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
+// Three waves a SIMD: a tile of each in flight covers the latency of HBM, and
+// nothing is gained by a second tile in registers at two waves (29 against
+// 24 us on 256 heads of 1100 keys).  32 rows at D = 128 need the registers of two.
 template <int D, int FMT, int MT>
-__global__ __launch_bounds__(kThreads) void k_q8_attend(Args A) {
+__global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_attend(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
   constexpr int kVWords = D / 64;       // words of one key's values in a lane
-  constexpr int kRowF = D + 4;          // floats of one merged row: sums, m, l, m2
-  constexpr int kKeysLds = kMaxChunk * 3;
-  constexpr int kMergeLds = 4 * 16 * kRowF;
+  constexpr int kRowF = D + 4;          // floats of one merged row: sums, m, l
+  constexpr int kKeysLds = kMaxChunk * 4;
+  constexpr int kMergeLds = kWaves * 16 * kRowF;
   __shared__ __align__(16) float lds[kKeysLds > kMergeLds ? kKeysLds : kMergeLds];
   uint32_t* const row_of = reinterpret_cast<uint32_t*>(lds);  // pool row of each key
   float* const ks_of = lds + kMaxChunk;                       // its key scale
   float* const lv_of = lds + 2 * kMaxChunk;                   // log2 of its value scale
+  float* const iv_of = lds + 3 * kMaxChunk;                   // 1 / its value scale
+
+  __shared__ float top_of[kWaves];
+  __shared__ uint32_t none_of[kMaxChunk / 32];                // which keys of a tile are none
 
   const Q8& c = A.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -118,58 +140,120 @@ __global__ __launch_bounds__(kThreads) void k_q8_attend(Args A) {
   const int piece = int(blockIdx.x % unsigned(A.pieces));
   const int n = A.n0 + int(blockIdx.x / unsigned(A.pieces)), rb = blockIdx.y;
   const int b = n / c.H, h = n % c.H;
+
+  // Queries, on their way while the keys are looked up.
+  u32x4 raw[MT][kSteps];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = (rb * MT + mt) * 16 + col;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      raw[mt][s] = u32x4{0, 0, 0, 0};
+      if (r < A.R) {
+        const int dim = (s >> 1) * 64 + g * 16 + (s & 1) * 8;
+        raw[mt][s] = *reinterpret_cast<const u32x4*>(A.q + (size_t(n) * A.R + r) * D + dim);
+      }
+    }
+  }
   const int len = q8_len(c, b);
-  const int chunk = q8_chunk(len);
+  const int chunk = q8_chunk(len, A.R);
   const int t0 = piece * chunk;
   if (t0 >= len && piece > 0) return;
   const int keys = len - t0 < chunk ? len - t0 : chunk;  // of this piece, 0 for an empty sequence
   const bool alone = len <= chunk;
 
-  // Where the keys of this piece are.
+  // Where the keys of this piece are; a key that is none (in no page, or past
+  // the end) points to row 0, whose bytes are dropped later.  The scales follow
+  // after a first barrier, when the first tile's loads are on their way.
   const int padded = (keys + 31) & ~31;
-  for (int i = tid; i < padded; i += kThreads) {
+  for (int i = tid; i < (padded + 63 & ~63); i += kThreads) {
     uint32_t row = kNone;
-    float ks = 0.0f, lv = -INFINITY;
     if (i < keys) {
       const uint32_t t = uint32_t(t0 + i), j = quot(c.div, t);
       const int page = q8_page(c, b, int(j));
-      if (page >= 0) {
-        const uint32_t ph = uint32_t(page) * uint32_t(c.H) + uint32_t(h);
-        row = ph * c.div.d + (t - j * c.div.d);
-        ks = c.ks[ph];
-        lv = __builtin_amdgcn_logf(c.vs[ph]);
+      if (page >= 0)
+        row = (uint32_t(page) * uint32_t(c.H) + uint32_t(h)) * c.div.d + (t - j * c.div.d);
+    }
+    const uint64_t none = __ballot(row == kNone);
+    if (i < padded) {
+      row_of[i] = row == kNone ? 0 : row;
+      lv_of[i] = row == kNone ? -INFINITY : 0.0f;
+      if ((lane & 31) == 0) none_of[i >> 5] = uint32_t(lane ? none >> 32 : none);
+    }
+  }
+  __syncthreads();
+
+  // One tile of 32 keys as it is loaded.  K: this lane's keys are col of either
+  // half, its bytes g*16..; V: keys 4g..4g+3 of both halves, D/16 bytes of each.
+  struct Tile {
+    u32x4 k[2][kSteps / 2];
+    uint32_t v[8][kVWords];
+  };
+  auto fetch = [&](int tile, Tile& x) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint8_t* at = c.k + size_t(row_of[tile + half * 16 + col]) * D + g * 16;
+#pragma unroll
+      for (int s = 0; s < kSteps / 2; ++s)
+        x.k[half][s] = *reinterpret_cast<const u32x4*>(at + s * 64);
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const u32x4 rows = *reinterpret_cast<const u32x4*>(row_of + tile + half * 16 + 4 * g);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint8_t* at = c.v + size_t(rows[i]) * D + col * (D / 16);
+        if constexpr (kVWords == 2) {
+          const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+          x.v[half * 4 + i][0] = y.x, x.v[half * 4 + i][1] = y.y;
+        } else {
+          x.v[half * 4 + i][0] = *reinterpret_cast<const uint32_t*>(at);
+        }
       }
     }
-    row_of[i] = row;
+  };
+  Tile cur;
+  if (wave * 32 < keys) fetch(wave * 32, cur);
+
+  float vtop = 0.0f;
+  for (int i = tid; i < padded; i += kThreads) {
+    float ks = 0.0f, vs = 0.0f;
+    if (lv_of[i] == 0.0f) {
+      const uint32_t ph = quot32(c.div, row_of[i]);
+      ks = c.ks[ph];
+      vs = c.vs[ph];
+    }
     ks_of[i] = ks;
-    lv_of[i] = lv;
+    iv_of[i] = vs;
+    vtop = fmaxf(vtop, vs);
+  }
+  vtop = block_max(vtop, top_of);
+  // A value scale more than 2^40 below the piece's largest (an empty page's)
+  // counts as that far below it: the weights span fp32, not more.
+  for (int i = tid; i < padded; i += kThreads) {
+    const float vs = fmaxf(iv_of[i], fmaxf(vtop * 0x1p-40f, 0x1p-126f));
+    if (lv_of[i] == 0.0f) lv_of[i] = __builtin_amdgcn_logf(vs);
+    iv_of[i] = __builtin_amdgcn_rcpf(vs);
   }
 
-  // Queries: fp16 fragments of rows scaled by a power of two.
+  // Queries to fp16 fragments of rows scaled by a power of two.
   f16x8 qf[MT][kSteps];
   float qc[MT];
   int last[MT];  // last key this row attends to
-  float m[MT], m2[MT], l[MT];
+  float m[MT], l[MT];
   f32x4 acc[MT][kTiles];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = (rb * MT + mt) * 16 + col;
-    u32x4 raw[kSteps];
     uint32_t top = 0;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      raw[s] = u32x4{0, 0, 0, 0};
-      if (r < A.R) {
-        const int dim = (s >> 1) * 64 + g * 16 + (s & 1) * 8;
-        raw[s] = *reinterpret_cast<const u32x4*>(A.q + (size_t(n) * A.R + r) * D + dim);
-      }
+    for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = raw[s][i] & 0x7fffu, hi = (raw[s][i] >> 16) & 0x7fffu;
+        const uint32_t lo = raw[mt][s][i] & 0x7fffu, hi = (raw[mt][s][i] >> 16) & 0x7fffu;
         top = top > lo ? top : lo;
         top = top > hi ? top : hi;
       }
-    }
 #pragma unroll
     for (int off = 16; off <= 32; off <<= 1) {
       const uint32_t o = uint32_t(__shfl_xor(int(top), off));
@@ -183,114 +267,105 @@ __global__ __launch_bounds__(kThreads) void k_q8_attend(Args A) {
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        qf[mt][s][2 * i] = _Float16(__uint_as_float(raw[s][i] << 16) * mul);
-        qf[mt][s][2 * i + 1] = _Float16(__uint_as_float(raw[s][i] & 0xffff0000u) * mul);
+        qf[mt][s][2 * i] = _Float16(__uint_as_float(raw[mt][s][i] << 16) * mul);
+        qf[mt][s][2 * i + 1] = _Float16(__uint_as_float(raw[mt][s][i] & 0xffff0000u) * mul);
       }
-    last[mt] = r < A.R ? len - A.W + r % A.W - t0 : -1;
-    m[mt] = m2[mt] = -INFINITY;
+    last[mt] = r < A.R ? len - A.W + r % A.W - t0 : 0x7ffffffe;  // rows that are none: see all
+    m[mt] = -INFINITY;
     l[mt] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[mt][i] = f32x4{0, 0, 0, 0};
   }
+  const int low = len - A.W - t0;  // the first query's last key: all rows see the keys up to it
   __syncthreads();
 
-  for (int tile = wave * 32; tile < keys; tile += 128) {
-    // K fragments of two 16-key tiles, as they lie.
-    f16x8 kf[2][kSteps];
+  auto work = [&](int tile, const Tile& x, auto checked) {
+    const auto at4 = [&](const float* of, int half) {
+      return *reinterpret_cast<const f32x4*>(of + tile + half * 16 + 4 * g);
+    };
+    const f32x4 ks[2] = {at4(ks_of, 0), at4(ks_of, 1)};
+    const f32x4 lv[2] = {at4(lv_of, 0), at4(lv_of, 1)};
+    const f32x4 iv[2] = {at4(iv_of, 0), at4(iv_of, 1)};
+    float scores[MT][8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint32_t row = row_of[tile + half * 16 + col];
+      f16x8 kf[kSteps];
 #pragma unroll
       for (int s = 0; s < kSteps; s += 2) {
-        u32x4 x = {0, 0, 0, 0};
-        if (row != kNone)
-          x = *reinterpret_cast<const u32x4*>(c.k + size_t(row) * D + s * 32 + g * 16);
-        kf[half][s] = frag<FMT>(x.x, x.y);
-        kf[half][s + 1] = frag<FMT>(x.z, x.w);
+        kf[s] = frag<FMT>(x.k[half][s / 2].x, x.k[half][s / 2].y);
+        kf[s + 1] = frag<FMT>(x.k[half][s / 2].z, x.k[half][s / 2].w);
       }
-    }
-    // V: this lane's keys are 4g..4g+3 of both tiles, its values D/16 wide.
-    const u32x4 rows[2] = {*reinterpret_cast<const u32x4*>(row_of + tile + 4 * g),
-                           *reinterpret_cast<const u32x4*>(row_of + tile + 16 + 4 * g)};
-    uint32_t vw[8][kVWords];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t row = rows[i >> 2][i & 3];
-#pragma unroll
-      for (int w = 0; w < kVWords; ++w) vw[i][w] = 0;
-      if (row != kNone) {
-        const uint8_t* at = c.v + size_t(row) * D + col * (D / 16);
-        if constexpr (kVWords == 2) {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(at);
-          vw[i][0] = x.x, vw[i][1] = x.y;
-        } else {
-          vw[i][0] = *reinterpret_cast<const uint32_t*>(at);
-        }
-      }
-    }
-    f16x8 vf[kTiles];
-#pragma unroll
-    for (int w = 0; w < kVWords; ++w) {
-      uint32_t lo[4], hi[4];
-      turn4(vw[0][w], vw[1][w], vw[2][w], vw[3][w], lo);
-      turn4(vw[4][w], vw[5][w], vw[6][w], vw[7][w], hi);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) vf[w * 4 + i] = frag<FMT>(lo[i], hi[i]);
-    }
-    const f32x4 ks[2] = {*reinterpret_cast<const f32x4*>(ks_of + tile + 4 * g),
-                         *reinterpret_cast<const f32x4*>(ks_of + tile + 16 + 4 * g)};
-    const f32x4 lv[2] = {*reinterpret_cast<const f32x4*>(lv_of + tile + 4 * g),
-                         *reinterpret_cast<const f32x4*>(lv_of + tile + 16 + 4 * g)};
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float s[8], x[8];
-      float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
+      for (int mt = 0; mt < MT; ++mt) {
         f32x4 a = {0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
-          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[half][k], qf[mt][k], a, 0, 0, 0);
+          a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[k], qf[mt][k], a, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int j = half * 4 + i;
-          const bool seen = tile + half * 16 + 4 * g + i <= last[mt] && rows[half][i] != kNone;
-          s[j] = seen ? a[i] * (ks[half][i] * qc[mt]) : -INFINITY;
-          x[j] = s[j] + lv[half][i];
-          top = fmaxf(top, s[j]);
-          top2 = fmaxf(top2, x[j]);
+          float y = __builtin_fmaf(a[i] * ks[half][i], qc[mt], lv[half][i]);
+          if constexpr (checked.value) {
+            const int t = tile + half * 16 + 4 * g + i;
+            if (t > last[mt] || lv[half][i] == -INFINITY) y = -INFINITY;
+          }
+          scores[mt][half * 4 + i] = y;
         }
       }
+    }
+    f16x8 w[MT];
 #pragma unroll
-      for (int off = 16; off <= 32; off <<= 1) {
-        top = fmaxf(top, __shfl_xor(top, off));
-        top2 = fmaxf(top2, __shfl_xor(top2, off));
-      }
-      if (__any(top > m[mt] || top2 > m2[mt])) {
-        const float nm = fmaxf(m[mt], top), nm2 = fmaxf(m2[mt], top2);
-        const float f = nm == -INFINITY ? 1.0f : fast_exp2(m[mt] - nm);
-        const float f2 = nm2 == -INFINITY ? 1.0f : fast_exp2(m2[mt] - nm2);
+    for (int mt = 0; mt < MT; ++mt) {
+      const float(&y)[8] = scores[mt];
+      float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
+                        fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
+      if (__any(top > m[mt])) {
+#pragma unroll
+        for (int off = 16; off <= 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
+        const float now = fmaxf(m[mt], top);
+        const float f = now == -INFINITY ? 1.0f : fast_exp2(m[mt] - now);
         l[mt] *= f;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f2;
-        m[mt] = nm;
-        m2[mt] = nm2;
+        for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f;
+        m[mt] = now;
       }
       const float base = m[mt] == -INFINITY ? 0.0f : m[mt];
-      const float base2 = m2[mt] == -INFINITY ? 0.0f : m2[mt];
-      f16x8 w;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        l[mt] += fast_exp2(s[j] - base);
-        w[j] = _Float16(fast_exp2(x[j] - base2));
+        const float e = fast_exp2(y[j] - base);
+        l[mt] = __builtin_fmaf(e, iv[j >> 2][j & 3], l[mt]);
+        w[mt][j] = _Float16(e);
       }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-        acc[mt][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i], w, acc[mt][i], 0, 0, 0);
     }
+#pragma unroll
+    for (int u = 0; u < kVWords; ++u) {
+      uint32_t v[8], lo[4], hi[4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = x.v[j][u];
+        if (checked.value && lv[j >> 2][j & 3] == -INFINITY) v[j] = 0;
+      }
+      turn4(v[0], v[1], v[2], v[3], lo);
+      turn4(v[4], v[5], v[6], v[7], hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f16x8 vf = frag<FMT>(lo[i], hi[i]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          acc[mt][u * 4 + i] =
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, w[mt], acc[mt][u * 4 + i], 0, 0, 0);
+      }
+    }
+  };
+  auto step = [&](int tile, const Tile& x) {
+    if (tile + 31 <= low && none_of[tile >> 5] == 0) work(tile, x, std::false_type{});
+    else work(tile, x, std::true_type{});
+  };
+  for (int tile = wave * 32; tile < keys; tile += kWaves * 32) {
+    if (tile != wave * 32) fetch(tile, cur);
+    step(tile, cur);
   }
 
-  // The four waves' sums meet in LDS (over the key arrays), 16 rows at a time.
+  // The waves' sums meet in LDS (over the key arrays), 16 rows at a time.
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     __syncthreads();
@@ -304,61 +379,78 @@ __global__ __launch_bounds__(kThreads) void k_q8_attend(Args A) {
     if (g == 0) {
       to[D] = m[mt];
       to[D + 1] = l[mt];
-      to[D + 2] = m2[mt];
     }
     __syncthreads();
     const int r0 = (rb * MT + mt) * 16, rows_here = A.R - r0 < 16 ? A.R - r0 : 16;
     for (int e = tid; e < rows_here * D; e += kThreads) {
       const int r = e / D, dim = e % D;
       const float* at = lds + r * kRowF;
-      float M = -INFINITY, M2 = -INFINITY;
+      float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        M = fmaxf(M, at[w * 16 * kRowF + D]);
-        M2 = fmaxf(M2, at[w * 16 * kRowF + D + 2]);
-      }
-      const float base = M == -INFINITY ? 0.0f : M, base2 = M2 == -INFINITY ? 0.0f : M2;
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * 16 * kRowF + D]);
+      const float base = M == -INFINITY ? 0.0f : M;
       float sum = 0.0f, L = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kWaves; ++w) {
         const float* aw = at + w * 16 * kRowF;
-        sum += aw[dim] * fast_exp2(aw[D + 2] - base2);
-        L += aw[D + 1] * fast_exp2(aw[D] - base);
+        const float f = fast_exp2(aw[D] - base);
+        sum += aw[dim] * f;
+        L += aw[D + 1] * f;
       }
       const size_t row = size_t(n) * A.R + r0 + r;
       if (alone) {
-        finish(A, row, D, dim, sum, L, base, base2);
+        finish(A, row, D, dim, sum, L, base);
       } else {
         const size_t at_piece = row * A.pieces + piece;
         A.part[at_piece * D + dim] = sum;
         if (dim == 0) {
-          float* st = A.stat + at_piece * 4;
-          st[0] = M, st[1] = L, st[2] = M2;
+          A.stat[at_piece * 2] = M;
+          A.stat[at_piece * 2 + 1] = L;
         }
       }
     }
   }
 }
 
-// Joins the pieces of one row.
+// Joins the pieces of one row: D/4 lanes read one piece's sums, the workgroup
+// 1024/D pieces at a time.
 template <int D>
-__global__ __launch_bounds__(D) void k_q8_join(Args A, size_t row0) {
+__global__ __launch_bounds__(kThreads) void k_q8_join(Args A, size_t row0) {
+  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+  __shared__ float sums[kAtOnce][D + 4];
   const size_t row = row0 + blockIdx.x;
   const int b = int(row / A.R / unsigned(A.c.H));
-  const int len = q8_len(A.c, b), chunk = q8_chunk(len);
+  const int len = q8_len(A.c, b), chunk = q8_chunk(len, A.R);
   if (len <= chunk) return;
-  const int pieces = (len + chunk - 1) / chunk, dim = threadIdx.x;
-  const float* st = A.stat + row * A.pieces * 4;
+  const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
+  const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
+  const float* st = A.stat + row * A.pieces * 2;
   const float* part = A.part + row * A.pieces * D + dim;
-  float M = -INFINITY, M2 = -INFINITY;
-  for (int p = 0; p < pieces; ++p) M = fmaxf(M, st[p * 4]), M2 = fmaxf(M2, st[p * 4 + 2]);
-  const float base = M == -INFINITY ? 0.0f : M, base2 = M2 == -INFINITY ? 0.0f : M2;
-  float sum = 0.0f, L = 0.0f;
-  for (int p = 0; p < pieces; ++p) {
-    sum += part[size_t(p) * D] * fast_exp2(st[p * 4 + 2] - base2);
-    L += st[p * 4 + 1] * fast_exp2(st[p * 4] - base);
+  float M = -INFINITY;
+  for (int p = lane; p < pieces; p += 64) M = fmaxf(M, st[p * 2]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  const float base = M == -INFINITY ? 0.0f : M;
+  f32x4 sum = {0, 0, 0, 0};
+  float L = 0.0f;
+#pragma unroll 4
+  for (int p = group; p < pieces; p += kAtOnce) {
+    const f32x4 x = *reinterpret_cast<const f32x4*>(part + size_t(p) * D);
+    const float f = fast_exp2(st[p * 2] - base);
+    sum += x * f;
+    L = __builtin_fmaf(st[p * 2 + 1], f, L);
   }
-  finish(A, row, D, dim, sum, L, base, base2);
+  *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
+  if (dim == 0) sums[group][D] = L;
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float out = 0.0f, l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) {
+    out += sums[i][threadIdx.x];
+    l += sums[i][D];
+  }
+  finish(A, row, D, threadIdx.x, out, l, base);
 }
 
 template <int D, int FMT, int MT>
@@ -375,7 +467,7 @@ void attend(Args A, hipStream_t s) {
   if (A.pieces == 1) return;
   const size_t rows = size_t(heads) * A.R, step = size_t(1) << 23;
   for (size_t r0 = 0; r0 < rows; r0 += step)
-    k_q8_join<D><<<unsigned(rows - r0 < step ? rows - r0 : step), D, 0, s>>>(A, r0);
+    k_q8_join<D><<<unsigned(rows - r0 < step ? rows - r0 : step), kThreads, 0, s>>>(A, r0);
 }
 
 template <int D, int FMT>
@@ -392,7 +484,7 @@ hipError_t launch_q8_attend(const Q8& c, int G, int W, float c_log2, const void*
   A.c = c;
   A.W = W;
   A.R = G * W;
-  A.pieces = q8_max_pieces(c.cap);
+  A.pieces = q8_max_pieces(c.cap, A.R);
   A.n0 = 0;
   A.c_log2 = c_log2;
   A.q = static_cast<const uint16_t*>(q);

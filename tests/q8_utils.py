@@ -91,17 +91,23 @@ def check_attention(c: oq.Cache, q_bits, out, lse, scale=0.0):
           row's largest, at most 2^-39 of that each (inside the same bound)
       w   a weight in fp16: 2^-11 of itself, and 2^-25 of the largest weight
           (fp16 subnormals), which its value scale rides on
-      p   each weight and the sum over them: 2 ds, exp2 at 2^-22, fp32 sums of
-          T terms at T * 2^-24 (in the pieces' order, far fewer roundings)
+      x   the exponent s + log2 vs in fp32, and log2 itself: 2^-23 of |s| and of
+          the largest |log2 vs| (a weight's value scale is part of its exponent)
+      p   each weight and the sum over them: 2 (ds + x), exp2 at 2^-22, fp32 sums
+          of T terms at T * 2^-24 (in the pieces' order, far fewer roundings)
+      v   a value scale counts as 2^-40 of the largest at least: 2^-40 of the
+          largest value of any code
       out bf16, 2^-8 of itself
     """
     q = widen(q_bits)
     ref, ref_lse, absdot, absout, tail = oq.attend(c, q, scale)
     T = max([c.length(b) for b in range(c.B)] + [1])
-    ds = absdot * (c.d + 8) * 2.0 ** -23
+    used = np.isfinite(c.vs)
+    lv = np.abs(np.log2(np.maximum(c.vs[used], 2.0 ** -126))).max(initial=0.0)
+    ds = absdot * (c.d + 8) * 2.0 ** -23 + lv * 2.0 ** -23   # ds and x (|s| <= absdot)
     rel = 2.0 ** -11 + 2 * ds + 2.0 ** -20 + T * 2.0 ** -24
     bound = (rel[..., None] * absout + 2.0 ** -25 * tail[..., None]) * (1 + 2.0 ** -8)
-    bound += 2.0 ** -8 * np.abs(ref) + 1e-30
+    bound += 2.0 ** -8 * np.abs(ref) + 2.0 ** -40 * 448 * float(c.vs[used].max(initial=0.0)) + 1e-30
     got = out.float().cpu().numpy().astype(np.float64)
     err = np.abs(got - ref)
     bad = ~(err <= bound)
