@@ -5,8 +5,8 @@
 
 namespace kvc {
 
-constexpr int kPageTile = 4096;     // pages a workgroup counts and ranks
-constexpr int kMaxBuffers = 64;     // buffers per launch (by value in the arguments)
+constexpr int kPageTile = 16384;    // pages a workgroup counts and ranks
+constexpr int kMaxBuffers = 16;     // buffers per launch (by value in the arguments)
 constexpr int64_t kCopyChunk = 8192;  // bytes of a page one workgroup copies at a time
 
 struct Pages {

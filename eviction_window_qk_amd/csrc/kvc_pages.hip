@@ -3,12 +3,15 @@
 //
 // A page is free when its count is zero, and new pages are the lowest free
 // ones: there is no free list to keep in step, and the same calls give the
-// same tables.  Finding them takes two small launches: workgroups count the
-// free (or live) pages of their tiles, then rank them by the tile counts before
-// them and write them down in order.  A last launch applies the decisions,
-// table rows by some workgroups and page bytes by others.  Counts change by
-// integer atomics, whose order does not matter to the result.  The page copies
-// are bound by HBM, the rest by launch latency.
+// same tables.  A first launch decides: workgroups list the free pages of their
+// tile of the pool in order, others look at the requests; a second applies the
+// decisions, table rows by some workgroups and page bytes by others.  A tile's
+// rank needs the counts of the tiles before it, which each workgroup takes
+// itself from pools of up to 65536 pages; larger pools, and calls for more than
+// 4096 sequences, spend a launch on sums first (two launches of a call take
+// about 7 us, three 10).  Counts change by integer atomics, whose order does not
+// matter to the result.  The page copies are bound by HBM, the rest by launch
+// latency.
 #include "kvc_pages.h"
 
 namespace kvc {
@@ -16,48 +19,58 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 256;
-constexpr int kPerLane = kPageTile / kThreads;  // pages a lane looks at
-enum { kRefused = 0, kShared = 1, kCopied = 2 };  // what a fork pair does
+constexpr int kThreads = 256;    // of the launches that apply
+constexpr int kPlanThreads = 1024;  // of those that decide
+constexpr int kPlanWaves = kPlanThreads / 64;
+constexpr int kPerLane = kPageTile / kPlanThreads;  // pages a lane looks at
+enum { kRefused = 0, kShared = 1, kCopied = 2 };    // what a fork pair does
 
 __device__ __forceinline__ int below(uint64_t mask, int lane) {
   return __popcll(mask & ((uint64_t(1) << lane) - 1));
 }
 
-// Sum over the workgroup, in every thread.
-__device__ __forceinline__ int block_sum(int x, int* sh) {
+// Sum over the workgroup's WAVES waves, in every thread.
+template <int WAVES, class T>
+__device__ __forceinline__ T block_sum(T x, T* sh) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) x += __shfl_xor(x, off);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = x;
   __syncthreads();
-  return sh[0] + sh[1] + sh[2] + sh[3];
+  x = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) x += sh[w];
+  return x;
 }
 
 // Exclusive prefix sum over the workgroup's threads; *total in every thread.
-__device__ __forceinline__ int block_scan(int x, int* sh, int* total) {
+template <int WAVES, class T>
+__device__ __forceinline__ T block_scan(T x, T* sh, T* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int incl = x;
+  T incl = x;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int y = __shfl_up(incl, off);
+    const T y = __shfl_up(incl, off);
     if (lane >= off) incl += y;
   }
   __syncthreads();
   if (lane == 63) sh[wave] = incl;
   __syncthreads();
-  int base = 0;
+  T base = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) base += w < wave ? sh[w] : 0;
-  *total = sh[0] + sh[1] + sh[2] + sh[3];
+  for (int w = 0; w < WAVES; ++w) {
+    base += w < wave ? sh[w] : 0;
+    all += sh[w];
+  }
+  *total = all;
   return base + incl - x;
 }
 
-// One tile's pages in order: wave w has its w-th quarter, 64 pages a step.
-// Bit i of the result: the lane's page of step i has a count above zero.
+// One tile's pages in order: each wave has its share, 64 pages a step.  Bit i
+// of the result: the lane's page of step i has a count above zero.
 __device__ __forceinline__ uint32_t tile_live(const int32_t* refs, int n, int tile, int* first) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  *first = tile * kPageTile + wave * (kPageTile / 4) + lane;
+  *first = tile * kPageTile + wave * (kPageTile / kPlanWaves) + lane;
   int r[kPerLane];
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
@@ -70,42 +83,53 @@ __device__ __forceinline__ uint32_t tile_live(const int32_t* refs, int n, int ti
   return live;
 }
 
-__device__ __forceinline__ int tile_size(int n, int tile) {
-  const int left = n - tile * kPageTile;
-  return left < kPageTile ? left : kPageTile;
+// Live pages among refs[0..n), this thread's share.
+__device__ __forceinline__ int count_live(const int32_t* refs, int n) {
+  int sum = 0;
+  for (int base = 0; base < n; base += kPageTile) {
+    int r[kPerLane];
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+      const int id = base + i * kPlanThreads + int(threadIdx.x);
+      r[i] = id < n ? refs[id] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) sum += r[i] > 0 ? 1 : 0;
+  }
+  return sum;
 }
 
-// Live pages of each tile, by the first n_tiles workgroups of a launch.
-__device__ __forceinline__ void count_tile(const Pages& t, int tile, int32_t* count, int* sh) {
+// Live pages of each tile, one workgroup each; count is NULL where the tiles
+// are few enough to be counted by everybody.
+__global__ __launch_bounds__(kPlanThreads) void k_count(Pages t, int32_t* count) {
+  __shared__ int sh[kPlanWaves];
+  int first;
+  const uint32_t live = tile_live(t.refs, t.n, blockIdx.x, &first);
+  const int total = block_sum<kPlanWaves>(int(__popc(live)), sh);
+  if (threadIdx.x == 0) count[blockIdx.x] = total;
+}
+
+// Live pages below page `end`.
+__device__ __forceinline__ int live_below(const Pages& t, const int32_t* count, int end, int* sh) {
+  int x = 0;
+  if (count == nullptr) {
+    x = count_live(t.refs, end);
+  } else {
+    for (int i = threadIdx.x; i < end / kPageTile; i += kPlanThreads) x += count[i];
+    const int cut = end / kPageTile * kPageTile;
+    x += count_live(t.refs + cut, end - cut);
+  }
+  return block_sum<kPlanWaves>(x, sh);
+}
+
+// Writes the tile's free pages to list[rank]; the last tile also the number of
+// all to meta[0].
+__device__ __forceinline__ void list_free(const Pages& t, int tile, const int32_t* count,
+                                          int32_t* list, int32_t* meta, int* sh) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int first;
   const uint32_t live = tile_live(t.refs, t.n, tile, &first);
-  const int total = block_sum(__popc(live), sh);
-  if (threadIdx.x == 0) count[tile] = total;
-}
-
-// Live pages before this tile, and in all tiles.
-__device__ __forceinline__ int live_before(const int32_t* count, int n_tiles, int tile, int* sh,
-                                           int* all) {
-  int before = 0, sum = 0;
-  for (int i = threadIdx.x; i < n_tiles; i += kThreads) {
-    const int x = count[i];
-    sum += x;
-    before += i < tile ? x : 0;
-  }
-  before = block_sum(before, sh);
-  *all = block_sum(sum, sh);
-  return before;
-}
-
-// Writes the tile's free pages to list[rank]; the number of free pages to
-// meta[0].
-__device__ __forceinline__ void list_free(const Pages& t, int tile, int n_tiles,
-                                          const int32_t* count, int32_t* list, int32_t* meta,
-                                          int* sh) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int all, first;
-  const uint32_t live = tile_live(t.refs, t.n, tile, &first);
-  const int before = live_before(count, n_tiles, tile, sh, &all);
+  const int before = live_below(t, count, tile * kPageTile, sh);
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i)
@@ -113,8 +137,12 @@ __device__ __forceinline__ void list_free(const Pages& t, int tile, int n_tiles,
   __syncthreads();
   if (lane == 0) sh[wave] = mine;
   __syncthreads();
-  int rank = tile * kPageTile - before;
-  for (int w = 0; w < wave; ++w) rank += sh[w];
+  int rank = tile * kPageTile - before, all = rank;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    rank += w < wave ? sh[w] : 0;
+    all += sh[w];
+  }
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const bool free = first + i * 64 < t.n && !(live >> i & 1);
@@ -122,7 +150,7 @@ __device__ __forceinline__ void list_free(const Pages& t, int tile, int n_tiles,
     if (free) list[rank + below(m, lane)] = first + i * 64;
     rank += __popcll(m);
   }
-  if (tile == 0 && threadIdx.x == 0) meta[0] = t.n - all;
+  if ((tile + 1) * int64_t(kPageTile) >= t.n && threadIdx.x == 0) meta[0] = all;
 }
 
 __device__ __forceinline__ bool is_page(const Pages& t, int32_t p) {
@@ -137,53 +165,80 @@ __device__ __forceinline__ int wanted(const Pages& t, int32_t want) {
   return int((int64_t(want) + t.bs - 1) / t.bs);
 }
 
-__global__ __launch_bounds__(kThreads) void k_alloc_count(Pages t, int n_tiles, const int32_t* want,
-                                                          int32_t* count, int32_t* need) {
-  __shared__ int sh[4];
-  if (int(blockIdx.x) < n_tiles) return count_tile(t, blockIdx.x, count, sh);
-  const int b = int(blockIdx.x) - n_tiles;
-  const int entries = wanted(t, want[b]);
-  const int32_t* row = t.table + size_t(b) * t.tb;
+// Free pages of a tile each, and the entries that four sequences each miss.
+__global__ __launch_bounds__(kPlanThreads) void k_alloc_plan(Pages t, int n_tiles,
+                                                             const int32_t* want,
+                                                             const int32_t* count, int32_t* list,
+                                                             int32_t* meta, int32_t* need) {
+  __shared__ int sh[kPlanWaves];
+  if (int(blockIdx.x) < n_tiles) return list_free(t, blockIdx.x, count, list, meta, sh);
+  const int part = threadIdx.x / kThreads, at = threadIdx.x % kThreads;
+  const int b = (int(blockIdx.x) - n_tiles) * (kPlanThreads / kThreads) + part;
   int miss = 0;
-  for (int j = threadIdx.x; j < entries; j += kThreads) miss += is_page(t, row[j]) ? 0 : 1;
-  miss = block_sum(miss, sh);
-  if (threadIdx.x == 0) need[b] = miss;
+  if (b < t.B) {
+    const int entries = wanted(t, want[b]);
+    const int32_t* row = t.table + size_t(b) * t.tb;
+#pragma unroll 8
+    for (int j = at; j < entries; j += kThreads) miss += is_page(t, row[j]) ? 0 : 1;
+  }
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) miss += __shfl_xor(miss, off);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = miss;
+  __syncthreads();
+  if (at == 0 && b < t.B) {
+    miss = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 64; ++w) miss += sh[part * (kThreads / 64) + w];
+    need[b] = miss;
+  }
 }
 
-__global__ __launch_bounds__(kThreads) void k_alloc_list(Pages t, int n_tiles, const int32_t* count,
-                                                         int32_t* list, int32_t* meta,
-                                                         const int32_t* need, int32_t* offset) {
-  __shared__ int sh[4];
-  if (int(blockIdx.x) < n_tiles) return list_free(t, blockIdx.x, n_tiles, count, list, meta, sh);
-  // Requests before each sequence's; a sum past 2^31 - 1 stays there.
+// need[b] summed over the sequences before each; a sum past 2^31 - 1 stays
+// there.
+__global__ __launch_bounds__(kPlanThreads) void k_alloc_scan(Pages t, const int32_t* need,
+                                                             int32_t* offset) {
+  __shared__ int64_t sh[kPlanWaves];
   int64_t base = 0;
-  for (int b0 = 0; b0 < t.B; b0 += kThreads) {
+  for (int b0 = 0; b0 < t.B; b0 += kPlanThreads) {
     const int b = b0 + int(threadIdx.x);
-    int total;
-    const int off = block_scan(b < t.B ? need[b] : 0, sh, &total);
-    const int64_t at = base + off;
+    int64_t total;
+    const int64_t at = base + block_scan<kPlanWaves>(int64_t(b < t.B ? need[b] : 0), sh, &total);
     if (b < t.B) offset[b] = at < 0x7fffffff ? int32_t(at) : 0x7fffffff;
     base += total;
   }
 }
 
+// One sequence each; offset is NULL where every workgroup sums for itself.
 __global__ __launch_bounds__(kThreads) void k_alloc_apply(Pages t, const int32_t* want,
                                                           const int32_t* list, const int32_t* meta,
                                                           const int32_t* need, const int32_t* offset,
                                                           int32_t* status) {
-  __shared__ int sh[4];
+  __shared__ int sh[kThreads / 64];
+  __shared__ int64_t sums[kThreads / 64];
   const int b = blockIdx.x;
-  const int entries = wanted(t, want[b]), n = need[b], off = offset[b];
-  const bool fits = int64_t(off) + n <= meta[0];
-  if (threadIdx.x == 0) status[b] = entries < 0 ? 2 : (n == 0 || fits ? 0 : 1);
-  if (n == 0 || !fits) return;
+  const int entries = wanted(t, want[b]), n = need[b];
+  if (n == 0) {  // the same for the whole workgroup
+    if (threadIdx.x == 0) status[b] = entries < 0 ? 2 : 0;
+    return;
+  }
+  int64_t off = 0;
+  if (offset) {
+    off = offset[b];
+  } else {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < b; i += kThreads) off += need[i];
+    off = block_sum<kThreads / 64>(off, sums);
+  }
+  const bool fits = off + n <= meta[0];
+  if (threadIdx.x == 0) status[b] = fits ? 0 : 1;
+  if (!fits) return;
   int32_t* row = t.table + size_t(b) * t.tb;
-  int rank = off;
+  int rank = int(off);
   for (int j0 = 0; j0 < entries; j0 += kThreads) {
     const int j = j0 + int(threadIdx.x);
     const bool miss = j < entries && !is_page(t, row[j]);
     int total;
-    const int at = block_scan(miss ? 1 : 0, sh, &total);
+    const int at = block_scan<kThreads / 64>(miss ? 1 : 0, sh, &total);
     if (miss) {
       const int32_t p = list[rank + at];
       row[j] = p;
@@ -243,24 +298,25 @@ __device__ __forceinline__ int length_of(const Pages& t, int b) {
   return len < 0 ? 0 : (len < cap ? len : cap);
 }
 
-// Tile counts, and in the last workgroup what every pair does and which of the
-// new pages it takes.
-__global__ __launch_bounds__(kThreads) void k_fork_plan(Pages t, int n_tiles, int n_pairs,
-                                                        const int32_t* src, const int32_t* dst,
-                                                        int32_t* count, int32_t* mark,
-                                                        int32_t* kind, int32_t* rank,
-                                                        int32_t* from) {
-  __shared__ int sh[4];
-  if (int(blockIdx.x) < n_tiles) return count_tile(t, blockIdx.x, count, sh);
+// Free pages of a tile each, and in the last workgroup what every pair does and
+// which of the new pages it takes.
+__global__ __launch_bounds__(kPlanThreads) void k_fork_plan(Pages t, int n_tiles, int n_pairs,
+                                                            const int32_t* src, const int32_t* dst,
+                                                            const int32_t* count, int32_t* list,
+                                                            int32_t* meta, int32_t* mark,
+                                                            int32_t* kind, int32_t* rank,
+                                                            int32_t* from) {
+  __shared__ int sh[kPlanWaves];
+  if (int(blockIdx.x) < n_tiles) return list_free(t, blockIdx.x, count, list, meta, sh);
   // mark[b]: the first pair whose dst is b
-  for (int b = threadIdx.x; b < t.B; b += kThreads)
+  for (int b = threadIdx.x; b < t.B; b += kPlanThreads)
     __hip_atomic_store(&mark[b], 0x7fffffff, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
-  for (int i = threadIdx.x; i < n_pairs; i += kThreads)
+  for (int i = threadIdx.x; i < n_pairs; i += kPlanThreads)
     if (is_seq(t, dst[i])) atomicMin(&mark[dst[i]], i);
   __syncthreads();
   int base = 0;
-  for (int i0 = 0; i0 < n_pairs; i0 += kThreads) {
+  for (int i0 = 0; i0 < n_pairs; i0 += kPlanThreads) {
     const int i = i0 + int(threadIdx.x);
     int what = kRefused, page = -1;
     if (i < n_pairs) {
@@ -278,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan(Pages t, int n_tiles, in
       }
     }
     int total;
-    const int r = base + block_scan(what == kCopied ? 1 : 0, sh, &total);
+    const int r = base + block_scan<kPlanWaves>(what == kCopied ? 1 : 0, sh, &total);
     if (i < n_pairs) {
       kind[i] = what;
       rank[i] = r;
@@ -286,12 +342,6 @@ __global__ __launch_bounds__(kThreads) void k_fork_plan(Pages t, int n_tiles, in
     }
     base += total;
   }
-}
-
-__global__ __launch_bounds__(kThreads) void k_list(Pages t, int n_tiles, const int32_t* count,
-                                                   int32_t* list, int32_t* meta) {
-  __shared__ int sh[4];
-  list_free(t, blockIdx.x, n_tiles, count, list, meta, sh);
 }
 
 // The first n_rows workgroups write one pair's table row each, the others copy
@@ -358,30 +408,20 @@ __global__ __launch_bounds__(kThreads) void k_pages_free(Pages t, const int32_t*
 
 // --- compact -----------------------------------------------------------------
 
-__global__ __launch_bounds__(kThreads) void k_compact_count(Pages t, int32_t* count) {
-  __shared__ int sh[4];
-  count_tile(t, blockIdx.x, count, sh);
-}
-
 // Free pages below n_live ("holes") and live ones at or past it ("movers"), each
 // in ascending order: there are as many of one as of the other.  place[p]: p
 // itself, -1 where it is free, -2 - m for the m-th mover.
-__global__ __launch_bounds__(kThreads) void k_compact_list(Pages t, int n_tiles,
-                                                           const int32_t* count, int32_t* holes,
-                                                           int32_t* movers, int32_t* place,
-                                                           int32_t* meta, int32_t* n_live_out) {
-  __shared__ int sh[4];
+__global__ __launch_bounds__(kPlanThreads) void k_compact_plan(Pages t, const int32_t* count,
+                                                               int32_t* holes, int32_t* movers,
+                                                               int32_t* place, int32_t* meta,
+                                                               int32_t* n_live_out) {
+  __shared__ int sh[kPlanWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tile = blockIdx.x;
-  int n_live, first;
+  int first;
   const uint32_t live = tile_live(t.refs, t.n, tile, &first);
-  const int before = live_before(count, n_tiles, tile, sh, &n_live);
-  // live pages below n_live: whole tiles, then the start of the one it cuts
-  const int cut = n_live / kPageTile;
-  int part = 0;
-  for (int i = threadIdx.x; i < cut; i += kThreads) part += count[i];
-  for (int id = cut * kPageTile + int(threadIdx.x); id < n_live; id += kThreads)
-    part += t.refs[id] > 0 ? 1 : 0;
-  const int low = block_sum(part, sh);
+  const int before = live_below(t, count, tile * kPageTile, sh);
+  const int n_live = live_below(t, count, t.n, sh);
+  const int low = live_below(t, count, n_live, sh);  // live pages that stay
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) mine += __popcll(__ballot(live >> i & 1));
@@ -389,7 +429,8 @@ __global__ __launch_bounds__(kThreads) void k_compact_list(Pages t, int n_tiles,
   if (lane == 0) sh[wave] = mine;
   __syncthreads();
   int rank = before;  // live pages before this step
-  for (int w = 0; w < wave; ++w) rank += sh[w];
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) rank += w < wave ? sh[w] : 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) {
     const int id = first + i * 64;
@@ -453,7 +494,18 @@ __global__ __launch_bounds__(kThreads) void k_compact_apply(Pages t, int n_rows,
   }
 }
 
+constexpr int kOwnTiles = 4;      // tiles that every workgroup counts for itself
+constexpr int kOwnSeqs = 4096;    // sequences whose needs every workgroup sums
+
 int tiles_of(const Pages& t) { return (t.n + kPageTile - 1) / kPageTile; }
+
+// The tile counts of a pool of many tiles, or NULL.
+const int32_t* counts(const Pages& t, int32_t* count, hipStream_t s) {
+  const int tiles = tiles_of(t);
+  if (tiles <= kOwnTiles) return nullptr;
+  k_count<<<unsigned(tiles), kPlanThreads, 0, s>>>(t, count);
+  return count;
+}
 
 unsigned copy_blocks(uint64_t items) {
   return unsigned(items < 8192 ? items : 8192);
@@ -486,12 +538,17 @@ PagesWs pages_ws(const Pages& t, int n_pairs) {
 hipError_t launch_pages_alloc(const Pages& t, const int32_t* want, int32_t* status, int32_t* ws,
                               hipStream_t s) {
   const PagesWs w = pages_ws(t, 0);
-  const int tiles = tiles_of(t);
-  k_alloc_count<<<unsigned(tiles + t.B), kThreads, 0, s>>>(t, tiles, want, ws + w.count, ws + w.need);
-  k_alloc_list<<<unsigned(tiles + 1), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list,
-                                                        ws + w.meta, ws + w.need, ws + w.offset);
+  const int tiles = tiles_of(t), per = kPlanThreads / kThreads;
+  const int32_t* count = counts(t, ws + w.count, s);
+  k_alloc_plan<<<unsigned(tiles + (t.B + per - 1) / per), kPlanThreads, 0, s>>>(
+      t, tiles, want, count, ws + w.list, ws + w.meta, ws + w.need);
+  int32_t* offset = nullptr;
+  if (t.B > kOwnSeqs) {
+    offset = ws + w.offset;
+    k_alloc_scan<<<1, kPlanThreads, 0, s>>>(t, ws + w.need, offset);
+  }
   k_alloc_apply<<<unsigned(t.B), kThreads, 0, s>>>(t, want, ws + w.list, ws + w.meta, ws + w.need,
-                                                   ws + w.offset, status);
+                                                   offset, status);
   return hipGetLastError();
 }
 
@@ -500,10 +557,10 @@ hipError_t launch_pages_fork(const Pages& t, int n_pairs, const int32_t* src, co
                              hipStream_t s) {
   const PagesWs w = pages_ws(t, n_pairs);
   const int tiles = tiles_of(t);
-  k_fork_plan<<<unsigned(tiles + 1), kThreads, 0, s>>>(t, tiles, n_pairs, src, dst, ws + w.count,
-                                                       ws + w.need, ws + w.kind, ws + w.rank,
-                                                       ws + w.from);
-  k_list<<<unsigned(tiles), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list, ws + w.meta);
+  const int32_t* count = counts(t, ws + w.count, s);
+  k_fork_plan<<<unsigned(tiles + 1), kPlanThreads, 0, s>>>(
+      t, tiles, n_pairs, src, dst, count, ws + w.list, ws + w.meta, ws + w.need, ws + w.kind,
+      ws + w.rank, ws + w.from);
   for (int gr = 0; gr < n_groups; ++gr) {
     const int rows = gr == 0 ? n_pairs : 0;
     const unsigned blocks = unsigned(rows) + copy_blocks(uint64_t(n_pairs) * groups[gr].chunks);
@@ -534,11 +591,9 @@ hipError_t launch_pages_compact(const Pages& t, const Buffers* groups, int n_gro
                                 int32_t* table_out, int32_t* refs_out, int32_t* remap,
                                 int32_t* n_live, int32_t* ws, hipStream_t s) {
   const PagesWs w = pages_ws(t, 0);
-  const int tiles = tiles_of(t);
-  k_compact_count<<<unsigned(tiles), kThreads, 0, s>>>(t, ws + w.count);
-  k_compact_list<<<unsigned(tiles), kThreads, 0, s>>>(t, tiles, ws + w.count, ws + w.list,
-                                                      ws + w.movers, ws + w.place, ws + w.meta,
-                                                      n_live);
+  const int32_t* count = counts(t, ws + w.count, s);
+  k_compact_plan<<<unsigned(tiles_of(t)), kPlanThreads, 0, s>>>(
+      t, count, ws + w.list, ws + w.movers, ws + w.place, ws + w.meta, n_live);
   const size_t entries = size_t(t.B) * t.tb + size_t(t.n);
   for (int gr = 0; gr < n_groups; ++gr) {
     size_t rows = gr == 0 ? (entries + 4 * kThreads - 1) / (4 * kThreads) : 0;

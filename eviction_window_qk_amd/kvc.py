@@ -532,40 +532,52 @@ def full_sync(part_pos, k_part, v_part, k_full, v_full, t_from: int, stream=None
 _Q8_FORMAT = {torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8}
 
 
-class _On:
-    """Device and stream of a call on tensors of `device`: the given stream or
-    that device's current one.  Inside, the device is current and so is the
-    stream, so that what is allocated belongs to it."""
-
-    def __init__(self, device, stream):
-        self.raw = torch.cuda.current_stream(device) if stream is None else stream
-        if self.raw.device != device:
-            raise ValueError(f"stream on {self.raw.device}, tensors on {device}")
-        here = stream is None and torch.cuda.current_device() == device.index
-        self.ctx = None if here else torch.cuda.stream(self.raw)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        return self.raw.cuda_stream
-
-    def __exit__(self, *a):
-        if self.ctx is not None:
-            self.ctx.__exit__(*a)
+def _here(device, stream):
+    """Raw handle of the stream a call runs on, or None when the call has to be
+    made again under `_there`: a stream was given, or another device is current.
+    (torch.cuda.current_stream would build a Stream object: 3 us a call.)"""
+    if stream is None and torch._C._cuda_getDevice() == device.index:
+        return torch._C._cuda_getCurrentRawStream(device.index)
+    return None
 
 
-def _one_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: on {t.device}, the cache is on {device}")
+def _there(device, stream):
+    """Context in which the stream (or the device's current one) and its device are
+    current, so that what a call allocates belongs to them."""
+    if stream is None:
+        return torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream on {stream.device}, tensors on {device}")
+    return torch.cuda.stream(stream)
 
 
-def _opt_ws(ws, n, device):
+def _at(t, dtypes, shape, device, name):
+    """_ptr for a tensor that has to be on `device`."""
+    if t is None:
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape
+            and t.device == device and t.is_contiguous() and device.type == "cuda"):
+        return t.data_ptr()
+    p = _ptr(t, dtypes, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return p
+
+
+_I32, _F32 = (torch.int32,), (torch.float32,)
+
+
+def _scratch(ws, n, device):
+    """A call's workspace: the given one, or n new bytes of the current stream."""
     if ws is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        return torch.empty(n, dtype=torch.uint8, device=device) if n else None
     if ws.dtype != torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError("workspace: contiguous uint8 tensor on the cache's GPU expected")
+        raise ValueError(f"workspace: contiguous uint8 tensor on {device} expected")
     return ws
+
+
+def _span(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
 class Q8Cache:
@@ -583,26 +595,29 @@ class Q8Cache:
             raise ValueError("k_pool: 4 dimensions expected, table: 2")
         n, H, bs, d = k_pool.shape
         B, tb = table.shape
+        dev, code = k_pool.device, (k_pool.dtype,)
         c = _CQ8Cache(n_seqs=B, kv_heads=H, head_dim=d, block_size=bs, table_blocks=tb,
                       max_len=int(max_len), format=_Q8_FORMAT[k_pool.dtype], reserved=0, n_blocks=n)
-        c.k_pool = _ptr(k_pool, (k_pool.dtype,), (n, H, bs, d), "k_pool")
-        c.v_pool = _ptr(v_pool, (k_pool.dtype,), (n, H, bs, d), "v_pool")
-        c.k_scale = _ptr(k_scale, (torch.float32,), (n, H), "k_scale")
-        c.v_scale = _ptr(v_scale, (torch.float32,), (n, H), "v_scale")
-        c.table = _ptr(table, (torch.int32,), (B, tb), "table")
-        c.seq_len = _ptr(seq_len, (torch.int32,), (B,), "seq_len")
-        self.device = k_pool.device
-        _one_device(self.device, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale, table=table,
-                    seq_len=seq_len)
+        c.k_pool = _at(k_pool, code, (n, H, bs, d), dev, "k_pool")
+        c.v_pool = _at(v_pool, code, (n, H, bs, d), dev, "v_pool")
+        c.k_scale = _at(k_scale, _F32, (n, H), dev, "k_scale")
+        c.v_scale = _at(v_scale, _F32, (n, H), dev, "v_scale")
+        c.table = _at(table, _I32, (B, tb), dev, "table")
+        c.seq_len = _at(seq_len, _I32, (B,), dev, "seq_len")
+        self.device = dev
         self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
         self.table, self.seq_len = table, seq_len
         self.heads, self.head_dim = B * H, d
-        self._c, self._ref = c, ctypes.addressof(c)
+        self._c, self._ref, self._ws = c, ctypes.addressof(c), {}
 
     def attend_workspace_bytes(self, group: int, window: int = 1) -> int:
-        n = int(lib().kvc_q8_attend_workspace_bytes(self._ref, int(group), int(window)))
-        if n == ctypes.c_size_t(-1).value:
-            raise KvcError(-1, "kvc_q8_attend_workspace_bytes")
+        """Bytes q8_attend needs for `group` query heads and `window` queries."""
+        n = self._ws.get((group, window))
+        if n is None:
+            n = int(lib().kvc_q8_attend_workspace_bytes(self._ref, int(group), int(window)))
+            if n == ctypes.c_size_t(-1).value:
+                raise KvcError(-4 if group > 64 else -1, "kvc_q8_attend_workspace_bytes")
+            self._ws[(group, window)] = n
         return n
 
 
@@ -610,15 +625,18 @@ def q8_store(cache: Q8Cache, k, v, kept=None, T: int = 0, stream=None):
     """Writes rows of k, v (bf16 [heads, t_stride, d], T of them valid, 0 = all)
     into the cache's pages: the rows kept (int32 [heads, n_kept]), or the last
     seq_len.  Returns the cache."""
-    if k.dim() != 3:
-        raise ValueError("k: 3 dimensions expected")
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return q8_store(cache, k, v, kept, T)
+    if k.dim() != 3 or (kept is not None and kept.dim() != 2):
+        raise ValueError("k: 3 dimensions expected, kept: 2")
     shp = (cache.heads, k.shape[1], cache.head_dim)
     n_kept = 0 if kept is None else kept.shape[1]
-    _one_device(cache.device, k=k, v=v, kept=kept)
-    with _On(cache.device, stream) as s:
-        rc = lib().kvc_q8_store(cache._ref, int(T) or shp[1], shp[1],
-                                _ptr(kept, (torch.int32,), (cache.heads, n_kept), "kept"), n_kept,
-                                _ptr(k, _BF16_LIKE, shp, "k"), _ptr(v, _BF16_LIKE, shp, "v"), s)
+    rc = lib().kvc_q8_store(cache._ref, int(T) or shp[1], shp[1],
+                            _at(kept, _I32, (cache.heads, n_kept), dev, "kept"), n_kept,
+                            _at(k, _BF16_LIKE, shp, dev, "k"), _at(v, _BF16_LIKE, shp, dev, "v"), s)
     _check(rc, "kvc_q8_store")
     return cache
 
@@ -626,16 +644,21 @@ def q8_store(cache: Q8Cache, k, v, kept=None, T: int = 0, stream=None):
 def q8_load(cache: Q8Cache, T: int, k_out=None, v_out=None, want_v: bool = True, stream=None):
     """The last T positions as bf16 rows, left-padded with zeros: returns (k, v),
     [heads, t_stride >= T, d] (want_v false and v_out None: (k, None))."""
-    _one_device(cache.device, k_out=k_out, v_out=v_out)
-    with _On(cache.device, stream) as s:
-        if k_out is None:
-            k_out = torch.empty((cache.heads, T, cache.head_dim), dtype=torch.bfloat16,
-                                device=cache.device)
-        if v_out is None and want_v:
-            v_out = torch.empty_like(k_out)
-        shp = (cache.heads, k_out.shape[1], cache.head_dim)
-        rc = lib().kvc_q8_load(cache._ref, int(T), shp[1], _ptr(k_out, _BF16_LIKE, shp, "k_out"),
-                               _ptr(v_out, _BF16_LIKE, shp, "v_out"), s)
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return q8_load(cache, T, k_out, v_out, want_v)
+    if k_out is None:
+        rows = T if v_out is None else v_out.shape[1]
+        k_out = torch.empty((cache.heads, rows, cache.head_dim), dtype=torch.bfloat16, device=dev)
+    if k_out.dim() != 3:
+        raise ValueError("k_out: 3 dimensions expected")
+    if v_out is None and want_v:
+        v_out = torch.empty_like(k_out)
+    shp = (cache.heads, k_out.shape[1], cache.head_dim)
+    rc = lib().kvc_q8_load(cache._ref, int(T), shp[1], _at(k_out, _BF16_LIKE, shp, dev, "k_out"),
+                           _at(v_out, _BF16_LIKE, shp, dev, "v_out"), s)
     _check(rc, "kvc_q8_load")
     return k_out, v_out
 
@@ -644,13 +667,16 @@ def q8_append(cache: Q8Cache, k_new, v_new, stream=None):
     """Appends k_new, v_new (bf16 [heads, window, d]) as the last `window`
     positions of every sequence (seq_len counts them already).  Returns the
     cache."""
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return q8_append(cache, k_new, v_new)
     if k_new.dim() != 3:
         raise ValueError("k_new: 3 dimensions expected")
     shp = (cache.heads, k_new.shape[1], cache.head_dim)
-    _one_device(cache.device, k_new=k_new, v_new=v_new)
-    with _On(cache.device, stream) as s:
-        rc = lib().kvc_q8_append(cache._ref, shp[1], _ptr(k_new, _BF16_LIKE, shp, "k_new"),
-                                 _ptr(v_new, _BF16_LIKE, shp, "v_new"), s)
+    rc = lib().kvc_q8_append(cache._ref, shp[1], _at(k_new, _BF16_LIKE, shp, dev, "k_new"),
+                             _at(v_new, _BF16_LIKE, shp, dev, "v_new"), s)
     _check(rc, "kvc_q8_append")
     return cache
 
@@ -660,22 +686,24 @@ def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, sca
     """Attention of the last `window` positions' queries q (bf16 [heads, group,
     window, d]) over the cache.  Returns out (bf16, like q), or (out, lse) with
     want_lse or an lse tensor (fp32 [heads, group, window])."""
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return q8_attend(cache, q, out, lse, want_lse, scale, ws)
     if q.dim() != 4:
         raise ValueError("q: 4 dimensions expected")
-    _, G, W, _ = q.shape
+    G, W = q.shape[1], q.shape[2]
     shp = (cache.heads, G, W, cache.head_dim)
-    _one_device(cache.device, q=q, out=out, lse=lse)
-    with _On(cache.device, stream) as s:
-        if out is None:
-            out = torch.empty(shp, dtype=q.dtype, device=cache.device)
-        if lse is None and want_lse:
-            lse = torch.empty(shp[:3], dtype=torch.float32, device=cache.device)
-        need = cache.attend_workspace_bytes(G, W)
-        ws = _opt_ws(ws, need, cache.device)
-        rc = lib().kvc_q8_attend(cache._ref, G, W, float(scale), _ptr(q, _BF16_LIKE, shp, "q"),
-                                 _ptr(out, _BF16_LIKE, shp, "out"),
-                                 _ptr(lse, (torch.float32,), shp[:3], "lse"), ws.data_ptr(),
-                                 ws.numel(), s)
+    q_ptr = _at(q, _BF16_LIKE, shp, dev, "q")
+    ws = _scratch(ws, cache.attend_workspace_bytes(G, W), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and want_lse:
+        lse = torch.empty(shp[:3], dtype=torch.float32, device=dev)
+    rc = lib().kvc_q8_attend(cache._ref, G, W, float(scale), q_ptr,
+                             _at(out, _BF16_LIKE, shp, dev, "out"),
+                             _at(lse, _F32, shp[:3], dev, "lse"), *_span(ws), s)
     _check(rc, "kvc_q8_attend")
     return out if lse is None else (out, lse)
 
@@ -689,21 +717,25 @@ class PageTable:
         if table.dim() != 2 or refs.dim() != 1:
             raise ValueError("table: 2 dimensions expected, refs: 1")
         B, tb = table.shape
+        dev = table.device
         c = _CPageTable(n_seqs=B, table_blocks=tb, block_size=int(block_size),
                         n_blocks=refs.shape[0])
-        c.table = _ptr(table, (torch.int32,), (B, tb), "table")
-        c.seq_len = _ptr(seq_len, (torch.int32,), (B,), "seq_len")
-        c.refs = _ptr(refs, (torch.int32,), (refs.shape[0],), "refs")
-        self.device = table.device
-        _one_device(self.device, seq_len=seq_len, refs=refs)
+        c.table = _at(table, _I32, (B, tb), dev, "table")
+        c.seq_len = _at(seq_len, _I32, (B,), dev, "seq_len")
+        c.refs = _at(refs, _I32, (refs.shape[0],), dev, "refs")
+        self.device = dev
         self.table, self.seq_len, self.refs = table, seq_len, refs
         self.block_size, self.n_blocks = int(block_size), refs.shape[0]
-        self._c, self._ref = c, ctypes.addressof(c)
+        self._c, self._ref, self._ws = c, ctypes.addressof(c), {}
 
     def workspace_bytes(self, n_pairs: int = 0) -> int:
-        n = int(lib().kvc_pages_workspace_bytes(self._ref, int(n_pairs)))
-        if n == 0:
-            raise KvcError(-1, "kvc_pages_workspace_bytes")
+        """Bytes pages_alloc, pages_fork (n_pairs pairs) and pages_compact need."""
+        n = self._ws.get(n_pairs)
+        if n is None:
+            n = int(lib().kvc_pages_workspace_bytes(self._ref, int(n_pairs)))
+            if n == 0:
+                raise KvcError(-1, "kvc_pages_workspace_bytes")
+            self._ws[n_pairs] = n
         return n
 
 
@@ -717,10 +749,9 @@ class PageBuffers:
         self.n_blocks = self.tensors[0].shape[0] if self.tensors else 0
         self.device = self.tensors[0].device if self.tensors else None
         for i, t in enumerate(self.tensors):
-            self._c[i].base = _ptr(t, (t.dtype,), (self.n_blocks,) + tuple(t.shape[1:]),
-                                   f"buffer {i}")
+            shp = (self.n_blocks,) + tuple(t.shape[1:])
+            self._c[i].base = _at(t, (t.dtype,), shp, self.device, f"buffer {i}")
             self._c[i].page_bytes = t[:1].numel() * t.element_size()
-            _one_device(self.device, **{f"buffer {i}": t})
         self._ref = ctypes.addressof(self._c)
 
     def _for(self, n_blocks: int, device):
@@ -733,75 +764,94 @@ class PageBuffers:
 def pages_alloc(pages: PageTable, want_len, status=None, ws=None, stream=None):
     """Gives every sequence pages for want_len (int32 [n_seqs]) positions.
     Returns status (int32 [n_seqs]: 0 served, 1 no room, 2 refused)."""
-    B = pages.table.shape[0]
-    _one_device(pages.device, want_len=want_len, status=status)
-    with _On(pages.device, stream) as s:
-        if status is None:
-            status = torch.empty((B,), dtype=torch.int32, device=pages.device)
-        ws = _opt_ws(ws, pages.workspace_bytes(), pages.device)
-        rc = lib().kvc_pages_alloc(pages._ref, _ptr(want_len, (torch.int32,), (B,), "want_len"),
-                                   _ptr(status, (torch.int32,), (B,), "status"), ws.data_ptr(),
-                                   ws.numel(), s)
+    dev = pages.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return pages_alloc(pages, want_len, status, ws)
+    shp = (pages.table.shape[0],)
+    w_ptr = _at(want_len, _I32, shp, dev, "want_len")
+    if status is None:
+        status = torch.empty_like(want_len)
+    ws = _scratch(ws, pages.workspace_bytes(), dev)
+    rc = lib().kvc_pages_alloc(pages._ref, w_ptr, _at(status, _I32, shp, dev, "status"),
+                               *_span(ws), s)
     _check(rc, "kvc_pages_alloc")
     return status
 
 
 def pages_fork(pages: PageTable, src, dst, bufs: PageBuffers, status=None, ws=None, stream=None):
-    """Sequence dst[i] becomes a copy of src[i] (int32 [n_pairs]).  Returns status
-    (int32 [n_pairs])."""
+    """Sequence dst[i] becomes a copy of src[i] (int32 [n_pairs]), its open page
+    copied in `bufs`.  Returns status (int32 [n_pairs])."""
+    dev = pages.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return pages_fork(pages, src, dst, bufs, status, ws)
     n = src.shape[0]
-    ref, n_bufs = bufs._for(pages.n_blocks, pages.device)
-    _one_device(pages.device, src=src, dst=dst, status=status)
-    with _On(pages.device, stream) as s:
-        if status is None:
-            status = torch.empty((n,), dtype=torch.int32, device=pages.device)
-        ws = _opt_ws(ws, pages.workspace_bytes(n), pages.device)
-        rc = lib().kvc_pages_fork(pages._ref, n, _ptr(src, (torch.int32,), (n,), "src"),
-                                  _ptr(dst, (torch.int32,), (n,), "dst"), ref, n_bufs,
-                                  _ptr(status, (torch.int32,), (n,), "status"), ws.data_ptr(),
-                                  ws.numel(), s)
+    ref, n_bufs = bufs._for(pages.n_blocks, dev)
+    s_ptr, d_ptr = _at(src, _I32, (n,), dev, "src"), _at(dst, _I32, (n,), dev, "dst")
+    if status is None:
+        status = torch.empty_like(src)
+    ws = _scratch(ws, pages.workspace_bytes(n), dev)
+    rc = lib().kvc_pages_fork(pages._ref, n, s_ptr, d_ptr, ref, n_bufs,
+                              _at(status, _I32, (n,), dev, "status"), *_span(ws), s)
     _check(rc, "kvc_pages_fork")
     return status
 
 
 def pages_free(pages: PageTable, ids, stream=None):
     """Frees the sequences ids (int32 [n])."""
-    _one_device(pages.device, ids=ids)
-    with _On(pages.device, stream) as s:
-        rc = lib().kvc_pages_free(pages._ref, ids.shape[0],
-                                  _ptr(ids, (torch.int32,), (ids.shape[0],), "ids"), s)
-    _check(rc, "kvc_pages_free")
+    dev = pages.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return pages_free(pages, ids)
+    n = ids.shape[0]
+    _check(lib().kvc_pages_free(pages._ref, n, _at(ids, _I32, (n,), dev, "ids"), s),
+           "kvc_pages_free")
 
 
 def pages_copy(src, dst, bufs: PageBuffers, stream=None):
     """Copies page src[i] to page dst[i] (int32 [n_pairs]) in every buffer."""
+    dev = src.device
+    if dev.type != "cuda":
+        raise ValueError(f"src: must be a GPU tensor, got {dev}")
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return pages_copy(src, dst, bufs)
     n = src.shape[0]
-    _one_device(src.device, dst=dst)
-    ref, n_bufs = bufs._for(bufs.n_blocks, src.device)
-    with _On(src.device, stream) as s:
-        rc = lib().kvc_pages_copy(max(1, bufs.n_blocks), n, _ptr(src, (torch.int32,), (n,), "src"),
-                                  _ptr(dst, (torch.int32,), (n,), "dst"), ref, n_bufs, s)
-    _check(rc, "kvc_pages_copy")
+    ref, n_bufs = bufs._for(bufs.n_blocks, dev)
+    _check(lib().kvc_pages_copy(max(1, bufs.n_blocks), n, _at(src, _I32, (n,), dev, "src"),
+                                _at(dst, _I32, (n,), dev, "dst"), ref, n_bufs, s),
+           "kvc_pages_copy")
 
 
 def pages_compact(pages: PageTable, bufs: PageBuffers, out=None, ws=None, stream=None):
     """Moves the live pages to the front of every buffer.  Returns dict(table,
     refs, remap, n_live): new tensors (or those of `out`), the handle's own are
     left as they were."""
-    ref, n_bufs = bufs._for(pages.n_blocks, pages.device)
+    dev = pages.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return pages_compact(pages, bufs, out, ws)
+    ref, n_bufs = bufs._for(pages.n_blocks, dev)
     o = dict(out or {})
-    _one_device(pages.device, **o)
-    n, shp = pages.n_blocks, tuple(pages.table.shape)
-    with _On(pages.device, stream) as s:
-        for name, shape in (("table", shp), ("refs", (n,)), ("remap", (n,)), ("n_live", (1,))):
-            if o.get(name) is None:
-                o[name] = torch.empty(shape, dtype=torch.int32, device=pages.device)
-        ws = _opt_ws(ws, pages.workspace_bytes(), pages.device)
-        rc = lib().kvc_pages_compact(pages._ref, ref, n_bufs,
-                                     _ptr(o["table"], (torch.int32,), shp, "table"),
-                                     _ptr(o["refs"], (torch.int32,), (n,), "refs"),
-                                     _ptr(o["remap"], (torch.int32,), (n,), "remap"),
-                                     _ptr(o["n_live"], (torch.int32,), (1,), "n_live"),
-                                     ws.data_ptr(), ws.numel(), s)
+    if o.get("table") is None:
+        o["table"] = torch.empty_like(pages.table)
+    for name in ("refs", "remap"):
+        if o.get(name) is None:
+            o[name] = torch.empty_like(pages.refs)
+    if o.get("n_live") is None:
+        o["n_live"] = torch.empty(1, dtype=torch.int32, device=dev)
+    n = (pages.n_blocks,)
+    ws = _scratch(ws, pages.workspace_bytes(), dev)
+    rc = lib().kvc_pages_compact(pages._ref, ref, n_bufs,
+                                 _at(o["table"], _I32, pages.table.shape, dev, "table"),
+                                 _at(o["refs"], _I32, n, dev, "refs"),
+                                 _at(o["remap"], _I32, n, dev, "remap"),
+                                 _at(o["n_live"], _I32, (1,), dev, "n_live"), *_span(ws), s)
     _check(rc, "kvc_pages_compact")
     return o

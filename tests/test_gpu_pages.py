@@ -12,7 +12,9 @@ pytestmark = pytest.mark.gpu
 
 # B, table_blocks, block_size, n_blocks
 SHAPES = [(1, 1, 1, 1), (3, 4, 16, 9), (20, 13, 24, 150), (64, 40, 16, 2000), (300, 20, 8, 4097),
-          (50, 300, 1, 9000)]
+          (50, 300, 1, 9000), (30, 40, 16, 40000),
+          (20, 5000, 2, 90000),      # more pages than every workgroup counts for itself
+          (5000, 3, 8, 12000)]       # more sequences than every workgroup sums
 
 
 def _buffers(seed, n, widths=((4, 16), (3,), (2, 2, 2))):
