@@ -5,7 +5,7 @@
 
 namespace kvc {
 
-constexpr int kPageTile = 16384;    // pages a workgroup counts and ranks
+constexpr int kPageTile = 4096;     // pages a workgroup ranks
 constexpr int kMaxBuffers = 16;     // buffers per launch (by value in the arguments)
 constexpr int64_t kCopyChunk = 8192;  // bytes of a page one workgroup copies at a time
 

@@ -73,30 +73,41 @@ __device__ __forceinline__ uint32_t tile_live(const int32_t* refs, int n, int ti
   *first = tile * kPageTile + wave * (kPageTile / kPlanWaves) + lane;
   int r[kPerLane];
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) {
+  for (int i = 0; i < kPerLane; ++i) {  // no branches: all loads in flight at once
     const int id = *first + i * 64;
-    r[i] = id < n ? refs[id] : 0;
+    r[i] = refs[id < n ? id : n - 1];
   }
   uint32_t live = 0;
 #pragma unroll
-  for (int i = 0; i < kPerLane; ++i) live |= r[i] > 0 ? 1u << i : 0u;
+  for (int i = 0; i < kPerLane; ++i)
+    live |= r[i] > 0 && *first + i * 64 < n ? 1u << i : 0u;
   return live;
 }
 
-// Live pages among refs[0..n), this thread's share.
-__device__ __forceinline__ int count_live(const int32_t* refs, int n) {
-  int sum = 0;
-  for (int base = 0; base < n; base += kPageTile) {
-    int r[kPerLane];
+// A pool of at most 65536 pages as one workgroup sees it: bit j of a thread's
+// mask is page j * 1024 + thread.
+constexpr int kOwnTiles = 64 * kPlanThreads / kPageTile, kBatch = 16;
+__device__ __forceinline__ uint64_t pool_live(const int32_t* refs, int n) {
+  uint64_t mask = 0;
+  for (int base = 0; base < n; base += kBatch * kPlanThreads) {
+    int r[kBatch];
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
+    for (int i = 0; i < kBatch; ++i) {
       const int id = base + i * kPlanThreads + int(threadIdx.x);
-      r[i] = id < n ? refs[id] : 0;
+      r[i] = refs[id < n ? id : n - 1];
     }
+    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) sum += r[i] > 0 ? 1 : 0;
+    for (int i = 0; i < kBatch; ++i)
+      bits |= r[i] > 0 && base + i * kPlanThreads + int(threadIdx.x) < n ? 1u << i : 0u;
+    mask |= uint64_t(bits) << (base / kPlanThreads);
   }
-  return sum;
+  return mask;
+}
+// This thread's live pages below page `end` of such a mask.
+__device__ __forceinline__ int live_in(uint64_t mask, int end) {
+  const int k = (end - int(threadIdx.x) + kPlanThreads - 1) / kPlanThreads;
+  return k <= 0 ? 0 : __popcll(k >= 64 ? mask : mask & ((uint64_t(1) << k) - 1));
 }
 
 // Live pages of each tile, one workgroup each; count is NULL where the tiles
@@ -109,16 +120,10 @@ __global__ __launch_bounds__(kPlanThreads) void k_count(Pages t, int32_t* count)
   if (threadIdx.x == 0) count[blockIdx.x] = total;
 }
 
-// Live pages below page `end`.
-__device__ __forceinline__ int live_below(const Pages& t, const int32_t* count, int end, int* sh) {
+// Sum of the first `tiles` tile counts.
+__device__ __forceinline__ int counted(const int32_t* count, int tiles, int* sh) {
   int x = 0;
-  if (count == nullptr) {
-    x = count_live(t.refs, end);
-  } else {
-    for (int i = threadIdx.x; i < end / kPageTile; i += kPlanThreads) x += count[i];
-    const int cut = end / kPageTile * kPageTile;
-    x += count_live(t.refs + cut, end - cut);
-  }
+  for (int i = threadIdx.x; i < tiles; i += kPlanThreads) x += count[i];
   return block_sum<kPlanWaves>(x, sh);
 }
 
@@ -129,7 +134,11 @@ __device__ __forceinline__ void list_free(const Pages& t, int tile, const int32_
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int first;
   const uint32_t live = tile_live(t.refs, t.n, tile, &first);
-  const int before = live_below(t, count, tile * kPageTile, sh);
+  int before = 0;
+  if (count)
+    before = counted(count, tile, sh);
+  else if (tile > 0)
+    before = block_sum<kPlanWaves>(int(__popcll(pool_live(t.refs, tile * kPageTile))), sh);
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i)
@@ -416,12 +425,25 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(Pages t, const in
                                                                int32_t* place, int32_t* meta,
                                                                int32_t* n_live_out) {
   __shared__ int sh[kPlanWaves];
+  __shared__ int64_t sums[kPlanWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tile = blockIdx.x;
   int first;
   const uint32_t live = tile_live(t.refs, t.n, tile, &first);
-  const int before = live_below(t, count, tile * kPageTile, sh);
-  const int n_live = live_below(t, count, t.n, sh);
-  const int low = live_below(t, count, n_live, sh);  // live pages that stay
+  int before, n_live, low;  // live pages before this tile, in the pool, and that stay
+  if (count) {
+    before = counted(count, tile, sh);
+    n_live = counted(count, int(gridDim.x), sh);
+    const int cut = n_live / kPageTile, at = cut * kPageTile;
+    low = counted(count, cut, sh);
+    low += block_sum<kPlanWaves>(int(__popcll(pool_live(t.refs + at, n_live - at))), sh);
+  } else {
+    const uint64_t mask = pool_live(t.refs, t.n);
+    const int64_t x = int64_t(__popcll(mask)) << 32 | live_in(mask, tile * kPageTile);
+    const int64_t y = block_sum<kPlanWaves>(x, sums);
+    before = int(y & 0x7fffffff);
+    n_live = int(y >> 32);
+    low = block_sum<kPlanWaves>(live_in(mask, n_live), sh);
+  }
   int mine = 0;
 #pragma unroll
   for (int i = 0; i < kPerLane; ++i) mine += __popcll(__ballot(live >> i & 1));
@@ -494,7 +516,6 @@ __global__ __launch_bounds__(kThreads) void k_compact_apply(Pages t, int n_rows,
   }
 }
 
-constexpr int kOwnTiles = 4;      // tiles that every workgroup counts for itself
 constexpr int kOwnSeqs = 4096;    // sequences whose needs every workgroup sums
 
 int tiles_of(const Pages& t) { return (t.n + kPageTile - 1) / kPageTile; }
