@@ -60,17 +60,22 @@ __device__ __forceinline__ int q8_page(const Q8& c, int b, int j) {
 // keys took 24 us so, 29 with 256 or 1024.  It depends on the sequence's own
 // length and rows only, so a head's sums are taken in the same order whatever
 // else is in the launch.
+constexpr int kQ8MaxChunk = 2048;  // the workgroup's LDS holds as many keys
+constexpr int kQ8Chunk = 512, kQ8ChunkRows = 1024;
+static_assert(kQ8Chunk % 128 == 0 && kQ8ChunkRows % 128 == 0 && kQ8MaxChunk % 128 == 0 &&
+                  kQ8Chunk <= kQ8MaxChunk && kQ8ChunkRows <= kQ8MaxChunk,
+              "pieces are whole strides and fit the LDS");
 __host__ __device__ inline int q8_chunk(int len, int rows) {
-  int c = rows <= 16 ? 512 : 1024;
-  while (c < 2048 && len > 64 * c) c *= 2;
+  int c = rows <= 16 ? kQ8Chunk : kQ8ChunkRows;
+  while (c < kQ8MaxChunk && len > 64 * c) c = 2 * c < kQ8MaxChunk ? 2 * c : kQ8MaxChunk;
   const int pieces = (len + c - 1) / c;
   return pieces > 1 ? ((len + pieces - 1) / pieces + 127) & ~127 : c;
 }
 // The most pieces that any length up to cap is cut into.
 inline int q8_max_pieces(int cap, int rows) {
-  const int base = q8_chunk(1, rows);
+  const int base = rows <= 16 ? kQ8Chunk : kQ8ChunkRows;
   if (cap <= 64 * base) return cap > 0 ? (cap + base - 1) / base : 1;
-  const int n = (cap + 2047) / 2048;
+  const int n = (cap + kQ8MaxChunk - 1) / kQ8MaxChunk;
   return n > 64 ? n : 64;
 }
 

@@ -35,17 +35,20 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
-constexpr int kMaxChunk = 2048;
+constexpr int kMaxChunk = kQ8MaxChunk;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
 struct Args {
   Q8 c;
   int W, R, pieces;  // pieces: of the longest length, the grid's
+  FastDiv by_W, by_pieces, by_H;
   int n0;            // first head of this launch
   float c_log2;
   const uint16_t* q;
@@ -106,10 +109,13 @@ __device__ __forceinline__ float block_max(float x, float* sh) {
   return x;
 }
 
-// One output value from its sums, relative to 2^m.
-__device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, float sum,
+// Four output values of a row from their sums, relative to 2^m.
+__device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, f32x4 sum,
                                        float l, float m) {
-  A.out[row * D + dim] = to_bf16(l == 0.0f ? 0.0f : sum / l);
+  const float f = l == 0.0f ? 0.0f : 1.0f / l;
+  sum = l == 0.0f ? f32x4{0, 0, 0, 0} : sum * f;
+  *reinterpret_cast<u16x4*>(A.out + row * D + dim) =
+      u16x4{to_bf16(sum.x), to_bf16(sum.y), to_bf16(sum.z), to_bf16(sum.w)};
   if (A.lse && dim == 0)
     A.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
@@ -137,9 +143,9 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
   const Q8& c = A.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int col = lane & 15, g = lane >> 4;
-  const int piece = int(blockIdx.x % unsigned(A.pieces));
-  const int n = A.n0 + int(blockIdx.x / unsigned(A.pieces)), rb = blockIdx.y;
-  const int b = n / c.H, h = n % c.H;
+  const int nth = int(quot(A.by_pieces, blockIdx.x)), piece = int(blockIdx.x) - nth * A.pieces;
+  const int n = A.n0 + nth, rb = blockIdx.y;
+  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
 
   // Queries, on their way while the keys are looked up.
   u32x4 raw[MT][kSteps];
@@ -245,15 +251,14 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int r = (rb * MT + mt) * 16 + col;
-    uint32_t top = 0;
+    u16x2 tops = {0, 0};  // bf16 magnitudes order like their bits
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = raw[mt][s][i] & 0x7fffu, hi = (raw[mt][s][i] >> 16) & 0x7fffu;
-        top = top > lo ? top : lo;
-        top = top > hi ? top : hi;
-      }
+      for (int i = 0; i < 4; ++i)
+        tops = __builtin_elementwise_max(
+            tops, __builtin_bit_cast(u16x2, raw[mt][s][i] & 0x7fff7fffu));
+    uint32_t top = tops.x > tops.y ? tops.x : tops.y;
 #pragma unroll
     for (int off = 16; off <= 32; off <<= 1) {
       const uint32_t o = uint32_t(__shfl_xor(int(top), off));
@@ -270,7 +275,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
         qf[mt][s][2 * i] = _Float16(__uint_as_float(raw[mt][s][i] << 16) * mul);
         qf[mt][s][2 * i + 1] = _Float16(__uint_as_float(raw[mt][s][i] & 0xffff0000u) * mul);
       }
-    last[mt] = r < A.R ? len - A.W + r % A.W - t0 : 0x7ffffffe;  // rows that are none: see all
+    last[mt] = r < A.R ? len - A.W + (r - int(quot(A.by_W, uint32_t(r))) * A.W) - t0 : 0x7ffffffe;  // rows that are none: see all
     m[mt] = -INFINITY;
     l[mt] = 0.0f;
 #pragma unroll
@@ -382,19 +387,20 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
     }
     __syncthreads();
     const int r0 = (rb * MT + mt) * 16, rows_here = A.R - r0 < 16 ? A.R - r0 : 16;
-    for (int e = tid; e < rows_here * D; e += kThreads) {
-      const int r = e / D, dim = e % D;
+    for (int e = tid; e < rows_here * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), dim = e % (D / 4) * 4;
       const float* at = lds + r * kRowF;
       float M = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * 16 * kRowF + D]);
       const float base = M == -INFINITY ? 0.0f : M;
-      float sum = 0.0f, L = 0.0f;
+      f32x4 sum = {0, 0, 0, 0};
+      float L = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float* aw = at + w * 16 * kRowF;
         const float f = fast_exp2(aw[D] - base);
-        sum += aw[dim] * f;
+        sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
         L += aw[D + 1] * f;
       }
       const size_t row = size_t(n) * A.R + r0 + r;
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
         finish(A, row, D, dim, sum, L, base);
       } else {
         const size_t at_piece = row * A.pieces + piece;
-        A.part[at_piece * D + dim] = sum;
+        *reinterpret_cast<f32x4*>(A.part + at_piece * D + dim) = sum;
         if (dim == 0) {
           A.stat[at_piece * 2] = M;
           A.stat[at_piece * 2 + 1] = L;
@@ -417,7 +423,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_q8_join(Args A, size_t row0) {
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  __shared__ float sums[kAtOnce][D + 4];
+  __shared__ __align__(16) float sums[kAtOnce][D + 4];
   const size_t row = row0 + blockIdx.x;
   const int b = int(row / A.R / unsigned(A.c.H));
   const int len = q8_len(A.c, b), chunk = q8_chunk(len, A.R);
@@ -443,14 +449,15 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A, size_t row0) {
   *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
   if (dim == 0) sums[group][D] = L;
   __syncthreads();
-  if (threadIdx.x >= D) return;
-  float out = 0.0f, l = 0.0f;
+  if (threadIdx.x >= kLanes) return;
+  f32x4 out = {0, 0, 0, 0};
+  float l = 0.0f;
 #pragma unroll
   for (int i = 0; i < kAtOnce; ++i) {
-    out += sums[i][threadIdx.x];
+    out += *reinterpret_cast<const f32x4*>(&sums[i][dim]);
     l += sums[i][D];
   }
-  finish(A, row, D, threadIdx.x, out, l, base);
+  finish(A, row, D, dim, out, l, base);
 }
 
 template <int D, int FMT, int MT>
@@ -486,6 +493,9 @@ hipError_t launch_q8_attend(const Q8& c, int G, int W, float c_log2, const void*
   A.R = G * W;
   A.pieces = q8_max_pieces(c.cap, A.R);
   A.n0 = 0;
+  A.by_W = fast_div(uint32_t(W));
+  A.by_pieces = fast_div(uint32_t(A.pieces));
+  A.by_H = fast_div(uint32_t(c.H));
   A.c_log2 = c_log2;
   A.q = static_cast<const uint16_t*>(q);
   A.out = static_cast<uint16_t*>(out);
