@@ -257,7 +257,7 @@ int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const void* k_new, cons
   const size_t nh = size_t(d.B) * d.H, rows = nh * size_t(window) * d.D * 2;
   int64_t pages = (int64_t(window) + d.bs - 2) / d.bs + 1;
   if (pages > d.tb) pages = d.tb;
-  if (too_many(nh * uint64_t(pages) * 2)) return KVC_EINVAL;
+  if (too_many(nh * uint64_t(pages))) return KVC_EINVAL;
   Range r[6];
   q8_ranges(c, r);
   const Range in[] = {r[4], r[5], {k_new, rows}, {v_new, rows}};

@@ -54,14 +54,17 @@ __device__ __forceinline__ int q8_page(const Q8& c, int b, int j) {
 }
 
 // Keys per workgroup of the attention, for a sequence of len keys and R query
-// rows: pieces of at most 512 (1024 for more than 16 rows, whose partial sums
-// weigh twice as much), at most 1024 and 2048 past 64 such pieces; equal
-// pieces, in multiples of the workgroup's 128-key stride.  256 heads of 1100
-// keys took 24 us so, 29 with 256 or 1024.  It depends on the sequence's own
-// length and rows only, so a head's sums are taken in the same order whatever
-// else is in the launch.
+// rows: pieces of at most 512 keys (640 for more than 16 rows, whose partial
+// sums weigh twice as much), doubled to 2048 while there are more than 64; equal
+// pieces, in multiples of the workgroup's 128-key stride.  Shorter pieces keep
+// a small batch's latency down, longer ones spend less on starting and joining:
+// 8 heads of 4096 keys take 13 us with 512, 18 with 1024, 27 with 2048; 512 heads
+// of 4096 keys 118, 113 and 117; 32 rows on 32 heads of 4096 keys 21 with 640 and
+// 25 with 1024, on 128 heads of 16384 155 and 137.  The length depends on the
+// sequence's own length and rows only, so a head's sums are taken in the same
+// order whatever else is in the launch.
 constexpr int kQ8MaxChunk = 2048;  // the workgroup's LDS holds as many keys
-constexpr int kQ8Chunk = 512, kQ8ChunkRows = 1024;
+constexpr int kQ8Chunk = 512, kQ8ChunkRows = 640;
 static_assert(kQ8Chunk % 128 == 0 && kQ8ChunkRows % 128 == 0 && kQ8MaxChunk % 128 == 0 &&
                   kQ8Chunk <= kQ8MaxChunk && kQ8ChunkRows <= kQ8MaxChunk,
               "pieces are whole strides and fit the LDS");
