@@ -244,8 +244,8 @@ int kvc_q8_load(const kvc_q8_cache* c, int32_t T, int32_t t_stride, void* k_out,
   });
 }
 
-int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const void* k_new, const void* v_new,
-                  void* stream) {
+int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const int32_t* n_new, const void* k_new,
+                  const void* v_new, void* stream) {
   Q8 d;
   int rc = q8_shape(c, &d);
   if (rc != KVC_OK) return rc;
@@ -253,16 +253,19 @@ int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const void* k_new, cons
   if (d.B == 0) return KVC_OK;
   if ((rc = q8_pointers(c)) != KVC_OK) return rc;
   if (!k_new || !v_new) return KVC_EINVAL;
-  if (!aligned(k_new, 16) || !aligned(v_new, 16)) return KVC_EALIGN;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || (n_new && !aligned(n_new, 4)))
+    return KVC_EALIGN;
   const size_t nh = size_t(d.B) * d.H, rows = nh * size_t(window) * d.D * 2;
   int64_t pages = (int64_t(window) + d.bs - 2) / d.bs + 1;
   if (pages > d.tb) pages = d.tb;
   if (too_many(nh * uint64_t(pages))) return KVC_EINVAL;
   Range r[6];
   q8_ranges(c, r);
-  const Range in[] = {r[4], r[5], {k_new, rows}, {v_new, rows}};
-  if (any_alias(in, 4, r, 4)) return KVC_EINVAL;
-  return launch_on(stream, [&](hipStream_t s) { return launch_q8_append(d, window, k_new, v_new, s); });
+  const Range in[] = {r[4], r[5], {k_new, rows}, {v_new, rows}, {n_new, size_t(d.B) * 4}};
+  if (any_alias(in, 5, r, 4)) return KVC_EINVAL;
+  return launch_on(stream, [&](hipStream_t s) {
+    return launch_q8_append(d, window, n_new, k_new, v_new, s);
+  });
 }
 
 size_t kvc_q8_attend_workspace_bytes(const kvc_q8_cache* c, int32_t group, int32_t window) {

@@ -85,8 +85,8 @@ inline int q8_max_pieces(int cap, int rows) {
 hipError_t launch_q8_store(const Q8& c, int T, int TS, const int32_t* kept, int n_kept,
                            const void* k, const void* v, hipStream_t s);
 hipError_t launch_q8_load(const Q8& c, int T, int TS, void* k_out, void* v_out, hipStream_t s);
-hipError_t launch_q8_append(const Q8& c, int W, const void* k_new, const void* v_new,
-                            hipStream_t s);
+hipError_t launch_q8_append(const Q8& c, int W, const int32_t* n_new, const void* k_new,
+                            const void* v_new, hipStream_t s);
 hipError_t launch_q8_attend(const Q8& c, int G, int W, float c_log2, const void* q, void* out,
                             float* lse, float* part, hipStream_t s);
 

@@ -243,6 +243,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_load(Q8 c, int T, int TS, int c
 // twice.
 template <int D, int FMT>
 __global__ __launch_bounds__(kThreads) void k_q8_append(Q8 c, int W,
+                                                        const int32_t* __restrict__ n_new,
                                                         const u32x4* __restrict__ k_new,
                                                         const u32x4* __restrict__ v_new, int pages,
                                                         uint32_t u0, uint32_t units) {
@@ -253,7 +254,13 @@ __global__ __launch_bounds__(kThreads) void k_q8_append(Q8 c, int W,
   const uint32_t pi = u % uint32_t(pages), n = u / uint32_t(pages);
   const int b = n / c.H, h = n % c.H;
   const int L = q8_len(c, b);
-  const int first = L > W ? L - W : 0;  // first new position that exists
+  int mine = W;  // rows this sequence appends
+  if (n_new) {
+    mine = n_new[b];
+    mine = mine < 0 ? 0 : (mine < W ? mine : W);
+    if (mine == 0) return;
+  }
+  const int first = L > mine ? L - mine : 0;  // first new position that exists
   const int pg = int(quot(c.div, uint32_t(first))) + int(pi);
   const int s0 = pg * c.bs;
   if (s0 >= L) return;
@@ -345,12 +352,13 @@ void store(const Q8& c, int T, int TS, const int32_t* kept, int n_kept, const u3
 }
 
 template <int D, int FMT>
-void append(const Q8& c, int W, const u32x4* k, const u32x4* v, hipStream_t s) {
+void append(const Q8& c, int W, const int32_t* n_new, const u32x4* k, const u32x4* v,
+            hipStream_t s) {
   int pages = (W + c.bs - 2) / c.bs + 1;  // pages that W positions can touch
   pages = pages < c.tb ? pages : c.tb;
   const uint64_t units = uint64_t(c.B) * c.H * pages;
   in_launches(units, 4, [&](uint32_t u0, unsigned blocks) {
-    k_q8_append<D, FMT><<<blocks, kThreads, 0, s>>>(c, W, k, v, pages, u0, uint32_t(units));
+    k_q8_append<D, FMT><<<blocks, kThreads, 0, s>>>(c, W, n_new, k, v, pages, u0, uint32_t(units));
   });
 }
 
@@ -393,11 +401,11 @@ hipError_t launch_q8_load(const Q8& c, int T, int TS, void* k_out, void* v_out, 
   return hipGetLastError();
 }
 
-hipError_t launch_q8_append(const Q8& c, int W, const void* k_new, const void* v_new,
-                            hipStream_t s) {
+hipError_t launch_q8_append(const Q8& c, int W, const int32_t* n_new, const void* k_new,
+                            const void* v_new, hipStream_t s) {
   const u32x4* kk = static_cast<const u32x4*>(k_new);
   const u32x4* vv = static_cast<const u32x4*>(v_new);
-#define CALL(D, F) append<D, F>(c, W, kk, vv, s)
+#define CALL(D, F) append<D, F>(c, W, n_new, kk, vv, s)
   KVC_Q8_CASES(CALL);
 #undef CALL
   return hipGetLastError();

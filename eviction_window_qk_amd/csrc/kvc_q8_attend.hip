@@ -48,7 +48,7 @@ constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 struct Args {
   Q8 c;
   int W, R, pieces;  // pieces: of the longest length, the grid's
-  FastDiv by_W, by_pieces, by_H;
+  FastDiv by_W, by_R, by_pieces, by_H;
   int n0;            // first head of this launch
   float c_log2;
   const uint16_t* q;
@@ -421,11 +421,11 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
 // Joins the pieces of one row: D/4 lanes read one piece's sums, the workgroup
 // 1024/D pieces at a time.
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_q8_join(Args A, size_t row0) {
+__global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
   __shared__ __align__(16) float sums[kAtOnce][D + 4];
-  const size_t row = row0 + blockIdx.x;
-  const int b = int(row / A.R / unsigned(A.c.H));
+  const int b = int(quot(A.by_H, A.n0 + quot(A.by_R, blockIdx.x)));
+  const size_t row = size_t(A.n0) * A.R + blockIdx.x;
   const int len = q8_len(A.c, b), chunk = q8_chunk(len, A.R);
   if (len <= chunk) return;
   const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
@@ -472,9 +472,11 @@ void attend(Args A, hipStream_t s) {
                               kThreads, 0, s>>>(A);
   }
   if (A.pieces == 1) return;
-  const size_t rows = size_t(heads) * A.R, step = size_t(1) << 23;
-  for (size_t r0 = 0; r0 < rows; r0 += step)
-    k_q8_join<D><<<unsigned(rows - r0 < step ? rows - r0 : step), kThreads, 0, s>>>(A, r0);
+  const int most_joined = (1 << 23) / A.R;
+  for (A.n0 = 0; A.n0 < heads; A.n0 += most_joined) {
+    const int nh = heads - A.n0 < most_joined ? heads - A.n0 : most_joined;
+    k_q8_join<D><<<unsigned(nh) * unsigned(A.R), kThreads, 0, s>>>(A);
+  }
 }
 
 template <int D, int FMT>
@@ -494,6 +496,7 @@ hipError_t launch_q8_attend(const Q8& c, int G, int W, float c_log2, const void*
   A.pieces = q8_max_pieces(c.cap, A.R);
   A.n0 = 0;
   A.by_W = fast_div(uint32_t(W));
+  A.by_R = fast_div(uint32_t(A.R));
   A.by_pieces = fast_div(uint32_t(A.pieces));
   A.by_H = fast_div(uint32_t(c.H));
   A.c_log2 = c_log2;

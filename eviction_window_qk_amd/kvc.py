@@ -171,7 +171,7 @@ def lib() -> ctypes.CDLL:
                           ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
         "kvc_q8_store": [vp, ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, vp],
         "kvc_q8_load": [vp, ctypes.c_int32, ctypes.c_int32, vp, vp, vp],
-        "kvc_q8_append": [vp, ctypes.c_int32, vp, vp, vp],
+        "kvc_q8_append": [vp, ctypes.c_int32, vp, vp, vp, vp],
         "kvc_q8_attend": [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, vp, vp, vp, vp, sz,
                           vp],
         "kvc_q8_attend_workspace_bytes": [vp, ctypes.c_int32, ctypes.c_int32],
@@ -663,19 +663,21 @@ def q8_load(cache: Q8Cache, T: int, k_out=None, v_out=None, want_v: bool = True,
     return k_out, v_out
 
 
-def q8_append(cache: Q8Cache, k_new, v_new, stream=None):
+def q8_append(cache: Q8Cache, k_new, v_new, n_new=None, stream=None):
     """Appends k_new, v_new (bf16 [heads, window, d]) as the last `window`
-    positions of every sequence (seq_len counts them already).  Returns the
-    cache."""
+    positions of every sequence (seq_len counts them already), or with n_new
+    (int32 [n_seqs]) the last n_new rows of each only.  Returns the cache."""
     dev = cache.device
     s = _here(dev, stream)
     if s is None:
         with _there(dev, stream):
-            return q8_append(cache, k_new, v_new)
+            return q8_append(cache, k_new, v_new, n_new)
     if k_new.dim() != 3:
         raise ValueError("k_new: 3 dimensions expected")
     shp = (cache.heads, k_new.shape[1], cache.head_dim)
-    rc = lib().kvc_q8_append(cache._ref, shp[1], _at(k_new, _BF16_LIKE, shp, dev, "k_new"),
+    rc = lib().kvc_q8_append(cache._ref, shp[1],
+                             _at(n_new, _I32, cache.seq_len.shape, dev, "n_new"),
+                             _at(k_new, _BF16_LIKE, shp, dev, "k_new"),
                              _at(v_new, _BF16_LIKE, shp, dev, "v_new"), s)
     _check(rc, "kvc_q8_append")
     return cache

@@ -380,14 +380,16 @@ int kvc_q8_load(const kvc_q8_cache* c, int32_t T, int32_t t_stride, void* k_out,
 
 /* Appends: the last `window` positions of every sequence (seq_len counts them
  * already) receive k_new, v_new (bf16 [n_seqs * kv_heads][window][d]); new row
- * w goes to position seq_len - window + w (skipped where negative).  A page
+ * w goes to position seq_len - window + w (skipped where negative).  n_new: NULL,
+ * or i32 [n_seqs] on the device: sequence b appends its last n_new[b] rows only
+ * (clamped to 0..window), the rows before them are skipped.  A page
  * whose first row is new takes its scale from the new rows.  One that holds
  * earlier rows keeps its scale unless the new rows alone need a larger one;
  * then its earlier rows are coded again under the larger scale (e4m3: code *
  * old / new rounded to nearest even; int8: rint(code * (old * (1 / new)))).
  * The same call repeated changes nothing.  No workspace. */
-int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const void* k_new, const void* v_new,
-                  void* stream);
+int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const int32_t* n_new, const void* k_new,
+                  const void* v_new, void* stream);
 
 /* Attention of the last `window` positions' queries over the cache.  q, out:
  * bf16 [n_seqs * kv_heads][group][window][d] (the layout of q_win); query w

@@ -133,12 +133,15 @@ def load(c: Cache, T):
     return out
 
 
-def append(c: Cache, k_new, v_new):
-    """k_new, v_new: bf16 bits [B*H, W, d]."""
+def append(c: Cache, k_new, v_new, n_new=None):
+    """k_new, v_new: bf16 bits [B*H, W, d]; the last n_new[b] rows of each."""
     W = k_new.shape[1]
     for b in range(c.B):
         L = c.length(b)
-        first = max(L - W, 0)
+        mine = W if n_new is None else min(max(int(n_new[b]), 0), W)
+        first = max(L - mine, 0)
+        if first >= L:
+            continue
         for j in range(first // c.bs, -(-L // c.bs)):
             p = c.page(b, j)
             if p < 0:

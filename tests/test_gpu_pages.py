@@ -164,3 +164,19 @@ def test_empty_requests():
     one = torch.tensor([0], dtype=torch.int32, device="cuda")
     kvc.pages_copy(one, one, bufs)                          # no buffers: nothing to copy
     u.same_pages(g, t)
+
+
+def test_tables_alone():
+    """Forks and compactions of tables whose pages are kept elsewhere."""
+    t = u.random_pages(12, 8, 5, 4, 30)
+    g = u.pages_to_gpu(t)
+    bufs = kvc.PageBuffers([])
+    src, dst = np.array([0, 1], np.int32), np.array([6, 7], np.int32)
+    st = kvc.pages_fork(g, torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), bufs)
+    assert st.cpu().numpy().tolist() == op.fork(t, src, dst)[0].tolist()
+    u.same_pages(g, t)
+    got = kvc.pages_compact(g, bufs)
+    table, refs, remap, live, _ = op.compact(t)
+    np.testing.assert_array_equal(got["table"].cpu().numpy(), table)
+    np.testing.assert_array_equal(got["remap"].cpu().numpy(), remap)
+    assert int(got["n_live"][0]) == live

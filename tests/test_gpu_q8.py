@@ -126,6 +126,19 @@ def test_append(case, fmt, loud):
     u.same_cache(g, c)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+def test_append_counts_per_sequence(fmt):
+    B, H, d, bs, W = 6, 2, 64, 16, 5
+    c = u.random_cache(27, B, H, d, bs, [20, 20, 33, 3, 40, 18], fmt, poison=False)
+    n_new = np.array([0, 2, 5, 4, -3, 99], np.int32)
+    k, v = u.random_rows(28, B * H, W, d), u.random_rows(29, B * H, W, d)
+    g = u.to_gpu(c)
+    kvc.q8_append(g, u.dev_bf16(k), u.dev_bf16(v), n_new=torch.from_numpy(n_new).cuda())
+    oq.append(c, k, v, n_new)
+    torch.cuda.synchronize()
+    u.same_cache(g, c)
+
+
 ATTEND = [
     # B, H, G, W, d, bs, lengths, holes
     (1, 1, 1, 1, 64, 16, [1], 0.0),

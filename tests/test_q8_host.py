@@ -54,8 +54,8 @@ def _load(c, T=50, ts=50, k=FAKE + 6 * GB, v=FAKE + 7 * GB):
     return kvc.lib().kvc_q8_load(ctypes.addressof(c), T, ts, k, v, None)
 
 
-def _append(c, W=1, k=FAKE + 6 * GB, v=FAKE + 7 * GB):
-    return kvc.lib().kvc_q8_append(ctypes.addressof(c), W, k, v, None)
+def _append(c, W=1, k=FAKE + 6 * GB, v=FAKE + 7 * GB, n_new=None):
+    return kvc.lib().kvc_q8_append(ctypes.addressof(c), W, n_new, k, v, None)
 
 
 def _attend(c, G=4, W=1, scale=0.0, q=FAKE + 6 * GB, out=FAKE + 7 * GB, lse=None, ws=FAKE + 8 * GB, n=1 << 20):
@@ -118,6 +118,8 @@ def test_append_refusals():
     assert _append(_cache(), k=None) == -1
     assert _append(_cache(), k=FAKE + 6 * GB + 4) == -2
     assert _append(_cache(), v=FAKE + 3 * GB) == -1
+    assert _append(_cache(), n_new=FAKE + 8 * GB + 2) == -2
+    assert _append(_cache(), n_new=FAKE + 64) == -1            # counts inside a pool
 
 
 def test_attend_refusals():
