@@ -576,6 +576,16 @@ def _scratch(ws, n, device):
     return ws
 
 
+def _new(like, n=None, dtype=None):
+    """A new tensor beside a checked one: same shape and type, or those given."""
+    t = torch.empty_like(like) if n is None else like.new_empty(n, dtype=dtype)
+    return t, t.data_ptr()
+
+
+def _given(t, dtypes, shape, device, name):
+    return t, _at(t, dtypes, shape, device, name)
+
+
 def _span(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
@@ -649,16 +659,13 @@ def q8_load(cache: Q8Cache, T: int, k_out=None, v_out=None, want_v: bool = True,
     if s is None:
         with _there(dev, stream):
             return q8_load(cache, T, k_out, v_out, want_v)
-    if k_out is None:
-        rows = T if v_out is None else v_out.shape[1]
-        k_out = torch.empty((cache.heads, rows, cache.head_dim), dtype=torch.bfloat16, device=dev)
-    if k_out.dim() != 3:
-        raise ValueError("k_out: 3 dimensions expected")
-    if v_out is None and want_v:
-        v_out = torch.empty_like(k_out)
-    shp = (cache.heads, k_out.shape[1], cache.head_dim)
-    rc = lib().kvc_q8_load(cache._ref, int(T), shp[1], _at(k_out, _BF16_LIKE, shp, dev, "k_out"),
-                           _at(v_out, _BF16_LIKE, shp, dev, "v_out"), s)
+    rows = T if k_out is None and v_out is None else (v_out if k_out is None else k_out).shape[1]
+    shp = (cache.heads, rows, cache.head_dim)
+    k_out, k_ptr = (_new(cache.table, shp, torch.bfloat16) if k_out is None else
+                    _given(k_out, _BF16_LIKE, shp, dev, "k_out"))
+    v_out, v_ptr = (_new(k_out) if v_out is None and want_v else
+                    _given(v_out, _BF16_LIKE, shp, dev, "v_out"))
+    rc = lib().kvc_q8_load(cache._ref, T, rows, k_ptr, v_ptr, s)
     _check(rc, "kvc_q8_load")
     return k_out, v_out
 
@@ -699,13 +706,11 @@ def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, sca
     shp = (cache.heads, G, W, cache.head_dim)
     q_ptr = _at(q, _BF16_LIKE, shp, dev, "q")
     ws = _scratch(ws, cache.attend_workspace_bytes(G, W), dev)
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty(shp[:3], dtype=torch.float32, device=dev)
-    rc = lib().kvc_q8_attend(cache._ref, G, W, float(scale), q_ptr,
-                             _at(out, _BF16_LIKE, shp, dev, "out"),
-                             _at(lse, _F32, shp[:3], dev, "lse"), *_span(ws), s)
+    out, out_ptr = _new(q) if out is None else _given(out, _BF16_LIKE, shp, dev, "out")
+    lse, lse_ptr = (_new(q, shp[:3], torch.float32) if lse is None and want_lse else
+                    _given(lse, _F32, shp[:3], dev, "lse"))
+    rc = lib().kvc_q8_attend(cache._ref, G, W, scale, q_ptr, out_ptr, lse_ptr,
+                             *_span(ws), s)
     _check(rc, "kvc_q8_attend")
     return out if lse is None else (out, lse)
 
@@ -773,11 +778,9 @@ def pages_alloc(pages: PageTable, want_len, status=None, ws=None, stream=None):
             return pages_alloc(pages, want_len, status, ws)
     shp = (pages.table.shape[0],)
     w_ptr = _at(want_len, _I32, shp, dev, "want_len")
-    if status is None:
-        status = torch.empty_like(want_len)
+    status, st_ptr = _new(want_len) if status is None else _given(status, _I32, shp, dev, "status")
     ws = _scratch(ws, pages.workspace_bytes(), dev)
-    rc = lib().kvc_pages_alloc(pages._ref, w_ptr, _at(status, _I32, shp, dev, "status"),
-                               *_span(ws), s)
+    rc = lib().kvc_pages_alloc(pages._ref, w_ptr, st_ptr, *_span(ws), s)
     _check(rc, "kvc_pages_alloc")
     return status
 
@@ -793,11 +796,9 @@ def pages_fork(pages: PageTable, src, dst, bufs: PageBuffers, status=None, ws=No
     n = src.shape[0]
     ref, n_bufs = bufs._for(pages.n_blocks, dev)
     s_ptr, d_ptr = _at(src, _I32, (n,), dev, "src"), _at(dst, _I32, (n,), dev, "dst")
-    if status is None:
-        status = torch.empty_like(src)
+    status, st_ptr = _new(src) if status is None else _given(status, _I32, (n,), dev, "status")
     ws = _scratch(ws, pages.workspace_bytes(n), dev)
-    rc = lib().kvc_pages_fork(pages._ref, n, s_ptr, d_ptr, ref, n_bufs,
-                              _at(status, _I32, (n,), dev, "status"), *_span(ws), s)
+    rc = lib().kvc_pages_fork(pages._ref, n, s_ptr, d_ptr, ref, n_bufs, st_ptr, *_span(ws), s)
     _check(rc, "kvc_pages_fork")
     return status
 
@@ -840,20 +841,14 @@ def pages_compact(pages: PageTable, bufs: PageBuffers, out=None, ws=None, stream
         with _there(dev, stream):
             return pages_compact(pages, bufs, out, ws)
     ref, n_bufs = bufs._for(pages.n_blocks, dev)
-    o = dict(out or {})
-    if o.get("table") is None:
-        o["table"] = torch.empty_like(pages.table)
-    for name in ("refs", "remap"):
-        if o.get(name) is None:
-            o[name] = torch.empty_like(pages.refs)
-    if o.get("n_live") is None:
-        o["n_live"] = torch.empty(1, dtype=torch.int32, device=dev)
-    n = (pages.n_blocks,)
+    o, ptr, n = dict(out or {}), {}, (pages.n_blocks,)
+    for name, like, shp in (("table", pages.table, pages.table.shape), ("refs", pages.refs, n),
+                            ("remap", pages.refs, n), ("n_live", pages.refs, (1,))):
+        t = o.get(name)
+        o[name], ptr[name] = (_given(t, _I32, shp, dev, name) if t is not None else
+                              _new(like) if name != "n_live" else _new(like, 1, torch.int32))
     ws = _scratch(ws, pages.workspace_bytes(), dev)
-    rc = lib().kvc_pages_compact(pages._ref, ref, n_bufs,
-                                 _at(o["table"], _I32, pages.table.shape, dev, "table"),
-                                 _at(o["refs"], _I32, n, dev, "refs"),
-                                 _at(o["remap"], _I32, n, dev, "remap"),
-                                 _at(o["n_live"], _I32, (1,), dev, "n_live"), *_span(ws), s)
+    rc = lib().kvc_pages_compact(pages._ref, ref, n_bufs, ptr["table"], ptr["refs"], ptr["remap"],
+                                 ptr["n_live"], *_span(ws), s)
     _check(rc, "kvc_pages_compact")
     return o
