@@ -74,6 +74,11 @@ __host__ __device__ inline int q8_chunk(int len, int rows) {
   const int pieces = (len + c - 1) / c;
   return pieces > 1 ? ((len + pieces - 1) / pieces + 127) & ~127 : c;
 }
+// The longest piece that any length up to cap has.
+inline int q8_longest_chunk(int cap, int rows) {
+  const int base = rows <= 16 ? kQ8Chunk : kQ8ChunkRows;
+  return cap <= 64 * base ? base : kQ8MaxChunk;
+}
 // The most pieces that any length up to cap is cut into.
 inline int q8_max_pieces(int cap, int rows) {
   const int base = rows <= 16 ? kQ8Chunk : kQ8ChunkRows;

@@ -25,7 +25,12 @@
 // The keys of a head are cut into pieces by its own length (q8_chunk); the
 // four waves of a workgroup take the 32-key tiles of a piece in turn, and
 // their sums meet in LDS.  A second kernel joins the pieces where there are
-// several.
+// several.  Where a piece's keys are and what they weigh is looked up once, into
+// LDS: for four keys at a time where the page size is a multiple of four (every
+// lane's keys come in fours), for each key where it is not.  With short pieces
+// the look-up and the merge, not the keys, are what a batch of ordinary lengths
+// spends its time on: on 512 heads of 1100 keys 11 of 40 us went into a look-up
+// by single keys.
 #include <type_traits>
 
 #include "kvc_q8.h"
@@ -41,8 +46,18 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
+#ifndef KVC_O
+#define KVC_O 3
+#endif
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr int kMaxChunk = kQ8MaxChunk;
+// What a look-up says of its keys: the first one's row in the pools, the key
+// scale, log2 of the value scale (-inf: there is no page) and its reciprocal.
+struct __align__(16) Where {
+  uint32_t row;
+  float ks, lv, iv;
+};
+
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
 struct Args {
@@ -50,6 +65,7 @@ struct Args {
   int W, R, pieces;  // pieces: of the longest length, the grid's
   FastDiv by_W, by_R, by_pieces, by_H;
   int n0;            // first head of this launch
+  int lds_rows;      // rows of a wave's sums in LDS: min(R, 16)
   float c_log2;
   const uint16_t* q;
   uint16_t* out;
@@ -123,22 +139,19 @@ __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim
 // Three waves a SIMD: a tile of each in flight covers the latency of HBM, and
 // nothing is gained by a second tile in registers at two waves (29 against
 // 24 us on 256 heads of 1100 keys).  32 rows at D = 128 need the registers of two.
-template <int D, int FMT, int MT>
-__global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_attend(Args A) {
+template <int D, int FMT, int MT, int GROUP>
+__global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q8_attend(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
   constexpr int kVWords = D / 64;       // words of one key's values in a lane
   constexpr int kRowF = D + 4;          // floats of one merged row: sums, m, l
-  constexpr int kKeysLds = kMaxChunk * 4;
-  constexpr int kMergeLds = kWaves * 16 * kRowF;
-  __shared__ __align__(16) float lds[kKeysLds > kMergeLds ? kKeysLds : kMergeLds];
-  uint32_t* const row_of = reinterpret_cast<uint32_t*>(lds);  // pool row of each key
-  float* const ks_of = lds + kMaxChunk;                       // its key scale
-  float* const lv_of = lds + 2 * kMaxChunk;                   // log2 of its value scale
-  float* const iv_of = lds + 3 * kMaxChunk;                   // 1 / its value scale
-
+  constexpr int kGroups = 4 / GROUP;    // look-ups of four keys
+  constexpr int kPerTile = 32 / GROUP;
+  extern __shared__ __align__(16) unsigned char lds_raw[];
+  Where* const where = reinterpret_cast<Where*>(lds_raw);  // then the waves' sums
+  float* const lds = reinterpret_cast<float*>(lds_raw);
   __shared__ float top_of[kWaves];
-  __shared__ uint32_t none_of[kMaxChunk / 32];                // which keys of a tile are none
+  __shared__ uint32_t none_of[kMaxChunk / 32];  // which look-ups of a tile found no page
 
   const Q8& c = A.c;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -146,6 +159,13 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
   const int nth = int(quot(A.by_pieces, blockIdx.x)), piece = int(blockIdx.x) - nth * A.pieces;
   const int n = A.n0 + nth, rb = blockIdx.y;
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
+
+  const int len = q8_len(c, b);
+  const int chunk = q8_chunk(len, A.R);
+  const int t0 = piece * chunk;
+  if (t0 >= len && piece > 0) return;
+  const int keys = len - t0 < chunk ? len - t0 : chunk;  // of this piece, 0 for an empty sequence
+  const bool alone = len <= chunk;
 
   // Queries, on their way while the keys are looked up.
   u32x4 raw[MT][kSteps];
@@ -161,30 +181,23 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
       }
     }
   }
-  const int len = q8_len(c, b);
-  const int chunk = q8_chunk(len, A.R);
-  const int t0 = piece * chunk;
-  if (t0 >= len && piece > 0) return;
-  const int keys = len - t0 < chunk ? len - t0 : chunk;  // of this piece, 0 for an empty sequence
-  const bool alone = len <= chunk;
-
-  // Where the keys of this piece are; a key that is none (in no page, or past
+  // Where the keys of this piece are.  A look-up that finds no page (or lies past
   // the end) points to row 0, whose bytes are dropped later.  The scales follow
   // after a first barrier, when the first tile's loads are on their way.
-  const int padded = (keys + 31) & ~31;
-  for (int i = tid; i < (padded + 63 & ~63); i += kThreads) {
+  const int padded = (keys + 31) & ~31, lookups = padded / GROUP;
+  for (int i = tid; i < ((lookups + 63) & ~63); i += kThreads) {
     uint32_t row = kNone;
-    if (i < keys) {
-      const uint32_t t = uint32_t(t0 + i), j = quot(c.div, t);
+    if (i * GROUP < keys) {
+      const uint32_t t = uint32_t(t0 + i * GROUP), j = quot(c.div, t);
       const int page = q8_page(c, b, int(j));
       if (page >= 0)
         row = (uint32_t(page) * uint32_t(c.H) + uint32_t(h)) * c.div.d + (t - j * c.div.d);
     }
     const uint64_t none = __ballot(row == kNone);
-    if (i < padded) {
-      row_of[i] = row == kNone ? 0 : row;
-      lv_of[i] = row == kNone ? -INFINITY : 0.0f;
-      if ((lane & 31) == 0) none_of[i >> 5] = uint32_t(lane ? none >> 32 : none);
+    if (i < lookups) {
+      where[i].row = row == kNone ? 0 : row;
+      where[i].lv = row == kNone ? -INFINITY : 0.0f;
+      if (lane % kPerTile == 0) none_of[i / kPerTile] = uint32_t(none >> lane) & (0xffffffffu >> (32 - kPerTile));
     }
   }
   __syncthreads();
@@ -198,23 +211,21 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
   auto fetch = [&](int tile, Tile& x) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const uint8_t* at = c.k + size_t(row_of[tile + half * 16 + col]) * D + g * 16;
+      const int key = tile + half * 16 + col;
+      const uint8_t* at = c.k + size_t(where[key / GROUP].row) * D + (col % GROUP * D + g * 16);
 #pragma unroll
       for (int s = 0; s < kSteps / 2; ++s)
         x.k[half][s] = *reinterpret_cast<const u32x4*>(at + s * 64);
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const u32x4 rows = *reinterpret_cast<const u32x4*>(row_of + tile + half * 16 + 4 * g);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint8_t* at = c.v + size_t(rows[i]) * D + col * (D / 16);
-        if constexpr (kVWords == 2) {
-          const u32x2 y = *reinterpret_cast<const u32x2*>(at);
-          x.v[half * 4 + i][0] = y.x, x.v[half * 4 + i][1] = y.y;
-        } else {
-          x.v[half * 4 + i][0] = *reinterpret_cast<const uint32_t*>(at);
-        }
+    for (int i = 0; i < 8; ++i) {
+      const int key = tile + (i >> 2) * 16 + 4 * g + (i & 3);
+      const uint8_t* at = c.v + size_t(where[key / GROUP].row) * D + (i % GROUP * D + col * (D / 16));
+      if constexpr (kVWords == 2) {
+        const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+        x.v[i][0] = y.x, x.v[i][1] = y.y;
+      } else {
+        x.v[i][0] = *reinterpret_cast<const uint32_t*>(at);
       }
     }
   };
@@ -222,24 +233,24 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
   if (wave * 32 < keys) fetch(wave * 32, cur);
 
   float vtop = 0.0f;
-  for (int i = tid; i < padded; i += kThreads) {
+  for (int i = tid; i < lookups; i += kThreads) {
     float ks = 0.0f, vs = 0.0f;
-    if (lv_of[i] == 0.0f) {
-      const uint32_t ph = quot32(c.div, row_of[i]);
+    if (where[i].lv == 0.0f) {
+      const uint32_t ph = quot32(c.div, where[i].row);
       ks = c.ks[ph];
       vs = c.vs[ph];
     }
-    ks_of[i] = ks;
-    iv_of[i] = vs;
+    where[i].ks = ks;
+    where[i].iv = vs;
     vtop = fmaxf(vtop, vs);
   }
   vtop = block_max(vtop, top_of);
   // A value scale more than 2^40 below the piece's largest (an empty page's)
   // counts as that far below it: the weights span fp32, not more.
-  for (int i = tid; i < padded; i += kThreads) {
-    const float vs = fmaxf(iv_of[i], fmaxf(vtop * 0x1p-40f, 0x1p-126f));
-    if (lv_of[i] == 0.0f) lv_of[i] = __builtin_amdgcn_logf(vs);
-    iv_of[i] = __builtin_amdgcn_rcpf(vs);
+  for (int i = tid; i < lookups; i += kThreads) {
+    const float vs = fmaxf(where[i].iv, fmaxf(vtop * 0x1p-40f, 0x1p-126f));
+    if (where[i].lv == 0.0f) where[i].lv = __builtin_amdgcn_logf(vs);
+    where[i].iv = __builtin_amdgcn_rcpf(vs);
   }
 
   // Queries to fp16 fragments of rows scaled by a power of two.
@@ -285,12 +296,12 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
   __syncthreads();
 
   auto work = [&](int tile, const Tile& x, auto checked) {
-    const auto at4 = [&](const float* of, int half) {
-      return *reinterpret_cast<const f32x4*>(of + tile + half * 16 + 4 * g);
-    };
-    const f32x4 ks[2] = {at4(ks_of, 0), at4(ks_of, 1)};
-    const f32x4 lv[2] = {at4(lv_of, 0), at4(lv_of, 1)};
-    const f32x4 iv[2] = {at4(iv_of, 0), at4(iv_of, 1)};
+    Where at[2][kGroups];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i)
+        at[half][i] = where[(tile + half * 16 + 4 * g) / GROUP + i];
     float scores[MT][8];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -308,10 +319,11 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
           a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[k], qf[mt][k], a, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float y = __builtin_fmaf(a[i] * ks[half][i], qc[mt], lv[half][i]);
+          const Where& of = at[half][i / GROUP];
+          float y = __builtin_fmaf(a[i] * of.ks, qc[mt], of.lv);
           if constexpr (checked.value) {
             const int t = tile + half * 16 + 4 * g + i;
-            if (t > last[mt] || lv[half][i] == -INFINITY) y = -INFINITY;
+            if (t > last[mt] || of.lv == -INFINITY) y = -INFINITY;
           }
           scores[mt][half * 4 + i] = y;
         }
@@ -337,7 +349,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float e = fast_exp2(y[j] - base);
-        l[mt] = __builtin_fmaf(e, iv[j >> 2][j & 3], l[mt]);
+        l[mt] = __builtin_fmaf(e, at[j >> 2][(j & 3) / GROUP].iv, l[mt]);
         w[mt][j] = _Float16(e);
       }
     }
@@ -347,7 +359,10 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         v[j] = x.v[j][u];
-        if (checked.value && lv[j >> 2][j & 3] == -INFINITY) v[j] = 0;
+        if constexpr (checked.value) {
+          const int t = tile + (j >> 2) * 16 + 4 * g + (j & 3);
+          if (t >= keys || at[j >> 2][(j & 3) / GROUP].lv == -INFINITY) v[j] = 0;
+        }
       }
       turn4(v[0], v[1], v[2], v[3], lo);
       turn4(v[4], v[5], v[6], v[7], hi);
@@ -361,13 +376,10 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
       }
     }
   };
-  auto step = [&](int tile, const Tile& x) {
-    if (tile + 31 <= low && none_of[tile >> 5] == 0) work(tile, x, std::false_type{});
-    else work(tile, x, std::true_type{});
-  };
   for (int tile = wave * 32; tile < keys; tile += kWaves * 32) {
     if (tile != wave * 32) fetch(tile, cur);
-    step(tile, cur);
+    if (tile + 31 <= low && none_of[tile >> 5] == 0) work(tile, cur, std::false_type{});
+    else work(tile, cur, std::true_type{});
   }
 
   // The waves' sums meet in LDS (over the key arrays), 16 rows at a time.
@@ -376,29 +388,31 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 3) void k_q8_at
     __syncthreads();
 #pragma unroll
     for (int off = 16; off <= 32; off <<= 1) l[mt] += __shfl_xor(l[mt], off);
-    float* to = lds + (wave * 16 + col) * kRowF;
+    const int r0 = (rb * MT + mt) * 16, rows_here = A.R - r0 < 16 ? A.R - r0 : 16;
+    float* to = lds + (wave * A.lds_rows + col) * kRowF;
+    if (col < rows_here) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)  // values of row 4g + r of tile i: dim (4g + r) * kTiles + i
+      for (int r = 0; r < 4; ++r)  // values of row 4g + r of tile i: dim (4g + r) * kTiles + i
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
-    if (g == 0) {
-      to[D] = m[mt];
-      to[D + 1] = l[mt];
+        for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
+      if (g == 0) {
+        to[D] = m[mt];
+        to[D + 1] = l[mt];
+      }
     }
     __syncthreads();
-    const int r0 = (rb * MT + mt) * 16, rows_here = A.R - r0 < 16 ? A.R - r0 : 16;
     for (int e = tid; e < rows_here * (D / 4); e += kThreads) {
       const int r = e / (D / 4), dim = e % (D / 4) * 4;
       const float* at = lds + r * kRowF;
       float M = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * 16 * kRowF + D]);
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * A.lds_rows * kRowF + D]);
       const float base = M == -INFINITY ? 0.0f : M;
       f32x4 sum = {0, 0, 0, 0};
       float L = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float* aw = at + w * 16 * kRowF;
+        const float* aw = at + w * A.lds_rows * kRowF;
         const float f = fast_exp2(aw[D] - base);
         sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
         L += aw[D + 1] * f;
@@ -460,16 +474,20 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
   finish(A, row, D, dim, out, l, base);
 }
 
-template <int D, int FMT, int MT>
+template <int D, int FMT, int MT, int GROUP>
 void attend(Args A, hipStream_t s) {
   // (head, piece) in x, below 2^23 workgroups (the grid counts work-items in
   // 32 bits), row blocks in y.
   const int heads = A.c.B * A.c.H, blocks_y = (A.R + MT * 16 - 1) / (MT * 16);
   const int most = (1 << 23) / A.pieces;
+  A.lds_rows = A.R < 16 ? A.R : 16;
+  const size_t keys = size_t(q8_longest_chunk(A.c.cap, A.R)) / GROUP * sizeof(Where);
+  const size_t sums = size_t(kWaves) * A.lds_rows * (D + 4) * sizeof(float);
   for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
     const int nh = heads - A.n0 < most ? heads - A.n0 : most;
-    k_q8_attend<D, FMT, MT><<<dim3(unsigned(nh) * unsigned(A.pieces), unsigned(blocks_y)),
-                              kThreads, 0, s>>>(A);
+    k_q8_attend<D, FMT, MT, GROUP>
+        <<<dim3(unsigned(nh) * unsigned(A.pieces), unsigned(blocks_y)), kThreads,
+           keys > sums ? keys : sums, s>>>(A);
   }
   if (A.pieces == 1) return;
   const int most_joined = (1 << 23) / A.R;
@@ -481,8 +499,14 @@ void attend(Args A, hipStream_t s) {
 
 template <int D, int FMT>
 void attend_rows(const Args& A, hipStream_t s) {
-  if (A.R <= 16) attend<D, FMT, 1>(A, s);
-  else attend<D, FMT, 2>(A, s);
+  const bool fours = A.c.bs % 4 == 0;
+  if (A.R <= 16) {
+    if (fours) attend<D, FMT, 1, 4>(A, s);
+    else attend<D, FMT, 1, 1>(A, s);
+  } else {
+    if (fours) attend<D, FMT, 2, 4>(A, s);
+    else attend<D, FMT, 2, 1>(A, s);
+  }
 }
 
 }  // namespace
