@@ -46,9 +46,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-#ifndef KVC_O
-#define KVC_O 3
-#endif
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr int kMaxChunk = kQ8MaxChunk;
 // What a look-up says of its keys: the first one's row in the pools, the key
@@ -136,11 +133,15 @@ __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim
     A.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
 
-// Three waves a SIMD: a tile of each in flight covers the latency of HBM, and
-// nothing is gained by a second tile in registers at two waves (29 against
-// 24 us on 256 heads of 1100 keys).  32 rows at D = 128 need the registers of two.
+// Four waves a SIMD: a tile of each in flight covers the latency of HBM, and
+// nothing is gained by a second tile in registers at two waves (29 against 24 us
+// on 256 heads of 1100 keys).  The checks for keys that are not seen sit in a
+// branch of the one tile body: a body with and one without them took 160
+// registers for 120 and ran at three waves, 10 % slower on ragged drafts.  32 rows
+// at D = 128 need the registers of two waves (at three they spill: 146 us
+// became 269 on 128 heads of 16384 keys).
 template <int D, int FMT, int MT, int GROUP>
-__global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q8_attend(Args A) {
+__global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : 4) void k_q8_attend(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
   constexpr int kVWords = D / 64;       // words of one key's values in a lane
@@ -295,7 +296,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q
   const int low = len - A.W - t0;  // the first query's last key: all rows see the keys up to it
   __syncthreads();
 
-  auto work = [&](int tile, const Tile& x, auto checked) {
+  auto work = [&](int tile, Tile& x, bool checked) {
     Where at[2][kGroups];
 #pragma unroll
     for (int half = 0; half < 2; ++half)
@@ -320,13 +321,21 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const Where& of = at[half][i / GROUP];
-          float y = __builtin_fmaf(a[i] * of.ks, qc[mt], of.lv);
-          if constexpr (checked.value) {
-            const int t = tile + half * 16 + 4 * g + i;
-            if (t > last[mt] || of.lv == -INFINITY) y = -INFINITY;
-          }
-          scores[mt][half * 4 + i] = y;
+          scores[mt][half * 4 + i] = __builtin_fmaf(a[i] * of.ks, qc[mt], of.lv);
         }
+      }
+    }
+    if (checked) {  // the same for the whole wave
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = tile + (j >> 2) * 16 + 4 * g + (j & 3);
+        const bool none = at[j >> 2][(j & 3) / GROUP].lv == -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if (t > last[mt] || none) scores[mt][j] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kVWords; ++u)
+          if (t >= keys || none) x.v[j][u] = 0;
       }
     }
     f16x8 w[MT];
@@ -355,17 +364,9 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q
     }
 #pragma unroll
     for (int u = 0; u < kVWords; ++u) {
-      uint32_t v[8], lo[4], hi[4];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = x.v[j][u];
-        if constexpr (checked.value) {
-          const int t = tile + (j >> 2) * 16 + 4 * g + (j & 3);
-          if (t >= keys || at[j >> 2][(j & 3) / GROUP].lv == -INFINITY) v[j] = 0;
-        }
-      }
-      turn4(v[0], v[1], v[2], v[3], lo);
-      turn4(v[4], v[5], v[6], v[7], hi);
+      uint32_t lo[4], hi[4];
+      turn4(x.v[0][u], x.v[1][u], x.v[2][u], x.v[3][u], lo);
+      turn4(x.v[4][u], x.v[5][u], x.v[6][u], x.v[7][u], hi);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f16x8 vf = frag<FMT>(lo[i], hi[i]);
@@ -378,8 +379,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && D == 128 ? 2 : KVC_O) void k_q
   };
   for (int tile = wave * 32; tile < keys; tile += kWaves * 32) {
     if (tile != wave * 32) fetch(tile, cur);
-    if (tile + 31 <= low && none_of[tile >> 5] == 0) work(tile, cur, std::false_type{});
-    else work(tile, cur, std::true_type{});
+    work(tile, cur, tile + 31 > low || none_of[tile >> 5] != 0);
   }
 
   // The waves' sums meet in LDS (over the key arrays), 16 rows at a time.
