@@ -323,8 +323,10 @@ int kvc_pages_alloc(const kvc_page_table* t, const int32_t* want_len, int32_t* s
   pages_ranges(t, out);
   out[3] = {status, per_seq};
   out[4] = {ws, ws_bytes};
-  const Range in[] = {{want_len, per_seq}};
-  if (any_alias(in, 1, out, 5)) return KVC_EINVAL;
+  // the lengths are not touched, and are what a caller wants most often
+  const Range in[] = {{want_len, per_seq}, out[1]};
+  out[1] = Range{nullptr, 0};
+  if (any_alias(in, 2, out, 5)) return KVC_EINVAL;
   return launch_on(stream, [&](hipStream_t s) {
     return launch_pages_alloc(p, want_len, status, static_cast<int32_t*>(ws), s);
   });

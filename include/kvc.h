@@ -442,7 +442,8 @@ typedef struct kvc_page_buffer {
 /* Gives every sequence b pages for its positions 0..want_len[b]-1: entries
  * among its first ceil(want_len[b] / block_size) that name no page receive
  * one, all or none per sequence.  want_len: i32 [n_seqs], 0 = leave alone,
- * negative or past the table: status 2.  seq_len is not changed.
+ * negative or past the table: status 2.  seq_len is not changed (want_len may be
+ * seq_len itself).
  * status: i32 [n_seqs]. */
 int kvc_pages_alloc(const kvc_page_table* t, const int32_t* want_len, int32_t* status, void* ws,
                     size_t ws_bytes, void* stream);

@@ -182,7 +182,7 @@ def test_captured_decode_step_replays():
 
     def step(g, pages):
         g.seq_len.add_(1)
-        st = kvc.pages_alloc(pages, g.seq_len.clone())
+        st = kvc.pages_alloc(pages, g.seq_len)
         kvc.q8_append(g, k_in, v_in)
         return (st,) + tuple(kvc.q8_attend(g, q_in, want_lse=True))
 

@@ -194,6 +194,7 @@ def test_page_calls_refused():
     assert _alloc(_table(), ws=None) == -3 and _alloc(_table(), n=16) == -3
     assert _alloc(_table(), ws=FAKE + 5 * GB + 4) == -2
     assert _alloc(_table(), want=FAKE) == -1                   # inside the table
+    assert _alloc(_table(), status=FAKE + GB) == -1            # the lengths
     assert _alloc(_table(n_seqs=0, table=None), want=None) == 0
     assert _fork(_table(), pairs=-1) == -1 and _fork(_table(), src=None) == -1 and _fork(_table(), status=None) == -1
     assert _fork(_table(), pairs=0, src=None) == 0
