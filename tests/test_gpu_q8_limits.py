@@ -1,0 +1,97 @@
+"""The 8-bit paged cache at sizes that take several launches, or offsets past 32
+bits: a few heads of each against the oracle or against a small call."""
+import numpy as np
+import pytest
+import torch
+
+from eviction_window_qk_amd import kvc
+from oracle import q8 as oq
+import q8_utils as u
+
+pytestmark = pytest.mark.gpu
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def test_attention_over_tables_of_2_to_30_positions():
+    """17 heads in tables with room for 2^30 positions each: the pieces of 16 heads
+    fill a launch.  Same bits as with tables as long as the sequences."""
+    B, bs, d, tb = 17, 4096, 64, 1 << 18
+    lens = [1, 5, 100, 512, 513, 4096, 4097, 9000] + [300 + 40 * i for i in range(9)]
+    small = u.random_cache(1, B, 1, d, bs, lens, oq.INT8, poison=False)
+    g = u.to_gpu(small)
+    table = torch.full((B, tb), -1, dtype=torch.int32, device="cuda")
+    table[:, : small.table.shape[1]] = g.table
+    wide = kvc.Q8Cache(g.k_pool, g.v_pool, g.k_scale, g.v_scale, table, g.seq_len)
+    q = u.dev_bf16(u.random_rows(2, B, 1, 1, d))
+    out, lse = kvc.q8_attend(wide, q, want_lse=True)
+    ref, ref_lse = kvc.q8_attend(g, q, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    bounded = kvc.Q8Cache(g.k_pool, g.v_pool, g.k_scale, g.v_scale, table, g.seq_len, max_len=9000)
+    assert bounded.attend_workspace_bytes(1) < wide.attend_workspace_bytes(1)
+    out = kvc.q8_attend(bounded, q)
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16))
+    u.check_attention(small, u.random_rows(2, B, 1, 1, d), ref, ref_lse)
+
+
+def test_attention_of_the_most_rows_on_many_heads():
+    """4096 query rows on 2100 heads: the pieces are joined in two launches.  The
+    last heads have the bits they have alone."""
+    B, H, G, W, d, bs, L = 300, 7, 64, 64, 64, 64, 700
+    n = 40
+    k = torch.randint(-127, 128, (n, H, bs, d), dtype=torch.int8, device="cuda")
+    v = torch.randint(-127, 128, (n, H, bs, d), dtype=torch.int8, device="cuda")
+    ks, vs = torch.rand((n, H), device="cuda") * 0.01, torch.rand((n, H), device="cuda")
+    table = torch.randint(0, n, (B, -(-L // bs)), dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    q = torch.randn((B * H, G, W, d), device="cuda", dtype=torch.bfloat16)
+    c = kvc.Q8Cache(k, v, ks, vs, table, lens)
+    out, lse = kvc.q8_attend(c, q, want_lse=True)
+    for b in (0, 292, B - 1):                              # head 2048 is sequence 292's
+        one = kvc.Q8Cache(k, v, ks, vs, table[b:b + 1].contiguous(), lens[:1].contiguous())
+        o, s = kvc.q8_attend(one, q[b * H:(b + 1) * H].contiguous(), want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[b * H:(b + 1) * H].view(torch.int16))
+        assert torch.equal(s, lse[b * H:(b + 1) * H])
+
+
+def test_store_in_two_launches():
+    """33.6 million pages of one row: past 2^25 pages of K and V a second launch."""
+    B, d, T = 260, 64, 65536
+    n = B * T
+    assert 2 * n > 1 << 25
+    k = torch.randn((B, T, d), device="cuda", dtype=torch.bfloat16)
+    v = torch.randn((B, T, d), device="cuda", dtype=torch.bfloat16)
+    pool = lambda: torch.zeros((n, 1, 1, d), dtype=torch.float8_e4m3fn, device="cuda")
+    c = kvc.Q8Cache(pool(), pool(), torch.zeros((n, 1), device="cuda"), torch.zeros((n, 1), device="cuda"),
+                    torch.arange(n, dtype=torch.int32, device="cuda").reshape(B, T), _i32([T] * B))
+    kvc.q8_store(c, k, v)
+    torch.cuda.synchronize()
+    for b in (0, 128, B - 1):
+        for rows, codes, scale in ((k, c.k_pool, c.k_scale), (v, c.v_pool, c.v_scale)):
+            at = torch.tensor([0, 1, T // 2, T - 1])
+            x = rows[b, at].float().cpu().numpy()
+            got = u.bits8(codes[b * T + at, 0, 0].contiguous())
+            for i in range(4):
+                s, inv = oq.page_scale(np.abs(x[i]).max(), oq.E4M3)
+                assert float(scale[b * T + int(at[i]), 0]) == float(s)
+                np.testing.assert_array_equal(got[i], oq.encode(x[i] * inv, oq.E4M3))
+    back, _ = kvc.q8_load(c, 4, want_v=False)
+    assert back.shape == (B, 4, d) and bool(torch.isfinite(back).all())
+
+
+def test_page_copies_past_32_bits():
+    """Pages of 16 MiB in a buffer of 5.4 GB, odd bytes beside it."""
+    n, size = 320, 16 << 20
+    big = torch.zeros((n, size), dtype=torch.uint8, device="cuda")
+    odd = torch.zeros((n, 7), dtype=torch.uint8, device="cuda")
+    for p in (317, 319):
+        big[p] = torch.randint(0, 256, (size,), dtype=torch.uint8, device="cuda")
+        odd[p] = p % 256
+    kvc.pages_copy(_i32([319, 317]), _i32([2, 300]), kvc.PageBuffers([big, odd]))
+    torch.cuda.synchronize()
+    assert torch.equal(big[2], big[319]) and torch.equal(big[300], big[317])
+    assert torch.equal(odd[2], odd[319]) and torch.equal(odd[300], odd[317])
+    assert int(big[:2].max()) == 0 and int(big[3:300].max()) == 0 and int(big[301:317].max()) == 0
