@@ -452,6 +452,8 @@ int kvc_pages_alloc(const kvc_page_table* t, const int32_t* want_len, int32_t* s
  * becomes a copy of src[i]: it shares the floor(len / block_size) full pages,
  * and an open last page is copied to a new page in all n_bufs buffers (host
  * array; n_bufs 0..4096).  Pages given up are free from the next call on.
+ * What a sequence appends to is then its own; one that is cut back into a page
+ * it shares (a shorter seq_len) has to be forked again before it appends.
  * src, dst: i32 [n_pairs] on the device.  Status 2: an id out of range, src
  * = dst, dst named by an earlier pair, or src named as dst by any pair.
  * status: i32 [n_pairs]. */

@@ -180,3 +180,31 @@ def test_tables_alone():
     np.testing.assert_array_equal(got["table"].cpu().numpy(), table)
     np.testing.assert_array_equal(got["remap"].cpu().numpy(), remap)
     assert int(got["n_live"][0]) == live
+
+
+def test_many_buffers_and_holes():
+    """Forty buffers (several launches), entries of a source that name no page."""
+    n = 40
+    rng = u.rng_of(13)
+    t = op.Pages(np.full((5, 4), -1), np.zeros(5), np.zeros(n), 8)
+    t.table[0], t.lens[0] = [30, -1, 12, 39], 27            # open page 39, a hole before it
+    t.table[1, :2], t.lens[1] = [5, 2 ** 31 - 1], 12        # the open entry names no page
+    t.table[4, :1], t.lens[4] = [39 - 8], 8
+    t.refs[[30, 12, 39, 5, 31]] = 1
+    g = u.pages_to_gpu(t)
+    tensors = [torch.from_numpy(rng.integers(0, 256, (n, 1 + 16 * i)).astype(np.uint8)).cuda() for i in range(40)]
+    bufs = kvc.PageBuffers(tensors)
+    before = _host(tensors)
+    src, dst = np.array([0, 1], np.int32), np.array([2, 4], np.int32)
+    st = kvc.pages_fork(g, torch.from_numpy(src).cuda(), torch.from_numpy(dst).cuda(), bufs)
+    ref, copies = op.fork(t, src, dst)
+    assert st.cpu().numpy().tolist() == ref.tolist() == [0, 0] and copies == [(39, 0)]
+    u.same_pages(g, t)
+    _check_copies(tensors, before, copies)
+    before = _host(tensors)
+    got = kvc.pages_compact(g, bufs)
+    table, refs, remap, live, copies = op.compact(t)
+    np.testing.assert_array_equal(got["table"].cpu().numpy(), table)
+    np.testing.assert_array_equal(got["refs"].cpu().numpy(), refs)
+    assert int(got["n_live"][0]) == live
+    _check_copies(tensors, before, copies)
