@@ -8,10 +8,10 @@
 // decisions, table rows by some workgroups and page bytes by others.  A tile's
 // rank needs the counts of the tiles before it, which each workgroup takes
 // itself from pools of up to 65536 pages; larger pools, and calls for more than
-// 4096 sequences, spend a launch on sums first (two launches of a call take
-// about 7 us, three 10).  Counts change by integer atomics, whose order does not
-// matter to the result.  The page copies are bound by HBM, the rest by launch
-// latency.
+// 4096 sequences, spend a launch on sums first (a launch costs a call about 3 us;
+// deciding takes 3 us in a pool of 1000 pages and 7 in one of 32768).  Counts
+// change by integer atomics, whose order does not matter to the result.  The
+// page copies are bound by HBM (5 TB/s), the rest by launch latency.
 #include "kvc_pages.h"
 
 namespace kvc {
@@ -254,6 +254,56 @@ __global__ __launch_bounds__(kThreads) void k_alloc_apply(Pages t, const int32_t
       t.refs[p] = 1;
     }
     rank += total;
+  }
+}
+
+// A small call in one launch, by one workgroup: the same decisions, with the
+// free pages and the needs in LDS; a wave looks at a sequence at a time.
+constexpr int kSmallSeqs = 64;
+__global__ __launch_bounds__(kPlanThreads) void k_alloc_small(Pages t, const int32_t* want,
+                                                              int32_t* status) {
+  __shared__ int sh[kPlanWaves];
+  __shared__ int32_t list[kPageTile];
+  __shared__ int32_t need[kSmallSeqs];  // then the requests before each
+  __shared__ int32_t n_free;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int b = wave; b < t.B; b += kPlanWaves) {
+    const int entries = wanted(t, want[b]);
+    const int32_t* row = t.table + size_t(b) * t.tb;
+    int miss = 0;
+    for (int j0 = 0; j0 < entries; j0 += 64)
+      miss += __popcll(__ballot(j0 + lane < entries && !is_page(t, row[j0 + lane])));
+    if (lane == 0) need[b] = miss;
+  }
+  list_free(t, 0, nullptr, list, &n_free, sh);
+  __syncthreads();
+  const int b0 = threadIdx.x;
+  const int mine = b0 < t.B ? need[b0] : 0;
+  int total;
+  const int off = block_scan<kPlanWaves>(mine, sh, &total);
+  const int free = n_free;
+  const bool fits = off + mine <= free;
+  __syncthreads();
+  if (b0 < t.B) {
+    need[b0] = mine > 0 && fits ? off : -1;
+    status[b0] = wanted(t, want[b0]) < 0 ? 2 : (fits || mine == 0 ? 0 : 1);
+  }
+  __syncthreads();
+  for (int b = wave; b < t.B; b += kPlanWaves) {
+    int rank = need[b];
+    if (rank < 0) continue;
+    const int entries = wanted(t, want[b]);
+    int32_t* row = t.table + size_t(b) * t.tb;
+    for (int j0 = 0; j0 < entries; j0 += 64) {
+      const bool miss = j0 + lane < entries && !is_page(t, row[j0 + lane]);
+      const uint64_t m = __ballot(miss);
+      if (miss) {
+        const int32_t p = list[rank + below(m, lane)];
+        row[j0 + lane] = p;
+        t.refs[p] = 1;
+      }
+      rank += __popcll(m);
+    }
   }
 }
 
@@ -565,6 +615,15 @@ hipError_t launch_pages_alloc(const Pages& t, const int32_t* want, int32_t* stat
                               hipStream_t s) {
   const PagesWs w = pages_ws(t, 0);
   const int tiles = tiles_of(t), per = kPlanThreads / kThreads;
+  // One launch where a wave has at most four steps of table entries to look at:
+  // 7.6 us a call against 10 with two launches (16 sequences of 49 entries; 5.3 us
+  // on the GPU either way).  256 sequences of 64 entries would take 12 in one.
+  const int steps = ((t.B + kPlanWaves - 1) / kPlanWaves) * ((t.tb + 63) / 64);
+  if (tiles == 1 && steps <= 4) {
+    static_assert(4 * kPlanWaves <= kSmallSeqs, "the needs fit the LDS");
+    k_alloc_small<<<1, kPlanThreads, 0, s>>>(t, want, status);
+    return hipGetLastError();
+  }
   const int32_t* count = counts(t, ws + w.count, s);
   k_alloc_plan<<<unsigned(tiles + (t.B + per - 1) / per), kPlanThreads, 0, s>>>(
       t, tiles, want, count, ws + w.list, ws + w.meta, ws + w.need);

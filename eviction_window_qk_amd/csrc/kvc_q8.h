@@ -58,9 +58,9 @@ __device__ __forceinline__ int q8_page(const Q8& c, int b, int j) {
 // sums weigh twice as much), doubled to 2048 while there are more than 64; equal
 // pieces, in multiples of the workgroup's 128-key stride.  Shorter pieces keep
 // a small batch's latency down, longer ones spend less on starting and joining:
-// 8 heads of 4096 keys take 13 us with 512, 18 with 1024, 27 with 2048; 512 heads
-// of 4096 keys 118, 113 and 117; 32 rows on 32 heads of 4096 keys 21 with 640 and
-// 25 with 1024, on 128 heads of 16384 155 and 137.  The length depends on the
+// 8 heads of 4096 keys take 12 us with 512 and 15 with 1024, 512 heads of 4096
+// keys 110 and 106; 32 rows on 32 heads of 4096 keys 20 us with 640 and 22 with
+// 1024, on 128 heads of 16384 keys 145 and 128.  The length depends on the
 // sequence's own length and rows only, so a head's sums are taken in the same
 // order whatever else is in the launch.
 constexpr int kQ8MaxChunk = 2048;  // the workgroup's LDS holds as many keys
