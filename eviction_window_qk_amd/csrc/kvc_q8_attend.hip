@@ -60,7 +60,8 @@ constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 struct Args {
   Q8 c;
   int W, R, pieces;  // pieces: of the longest length, the grid's
-  FastDiv by_W, by_R, by_pieces, by_H;
+  FastDiv by_W, by_R, by_pieces, by_H, by_blocks;
+  int units, unit0;  // (head, piece) pairs of n0's heads, first one of this launch
   int n0;            // first head of this launch
   int lds_rows;      // rows of a wave's sums in LDS: min(R, 16)
   float c_log2;
@@ -161,10 +162,17 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
   // the XCDs in turn, and where only the first pieces of a long table have keys
   // they would all be one XCD's (512 heads of 128 keys in tables of 16384: 118 us
   // without the rotation, 18 with it).
-  const int nth = int(quot(A.by_pieces, blockIdx.x));
-  int piece = int(blockIdx.x) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
+  // The row blocks of a piece follow each other on one XCD, whose L2 then reads its
+  // keys once (81 rows on 9 heads of 62000 keys: 57 us with the blocks in a grid
+  // dimension of their own, 52 so).
+  const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
+  const int rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
+  const uint32_t unit = uint32_t(A.unit0) + eight * 8 + (blockIdx.x & 7);
+  if (unit >= uint32_t(A.units)) return;
+  const int nth = int(quot(A.by_pieces, unit));
+  int piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
   piece -= piece >= A.pieces ? A.pieces : 0;
-  const int n = A.n0 + nth, rb = blockIdx.y;
+  const int n = A.n0 + nth;
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
 
   const int len = q8_len(c, b);
@@ -482,18 +490,23 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
 
 template <int D, int FMT, int MT, int GROUP>
 void attend(Args A, hipStream_t s) {
-  // (head, piece) in x, below 2^23 workgroups (the grid counts work-items in
-  // 32 bits), row blocks in y.
-  const int heads = A.c.B * A.c.H, blocks_y = (A.R + MT * 16 - 1) / (MT * 16);
-  const int most = (1 << 23) / A.pieces;
+  // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits), in
+  // whole eights of units.
+  const int heads = A.c.B * A.c.H, blocks = (A.R + MT * 16 - 1) / (MT * 16);
+  const int room = ((1 << 23) / blocks) & ~7;
+  const int most = room / A.pieces > 0 ? room / A.pieces : 1;
+  A.by_blocks = fast_div(uint32_t(blocks));
   A.lds_rows = A.R < 16 ? A.R : 16;
   const size_t keys = size_t(q8_longest_chunk(A.c.cap, A.R)) / GROUP * sizeof(Where);
   const size_t sums = size_t(kWaves) * A.lds_rows * (D + 4) * sizeof(float);
   for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
     const int nh = heads - A.n0 < most ? heads - A.n0 : most;
-    k_q8_attend<D, FMT, MT, GROUP>
-        <<<dim3(unsigned(nh) * unsigned(A.pieces), unsigned(blocks_y)), kThreads,
-           keys > sums ? keys : sums, s>>>(A);
+    A.units = nh * A.pieces;
+    for (A.unit0 = 0; A.unit0 < A.units; A.unit0 += room) {
+      const int here = A.units - A.unit0 < room ? A.units - A.unit0 : room;
+      k_q8_attend<D, FMT, MT, GROUP><<<unsigned((here + 7) / 8) * 8u * unsigned(blocks), kThreads,
+                                       keys > sums ? keys : sums, s>>>(A);
+    }
   }
   if (A.pieces == 1) return;
   const int most_joined = (1 << 23) / A.R;
