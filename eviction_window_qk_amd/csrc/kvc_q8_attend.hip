@@ -111,6 +111,12 @@ __device__ __forceinline__ uint16_t to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
 
+template <bool STREAM, class T>
+__device__ __forceinline__ T load(const uint8_t* at) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(at));
+  else return *reinterpret_cast<const T*>(at);
+}
+
 // Maximum over the workgroup, in every thread.
 __device__ __forceinline__ float block_max(float x, float* sh) {
 #pragma unroll
@@ -141,7 +147,7 @@ __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim
 // registers for 120 and ran at three waves, 10 % slower on ragged drafts.  32 rows
 // at D = 128 need the registers of two waves (at three they spill: 146 us
 // became 269 on 128 heads of 16384 keys).
-template <int D, int FMT, int MT, int GROUP>
+template <int D, int FMT, int MT, int GROUP, bool STREAM>
 __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 3 : 4) void k_q8_attend(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
@@ -229,18 +235,17 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
       const int key = tile + half * 16 + col;
       const uint8_t* at = c.k + size_t(where[key / GROUP].row) * D + (col % GROUP * D + g * 16);
 #pragma unroll
-      for (int s = 0; s < kSteps / 2; ++s)
-        x.k[half][s] = *reinterpret_cast<const u32x4*>(at + s * 64);
+      for (int s = 0; s < kSteps / 2; ++s) x.k[half][s] = load<STREAM, u32x4>(at + s * 64);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int key = tile + (i >> 2) * 16 + 4 * g + (i & 3);
       const uint8_t* at = c.v + size_t(where[key / GROUP].row) * D + (i % GROUP * D + col * (D / 16));
       if constexpr (kVWords == 2) {
-        const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+        const u32x2 y = load<STREAM, u32x2>(at);
         x.v[i][0] = y.x, x.v[i][1] = y.y;
       } else {
-        x.v[i][0] = *reinterpret_cast<const uint32_t*>(at);
+        x.v[i][0] = load<STREAM, uint32_t>(at);
       }
     }
   };
@@ -488,7 +493,7 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
   finish(A, row, D, dim, out, l, base);
 }
 
-template <int D, int FMT, int MT, int GROUP>
+template <int D, int FMT, int MT, int GROUP, bool STREAM>
 void attend(Args A, hipStream_t s) {
   // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits), in
   // whole eights of units.
@@ -504,8 +509,9 @@ void attend(Args A, hipStream_t s) {
     A.units = nh * A.pieces;
     for (A.unit0 = 0; A.unit0 < A.units; A.unit0 += room) {
       const int here = A.units - A.unit0 < room ? A.units - A.unit0 : room;
-      k_q8_attend<D, FMT, MT, GROUP><<<unsigned((here + 7) / 8) * 8u * unsigned(blocks), kThreads,
-                                       keys > sums ? keys : sums, s>>>(A);
+      k_q8_attend<D, FMT, MT, GROUP, STREAM>
+          <<<unsigned((here + 7) / 8) * 8u * unsigned(blocks), kThreads, keys > sums ? keys : sums,
+             s>>>(A);
     }
   }
   if (A.pieces == 1) return;
@@ -519,12 +525,19 @@ void attend(Args A, hipStream_t s) {
 template <int D, int FMT>
 void attend_rows(const Args& A, hipStream_t s) {
   const bool fours = A.c.bs % 4 == 0;
+  // Keys and values that one row block reads, out of pools that are a good part of the
+  // last-level cache (256 MB), are read past the caches, which they would only empty.
+  // 51 us against 55 on one sequence of 131072 keys (270 MB), 56 against 60 on 512
+  // heads of 2048 keys, 30 against 32 on 8 heads of 65536; on pools of 70 MB, found
+  // there again by the next call, 22.2 against 20.8.
+  const bool stream = uint64_t(A.c.n_blocks) * A.c.H * A.c.bs * D * 2 > (uint64_t(96) << 20);
   if (A.R <= 16) {
-    if (fours) attend<D, FMT, 1, 4>(A, s);
-    else attend<D, FMT, 1, 1>(A, s);
+    if (fours && stream) attend<D, FMT, 1, 4, true>(A, s);
+    else if (fours) attend<D, FMT, 1, 4, false>(A, s);
+    else attend<D, FMT, 1, 1, false>(A, s);
   } else {
-    if (fours) attend<D, FMT, 2, 4>(A, s);
-    else attend<D, FMT, 2, 1>(A, s);
+    if (fours) attend<D, FMT, 2, 4, false>(A, s);
+    else attend<D, FMT, 2, 1, false>(A, s);
   }
 }
 

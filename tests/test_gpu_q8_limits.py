@@ -57,6 +57,36 @@ def test_attention_of_the_most_rows_on_many_heads():
         assert torch.equal(s, lse[b * H:(b + 1) * H])
 
 
+@pytest.mark.parametrize("fmt", [oq.E4M3, oq.INT8])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_out_of_large_pools(fmt, d):
+    """Keys out of pools of over 100 MB, read past the caches: the bits of the same
+    call on pools that hold no other page, with dead pages and empty sequences."""
+    B, H, G, W, bs = 5, 2, 4, 3, 16
+    small = u.random_cache(3, B, H, d, bs, [0, 1, 77, 1100, 4097], fmt, holes=0.05, poison=True)
+    g = u.to_gpu(small)
+    held = g.k_pool.shape[0]
+    n = -(-(101 << 20) // (2 * H * bs * d))
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(4))[:held].cuda()
+
+    def spread(x):
+        as_int = torch.int8 if x.element_size() == 1 else torch.int32
+        y = torch.zeros((n, *x.shape[1:]), dtype=as_int, device="cuda")
+        y[at] = x.view(as_int)
+        return y.view(x.dtype)
+
+    good = (g.table >= 0) & (g.table < held)
+    table = torch.where(good, at[g.table.clamp(0, held - 1).long()].int(), torch.full_like(g.table, -1))
+    big = kvc.Q8Cache(spread(g.k_pool), spread(g.v_pool), spread(g.k_scale), spread(g.v_scale), table, g.seq_len)
+    bits = u.random_rows(5, B * H, G, W, d)
+    q = u.dev_bf16(bits)
+    out, lse = kvc.q8_attend(big, q, want_lse=True)
+    ref, ref_lse = kvc.q8_attend(g, q, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), ref.view(torch.int16)) and torch.equal(lse, ref_lse)
+    u.check_attention(small, bits, out, lse)
+
+
 def test_store_in_two_launches():
     """33.6 million pages of one row: past 2^25 pages of K and V a second launch."""
     B, d, T = 260, 64, 65536
