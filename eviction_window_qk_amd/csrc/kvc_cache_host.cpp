@@ -279,7 +279,7 @@ int kvc_q8_attend(const kvc_q8_cache* c, int32_t group, int32_t window, float sc
   Q8 d;
   int rc = attend_shape(c, group, window, &d);
   if (rc != KVC_OK) return rc;
-  if (!(scale >= 0.0f) || !std::isfinite(scale)) return KVC_EINVAL;
+  if (!(scale >= 0.0f && scale <= 0x1p127f)) return KVC_EINVAL;  // scale * log2(e) is finite
   if (d.B == 0) return KVC_OK;
   if ((rc = q8_pointers(c)) != KVC_OK) return rc;
   if (!q || !out) return KVC_EINVAL;

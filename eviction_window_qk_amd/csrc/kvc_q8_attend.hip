@@ -2,10 +2,10 @@
 //
 // For every (sequence, KV head) the G query heads' W queries form the R = G*W
 // rows of two products against the same keys and values:
-//   x = c * ks * <q, code_k> + log2 vs,  w = 2^(x - m),
-//   l = sum w / vs,  out = sum w * code_v / l
-// with c = scale * log2(e), ks and vs the page scales, m a running maximum of
-// x.  Each cached byte is read once for all R rows; with the few rows of a
+//   x = c * ks * <q, code_k> + log2 r,  w = 2^(x - m),
+//   l = sum w / r,  out = top * sum w * code_v / l
+// with c = scale * log2(e), ks and vs the page scales, top the largest vs among
+// the keys that a workgroup takes and r = vs / top, m a running maximum of x.  Each cached byte is read once for all R rows; with the few rows of a
 // decode step the bound is HBM: 2*d bytes per key.
 //
 // Both products run on fp16 matrix instructions, 16x16x32: e4m3 and int8 codes
@@ -13,7 +13,9 @@
 // below 2^-29 of the row's largest lose bits), and the weights keep 11 bits.
 // A weight carries its page's value scale inside the exponent, so one exp2 a
 // score gives a number in (0, 1] whatever the scales are; the denominator
-// takes the scale out again, in fp32.
+// takes the scale out again, in fp32.  The scale is taken relative to the
+// largest of the workgroup's keys: hundreds of zero values (scale 2^-126) weigh
+// in the denominator as much as any others, and 2^126 each would overflow it.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P': the lane that
 // holds eight scores of a query row (keys 4g..4g+3 of two 16-key tiles, g its
@@ -42,6 +44,7 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
@@ -68,8 +71,8 @@ struct Args {
   const uint16_t* q;
   uint16_t* out;
   float* lse;
-  float* part;  // [n][row][piece][D] sums
-  float* stat;  // [n][row][piece][2] m, l
+  float* part;  // [n][row][piece][D] outputs of a piece
+  float* stat;  // [n][row][piece][2] their m, l
 };
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -129,13 +132,11 @@ __device__ __forceinline__ float block_max(float x, float* sh) {
   return x;
 }
 
-// Four output values of a row from their sums, relative to 2^m.
-__device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, f32x4 sum,
+// Four output values of a row, and its sum of weights l relative to 2^m.
+__device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, f32x4 out,
                                        float l, float m) {
-  const float f = l == 0.0f ? 0.0f : 1.0f / l;
-  sum = l == 0.0f ? f32x4{0, 0, 0, 0} : sum * f;
   *reinterpret_cast<u16x4*>(A.out + row * D + dim) =
-      u16x4{to_bf16(sum.x), to_bf16(sum.y), to_bf16(sum.z), to_bf16(sum.w)};
+      u16x4{to_bf16(out.x), to_bf16(out.y), to_bf16(out.z), to_bf16(out.w)};
   if (A.lse && dim == 0)
     A.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
 }
@@ -264,13 +265,15 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
     where[i].iv = vs;
     vtop = fmaxf(vtop, vs);
   }
-  vtop = block_max(vtop, top_of);
+  vtop = fmaxf(block_max(vtop, top_of), 0x1p-126f);
+  vtop = __uint_as_float(uint32_t(__builtin_amdgcn_readfirstlane(int(__float_as_uint(vtop)))));
   // A value scale more than 2^40 below the piece's largest (an empty page's)
   // counts as that far below it: the weights span fp32, not more.
+  const float by_top = 1.0f / vtop;
   for (int i = tid; i < lookups; i += kThreads) {
-    const float vs = fmaxf(where[i].iv, fmaxf(vtop * 0x1p-40f, 0x1p-126f));
-    if (where[i].lv == 0.0f) where[i].lv = __builtin_amdgcn_logf(vs);
-    where[i].iv = __builtin_amdgcn_rcpf(vs);
+    const float r = fmaxf(where[i].iv * by_top, 0x1p-40f);
+    if (where[i].lv == 0.0f) where[i].lv = __builtin_amdgcn_logf(r);
+    where[i].iv = __builtin_amdgcn_rcpf(r);
   }
 
   // Queries to fp16 fragments of rows scaled by a power of two.
@@ -436,6 +439,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
         sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
         L += aw[D + 1] * f;
       }
+      sum = L == 0.0f ? f32x4{0, 0, 0, 0} : sum * __builtin_amdgcn_rcpf(L) * vtop;
       const size_t row = size_t(n) * A.R + r0 + r;
       if (alone) {
         finish(A, row, D, dim, sum, L, base);
@@ -451,46 +455,47 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
   }
 }
 
-// Joins the pieces of one row: D/4 lanes read one piece's sums, the workgroup
-// 1024/D pieces at a time.
+// Joins the pieces of one row, each weighted by its l: D/4 lanes read one
+// piece's outputs, the workgroup 1024/D pieces at a time.
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  __shared__ __align__(16) float sums[kAtOnce][D + 4];
+  __shared__ __align__(16) float sums[kAtOnce][D];
   const int b = int(quot(A.by_H, A.n0 + quot(A.by_R, blockIdx.x)));
   const size_t row = size_t(A.n0) * A.R + blockIdx.x;
   const int len = q8_len(A.c, b), chunk = q8_chunk(len, A.R);
   if (len <= chunk) return;
   const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
   const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
-  const float* st = A.stat + row * A.pieces * 2;
+  const f32x2* st = reinterpret_cast<const f32x2*>(A.stat) + row * A.pieces;
   const float* part = A.part + row * A.pieces * D + dim;
-  float M = -INFINITY;
-  for (int p = lane; p < pieces; p += 64) M = fmaxf(M, st[p * 2]);
+  f32x2 ml = {-INFINITY, 0.0f};  // the lane's piece of the first 64
+  if (lane < pieces) ml = st[lane];
+  float M = ml.x;
+  for (int p = lane + 64; p < pieces; p += 64) M = fmaxf(M, st[p].x);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
   const float base = M == -INFINITY ? 0.0f : M;
+  float L = ml.y * fast_exp2(ml.x - base);
+  for (int p = lane + 64; p < pieces; p += 64)
+    L = __builtin_fmaf(st[p].y, fast_exp2(st[p].x - base), L);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off);
+  const float by_L = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
   f32x4 sum = {0, 0, 0, 0};
-  float L = 0.0f;
 #pragma unroll 4
   for (int p = group; p < pieces; p += kAtOnce) {
     const f32x4 x = *reinterpret_cast<const f32x4*>(part + size_t(p) * D);
-    const float f = fast_exp2(st[p * 2] - base);
-    sum += x * f;
-    L = __builtin_fmaf(st[p * 2 + 1], f, L);
+    const f32x2 w = st[p];
+    sum += x * (w.y * fast_exp2(w.x - base) * by_L);
   }
   *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
-  if (dim == 0) sums[group][D] = L;
   __syncthreads();
   if (threadIdx.x >= kLanes) return;
   f32x4 out = {0, 0, 0, 0};
-  float l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) {
-    out += *reinterpret_cast<const f32x4*>(&sums[i][dim]);
-    l += sums[i][D];
-  }
-  finish(A, row, D, dim, out, l, base);
+  for (int i = 0; i < kAtOnce; ++i) out += *reinterpret_cast<const f32x4*>(&sums[i][dim]);
+  finish(A, row, D, dim, out, L, base);
 }
 
 template <int D, int FMT, int MT, int GROUP, bool STREAM>

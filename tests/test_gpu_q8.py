@@ -184,6 +184,51 @@ def test_attend_scales_far_apart(fmt, spread):
     u.check_attention(c, q, out, lse, scale=0.25)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("where", ["all", "first", "middle"])
+def test_attend_values_of_nothing(where, d, fmt):
+    """Zero values over hundreds of keys weigh in the denominators like any others:
+    in pages stored as zeros (scale 2^-126) and in pages of scale 0, next to values
+    in the thousands."""
+    B, H, G, W, bs, lens = 2, 2, 3, 2, 16, [1700, 40]
+    c = u.random_cache(40, B, H, d, bs, lens, fmt, poison=False)
+    c.vs = (c.vs * np.float32(2.0 ** 16)).astype(np.float32)
+    at = {"all": [(0, 1700), (0, 40)], "first": [(0, 640), (0, 16)], "middle": [(512, 1264), (16, 32)]}[where]
+    for b in range(B):
+        pages = c.table[b, at[b][0] // bs:-(-at[b][1] // bs)]
+        c.v[pages] = 0
+        c.vs[pages, 0] = 2.0 ** -126
+        c.vs[pages, 1] = 0.0
+    q = u.random_rows(41, B * H, G, W, d)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse)
+    if where == "all":
+        assert not out.view(torch.int16).bitwise_and(0x7FFF).any()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("power", [-90, 100])
+def test_attend_values_at_the_ends_of_fp32(power, fmt):
+    """Values of 2^-90 or 2^100 only: relative accuracy as at one.  In pages 2^60
+    apart, hundreds of keys each, the small ones' outputs vanish beside the
+    large, their weights do not."""
+    B, H, G, W, d, bs = 1, 2, 3, 1, 128, 16
+    c = u.random_cache(42, B, H, d, bs, [1500], fmt, poison=False)
+    plain = c.vs.copy()
+    q = u.random_rows(43, B * H, G, W, d)
+    c.vs = (plain * np.float32(2.0 ** power)).astype(np.float32)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True)
+    c.vs = plain
+    u.check_attention(c, q, (out.double() * 2.0 ** -power).float(), lse)
+    c.vs = (plain * np.float32(2.0 ** power)).astype(np.float32)
+    c.vs[c.table[0, : 768 // bs]] *= np.float32(2.0 ** (60 if power < 0 else -60))
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse)
+
+
 def test_attend_query_range():
     """Queries from the smallest to large magnitudes, and a zero row."""
     B, H, G, W, d, bs = 1, 1, 6, 1, 128, 16

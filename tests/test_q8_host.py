@@ -133,6 +133,7 @@ def test_attend_refusals():
     assert _attend(c, G=64, W=65) == -1                        # 4160 rows
     assert _attend(c, scale=-1.0) == -1
     assert _attend(c, scale=float("nan")) == -1 and _attend(c, scale=float("inf")) == -1
+    assert _attend(c, scale=2.0 ** 127 * 1.5) == -1            # times log2(e) past fp32
     assert _attend(c, q=None) == -1 and _attend(c, out=None) == -1
     assert _attend(c, q=FAKE + 6 * GB + 2) == -2 and _attend(c, lse=FAKE + 9 * GB + 1) == -2
     assert _attend(c, ws=None) == -3 and _attend(c, n=need - 1) == -3
