@@ -58,6 +58,7 @@ struct __align__(16) Where {
   float ks, lv, iv;
 };
 
+constexpr float kMost = 0x1.fffffep127f;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
 struct Args {
@@ -340,10 +341,12 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
 #pragma unroll
         for (int k = 0; k < kSteps; ++k)
           a = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[k], qf[mt][k], a, 0, 0, 0);
+        // the scales' product first: one for a look-up's keys, and a tiny query's
+        // takes a huge key's back into range
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const Where& of = at[half][i / GROUP];
-          scores[mt][half * 4 + i] = __builtin_fmaf(a[i] * of.ks, qc[mt], of.lv);
+          scores[mt][half * 4 + i] = __builtin_fmaf(a[i], fminf(of.ks * qc[mt], kMost), of.lv);
         }
       }
     }

@@ -93,6 +93,50 @@ def test_every_code_rounds_to_nearest_even(fmt):
     u.same_cache(g, c)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+def test_load_every_code_at_the_ends_of_fp32(fmt):
+    """Products that are subnormal, vanish, or lie next to the largest bf16."""
+    scales = np.float32([0.0, 2.0 ** -149, 2.0 ** -140, 2.0 ** -130, 2.0 ** -126, 1.37 * 2.0 ** -126,
+                         2.0 ** -100, 1.0, 2.0 ** 118, 1.3 * 2.0 ** 118])
+    B, d, bs = scales.size, 64, 8
+    c = u.random_cache(44, B, 1, d, bs, [4] * B, fmt, poison=False)
+    codes = np.array([x for x in range(256) if x & 0x7F != (0x7F if fmt == oq.E4M3 else -1)], np.uint8)
+    for b in range(B):
+        page = c.table[b, 0]
+        c.k[page, 0, :4].reshape(-1)[: codes.size] = codes
+        c.v[page] = c.k[page]
+        c.ks[page] = c.vs[page] = scales[b]
+    gk, gv = kvc.q8_load(u.to_gpu(c), 6)
+    rk, rv = oq.load(c, 6)
+    np.testing.assert_array_equal(gk.view(torch.int16).cpu().numpy().view(np.uint16), rk)
+    np.testing.assert_array_equal(gv.view(torch.int16).cpu().numpy().view(np.uint16), rv)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+def test_append_to_pages_of_extreme_scales(fmt):
+    """Earlier rows under scales from 0 over subnormal ones to 2^100, new rows from
+    zero to the largest bf16: the earlier rows' codes and the scales."""
+    scales = np.float32([0.0, 2.0 ** -149, 2.0 ** -126, 2.0 ** -30, 1.0, 0.7, 2.0 ** 60, 2.0 ** 100])
+    tops = [0x0000, 0x0001, 0x0080, 0x3F80, 0x3F81, 0x7F7F]      # bf16 bits
+    B, d, bs, W = scales.size * len(tops), 64, 16, 2
+    lens = [9] * B
+    c = u.random_cache(45, B, 1, d, bs, lens, fmt, poison=False)
+    k = u.random_rows(46, B, W, d)
+    f = u.synth.bf16_bits_to_f32(k)
+    f /= np.abs(f).max((1, 2), keepdims=True)
+    for b in range(B):
+        c.ks[c.table[b, 0]] = c.vs[c.table[b, 0]] = scales[b // len(tops)]
+        top = u.synth.bf16_bits_to_f32(np.array([tops[b % len(tops)]], np.uint16))[0]
+        k[b] = u.synth.f32_to_bf16_bits((f[b] * top).astype(np.float32))
+    v = k[:, ::-1].copy()
+    g = u.to_gpu(c)
+    for _ in range(2):
+        kvc.q8_append(g, u.dev_bf16(k), u.dev_bf16(v))
+    oq.append(c, k, v)
+    torch.cuda.synchronize()
+    u.same_cache(g, c)
+
+
 APPEND = [
     # B, H, d, bs, lengths after, W
     (4, 2, 128, 16, [1, 16, 17, 40], 1),
@@ -226,6 +270,22 @@ def test_attend_values_at_the_ends_of_fp32(power, fmt):
     c.vs[c.table[0, : 768 // bs]] *= np.float32(2.0 ** (60 if power < 0 else -60))
     out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(q), want_lse=True)
     torch.cuda.synchronize()
+    u.check_attention(c, q, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("power", [-110, -60, 60, 110])
+def test_attend_keys_at_the_ends_of_fp32(power, fmt):
+    """Keys of 2^power under queries of 2^-power: the scores of keys of one."""
+    B, H, G, W, d, bs = 1, 2, 5, 4, 64, 16
+    c = u.random_cache(47, B, H, d, bs, [900], fmt, poison=False)
+    q = u.random_rows(48, B * H, G, W, d)
+    far = u.synth.f32_to_bf16_bits((u.synth.bf16_bits_to_f32(q) * np.float32(2.0 ** -power)).astype(np.float32))
+    plain = c.ks.copy()
+    c.ks = (plain * np.float32(2.0 ** power)).astype(np.float32)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(far), want_lse=True)
+    torch.cuda.synchronize()
+    c.ks = plain
     u.check_attention(c, q, out, lse)
 
 
