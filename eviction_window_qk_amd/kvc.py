@@ -590,7 +590,18 @@ def _span(ws):
     return (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
 
 
-class Q8Cache:
+class _Handle:
+    """A C structure over tensors that were checked when it was made: another
+    tensor needs another handle."""
+
+    def __setattr__(self, name, value):
+        if "_ref" in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name}: a handle keeps its tensors, copy into "
+                                 "them or make a new one")
+        super().__setattr__(name, value)
+
+
+class Q8Cache(_Handle):
     """An 8-bit paged cache: k_pool, v_pool [n_blocks, kv_heads, block_size, d]
     (torch.float8_e4m3fn or torch.int8), k_scale, v_scale fp32 [n_blocks,
     kv_heads], table int32 [n_seqs, table_blocks], seq_len int32 [n_seqs].
@@ -618,7 +629,7 @@ class Q8Cache:
         self.k_pool, self.v_pool, self.k_scale, self.v_scale = k_pool, v_pool, k_scale, v_scale
         self.table, self.seq_len = table, seq_len
         self.heads, self.head_dim = B * H, d
-        self._c, self._ref, self._ws = c, ctypes.addressof(c), {}
+        self._c, self._ws, self._ref = c, {}, ctypes.addressof(c)
 
     def attend_workspace_bytes(self, group: int, window: int = 1) -> int:
         """Bytes q8_attend needs for `group` query heads and `window` queries."""
@@ -715,7 +726,7 @@ def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, sca
     return out if lse is None else (out, lse)
 
 
-class PageTable:
+class PageTable(_Handle):
     """Who owns which page: table int32 [n_seqs, table_blocks], seq_len int32
     [n_seqs], refs int32 [n_blocks], pages of block_size positions.  A handle
     like Q8Cache."""
@@ -733,7 +744,7 @@ class PageTable:
         self.device = dev
         self.table, self.seq_len, self.refs = table, seq_len, refs
         self.block_size, self.n_blocks = int(block_size), refs.shape[0]
-        self._c, self._ref, self._ws = c, ctypes.addressof(c), {}
+        self._c, self._ws, self._ref = c, {}, ctypes.addressof(c)
 
     def workspace_bytes(self, n_pairs: int = 0) -> int:
         """Bytes pages_alloc, pages_fork (n_pairs pairs) and pages_compact need."""
@@ -746,12 +757,12 @@ class PageTable:
         return n
 
 
-class PageBuffers:
+class PageBuffers(_Handle):
     """Tensors indexed by page in their first dimension (pools, scales): what a
     page id stands for in every one of them."""
 
     def __init__(self, tensors):
-        self.tensors = list(tensors)
+        self.tensors = tuple(tensors)
         self._c = (_CPageBuffer * max(1, len(self.tensors)))()
         self.n_blocks = self.tensors[0].shape[0] if self.tensors else 0
         self.device = self.tensors[0].device if self.tensors else None

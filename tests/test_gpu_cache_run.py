@@ -269,6 +269,31 @@ def test_two_streams_and_two_threads():
         assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+def test_two_graphs_replayed_at_once():
+    """Two captured steps over one cache, each with workspaces of its own, on two
+    streams."""
+    g = u.to_gpu(_cache(18, [5000, 1200, 77]))
+    qs = [u.dev_bf16(u.random_rows(19 + i, 6, 4, 1 + i, 128)) for i in range(2)]
+    want = [kvc.q8_attend(g, q, want_lse=True) for q in qs]
+    torch.cuda.synchronize()
+    graphs, got = [torch.cuda.CUDAGraph() for _ in qs], []
+    for graph, q in zip(graphs, qs):
+        with torch.cuda.graph(graph):
+            got.append(kvc.q8_attend(g, q, want_lse=True))
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(4):
+        for a in got:
+            a[0].zero_(), a[1].zero_()
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
+
+
 def test_lengths_out_of_range_are_clamped():
     c = _cache(11, [20, 64, 5])
     c.lens = np.array([-7, 1000, 2 ** 31 - 1], np.int32)
@@ -303,6 +328,19 @@ def test_given_outputs_and_workspace_are_used():
         kvc.q8_attend(g, q.float())
     with pytest.raises(kvc.KvcError):
         kvc.q8_attend(g, q, out=q)
+
+
+def test_handles_keep_their_tensors():
+    """Another table has to come with another handle: set on the old one, it would
+    not be what the calls read."""
+    c = _cache(17, [40, 3])
+    g = u.to_gpu(c)
+    pages = kvc.PageTable(g.table, g.seq_len, torch.ones(c.n, dtype=torch.int32, device="cuda"), 16)
+    bufs = kvc.PageBuffers([g.k_pool, g.v_pool])
+    out = kvc.pages_compact(pages, bufs)
+    for handle, name in ((g, "table"), (g, "k_scale"), (pages, "table"), (pages, "refs"), (bufs, "tensors")):
+        with pytest.raises(AttributeError, match="new one"):
+            setattr(handle, name, out["table"])
 
 
 def test_seeded_sweep():
