@@ -539,8 +539,13 @@ void attend_rows(const Args& A, hipStream_t s) {
   // heads of 2048 keys, 30 against 32 on 8 heads of 65536; on pools of 70 MB, found
   // there again by the next call, 22.2 against 20.8.
   const bool stream = uint64_t(A.c.n_blocks) * A.c.H * A.c.bs * D * 2 > (uint64_t(96) << 20);
-  if (A.R <= 16) {
-    if (fours && stream) attend<D, FMT, 1, 4, true>(A, s);
+  // Rows by 16 a workgroup where the last one of 32 would be half empty: 40 rows on
+  // 128 heads of 4096 keys take 67 us by 16 and 75 by 32 (D = 64: 40 and 42), 72 rows
+  // 99 and 104 (59 and 57), 104 rows 134 and 137 (79 and 72).  An even number of
+  // 16s is as fast or faster by 32 (32 rows: 52 and 51).
+  const int n = (A.R + 15) / 16;
+  if (n % 2 == 1 && n <= (D == 128 ? 7 : 3)) {
+    if (fours && stream && n == 1) attend<D, FMT, 1, 4, true>(A, s);
     else if (fours) attend<D, FMT, 1, 4, false>(A, s);
     else attend<D, FMT, 1, 1, false>(A, s);
   } else {

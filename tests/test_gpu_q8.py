@@ -198,6 +198,11 @@ ATTEND = [
     (3, 1, 2, 2, 128, 16, [50, 60, 70], 1.0),
     (1, 1, 3, 1, 128, 128, [16500], 0.0),
     (1, 1, 2, 1, 64, 48, [140001], 0.02),
+    (2, 2, 8, 5, 128, 16, [700, 41], 0.1),
+    (2, 1, 11, 3, 64, 24, [1500, 3], 0.0),
+    (1, 2, 6, 8, 64, 7, [900], 0.1),
+    (1, 1, 16, 7, 128, 33, [1300], 0.0),
+    (1, 2, 9, 8, 128, 16, [2000], 0.0),
 ]
 
 
