@@ -5,14 +5,15 @@
 //   x = c * ks * <q, code_k> + log2 r,  w = 2^(x - m),
 //   l = sum w / r,  out = top * sum w * code_v / l
 // with c = scale * log2(e), ks and vs the page scales, top the largest vs among
-// the keys that a workgroup takes and r = vs / top, m a running maximum of x.  Each cached byte is read once for all R rows; with the few rows of a
+// the keys that a workgroup takes and r = vs / top, m within kSlack below the
+// running maximum of x.  Each cached byte is read once for all R rows; with the few rows of a
 // decode step the bound is HBM: 2*d bytes per key.
 //
 // Both products run on fp16 matrix instructions, 16x16x32: e4m3 and int8 codes
 // are exact in fp16, so is a bf16 query scaled by a power of two (elements
 // below 2^-29 of the row's largest lose bits), and the weights keep 11 bits.
 // A weight carries its page's value scale inside the exponent, so one exp2 a
-// score gives a number in (0, 1] whatever the scales are; the denominator
+// score gives a number in (0, 64] whatever the scales are; the denominator
 // takes the scale out again, in fp32.  The scale is taken relative to the
 // largest of the workgroup's keys: hundreds of zero values (scale 2^-126) weigh
 // in the denominator as much as any others, and 2^126 each would overflow it.
@@ -58,6 +59,10 @@ struct __align__(16) Where {
   float ks, lv, iv;
 };
 
+// How far a score may pass its row's m before m and the sums follow: the weights
+// stay below 2^6, fp16 as exact as below 1, and the sums are scaled once or twice a
+// row and wave, not at every new maximum (20 rows on ragged drafts 57.6 us, 55.2 so).
+constexpr float kSlack = 6.0f;
 constexpr float kMost = 0x1.fffffep127f;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
@@ -75,6 +80,17 @@ struct Args {
   float* part;  // [n][row][piece][D] outputs of a piece
   float* stat;  // [n][row][piece][2] their m, l
 };
+
+// Largest of eight.  (Written with fmaxf it is eleven instructions: each operand
+// that a branch may have changed is quieted first.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float x;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(x) : "v"(a), "v"(b), "v"(c));
+  return x;
+}
+__device__ __forceinline__ float max8(const float (&y)[8]) {
+  return max3(max3(y[0], y[1], y[2]), max3(y[3], y[4], y[5]), max3(y[6], y[7], y[7]));
+}
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -149,8 +165,14 @@ __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim
 // registers for 120 and ran at three waves, 10 % slower on ragged drafts.  32 rows
 // at D = 128 need the registers of two waves (at three they spill: 146 us
 // became 269 on 128 heads of 16384 keys).
+// Look-ups of single keys take up to ten registers more: asked for four waves the
+// compiler spills some of them where it needs none for three (and four fit).
+constexpr int waves(int D, int FMT, int MT, int GROUP) {
+  if (D == 128 && MT == 2) return 2;
+  return GROUP == 1 && (D == 128 || (MT == 2 && FMT == KVC_Q8_INT8)) ? 3 : 4;
+}
 template <int D, int FMT, int MT, int GROUP, bool STREAM>
-__global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 3 : 4) void k_q8_attend(Args A) {
+__global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_attend(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
   constexpr int kVWords = D / 64;       // words of one key's values in a lane
@@ -281,7 +303,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
   f16x8 qf[MT][kSteps];
   float qc[MT];
   int last[MT];  // last key this row attends to
-  float m[MT], l[MT];
+  float base[MT], most[MT], l[MT];  // most: -inf until the row has a base
   f32x4 acc[MT][kTiles];
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
@@ -311,7 +333,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
         qf[mt][s][2 * i + 1] = _Float16(__uint_as_float(raw[mt][s][i] & 0xffff0000u) * mul);
       }
     last[mt] = r < A.R ? len - A.W + (r - int(quot(A.by_W, uint32_t(r))) * A.W) - t0 : 0x7ffffffe;  // rows that are none: see all
-    m[mt] = -INFINITY;
+    base[mt] = 0.0f;
+    most[mt] = -INFINITY;
     l[mt] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) acc[mt][i] = f32x4{0, 0, 0, 0};
@@ -346,7 +369,8 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const Where& of = at[half][i / GROUP];
-          scores[mt][half * 4 + i] = __builtin_fmaf(a[i], fminf(of.ks * qc[mt], kMost), of.lv);
+          scores[mt][half * 4 + i] =
+              __builtin_fmaf(a[i], fminf(of.ks * qc[mt], kMost), of.lv - base[mt]);
         }
       }
     }
@@ -363,27 +387,34 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
           if (t >= keys || none) x.v[j][u] = 0;
       }
     }
+    // look-ups of single keys: the eight reciprocals come from LDS now, not with
+    // the scales above (they would not fit the registers beside them)
+    int later = tile + 4 * g;
+    if constexpr (GROUP == 1) asm("" : "+v"(later));
     f16x8 w[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float(&y)[8] = scores[mt];
-      float top = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])),
-                        fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])));
-      if (__any(top > m[mt])) {
+      float(&y)[8] = scores[mt];
+      float top = max8(y);
+      if (__any(top > most[mt])) {
 #pragma unroll
         for (int off = 16; off <= 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-        const float now = fmaxf(m[mt], top);
-        const float f = now == -INFINITY ? 1.0f : fast_exp2(m[mt] - now);
+        const float up = top > most[mt] ? top : 0.0f;
+        const float f = most[mt] == -INFINITY ? 1.0f : fast_exp2(-up);
         l[mt] *= f;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f;
-        m[mt] = now;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] -= up;
+        base[mt] += up;
+        most[mt] = top > most[mt] ? kSlack : most[mt];
       }
-      const float base = m[mt] == -INFINITY ? 0.0f : m[mt];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float e = fast_exp2(y[j] - base);
-        l[mt] = __builtin_fmaf(e, at[j >> 2][(j & 3) / GROUP].iv, l[mt]);
+        const float e = fast_exp2(y[j]);
+        const float iv = GROUP == 1 ? where[later + (j >> 2) * 16 + (j & 3)].iv
+                                    : at[j >> 2][(j & 3) / GROUP].iv;
+        l[mt] = __builtin_fmaf(e, iv, l[mt]);
         w[mt][j] = _Float16(e);
       }
     }
@@ -421,7 +452,7 @@ __global__ __launch_bounds__(kThreads, D == 64 ? 4 : MT == 2 ? 2 : GROUP == 1 ? 
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
       if (g == 0) {
-        to[D] = m[mt];
+        to[D] = most[mt] == -INFINITY ? -INFINITY : base[mt];
         to[D + 1] = l[mt];
       }
     }

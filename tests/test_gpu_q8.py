@@ -309,6 +309,52 @@ def test_attend_query_range():
     u.check_attention(c, q, out, lse)
 
 
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("G,W,d", [(4, 1, 128), (5, 4, 64), (3, 8, 128), (8, 5, 128)])
+def test_attend_rows_do_not_mix(G, W, d, fmt):
+    """A query of NaN or infinity gives NaN in its own row; the other rows have the
+    bits they have beside a query of zeros, and beside one of large scores."""
+    c = u.random_cache(49, 2, 2, d, 16, [700, 19], fmt, holes=0.1)
+    g = u.to_gpu(c)
+    q = u.dev_bf16(u.random_rows(50, 4, G, W, d))
+    row = (slice(None), G - 2, W - 1)
+    got = []
+    for fill in (0.0, 30.0, float("nan"), float("inf")):
+        x = q.clone()
+        x[row] = x[row] * fill if fill == 30.0 else fill
+        got.append(kvc.q8_attend(g, x, want_lse=True))
+    torch.cuda.synchronize()
+    others = torch.ones((4, G, W), dtype=torch.bool, device="cuda")
+    others[row] = False
+    for out, lse in got[1:]:
+        assert torch.equal(out[others].view(torch.int16), got[0][0][others].view(torch.int16))
+        assert torch.equal(lse[others], got[0][1][others])
+    assert torch.isfinite(got[1][0]).all()
+    assert torch.isnan(got[2][0][row]).all() and torch.isnan(got[3][0][row]).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("step", [0.004, 0.05, -0.05, 1.0])
+def test_attend_scores_that_rise_and_fall(step, fmt):
+    """Scores that grow or fall by `step` a key: maxima that move a little, a lot,
+    and at every tile."""
+    B, H, G, W, d, bs, L = 1, 1, 3, 2, 64, 16, 1300
+    c = u.random_cache(51, B, H, d, bs, [L], fmt, poison=False)
+    q = np.zeros((1, G, W, d), np.float32)
+    q[..., 0] = 1.0                                     # the score is the key's first value
+    q[..., 1:] = 0.01 * u.rng_of(52).normal(size=q[..., 1:].shape)
+    pages = c.table[0]
+    one = 0x38 if fmt == oq.E4M3 else 1                 # the code of 1
+    c.k[pages] = 0
+    c.k[pages, 0, :, 0] = one
+    at = np.arange(pages.size) * bs * abs(step) * 8.0 / max(1.0, abs(step) * 8.0 * L / 2000.0)
+    c.ks[pages, 0] = (at if step > 0 else at[::-1]).astype(np.float32)
+    bits = u.synth.f32_to_bf16_bits(q)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(bits), want_lse=True)
+    torch.cuda.synchronize()
+    u.check_attention(c, bits, out, lse)
+
+
 def test_max_len_bounds_the_length():
     c = u.random_cache(18, 2, 2, 64, 16, [300, 40], oq.INT8, poison=False)
     g = u.to_gpu(c, max_len=100)
