@@ -12,13 +12,14 @@
 namespace kvc {
 namespace {
 
-// Makes the device of `stream` current for the launches of a call (the NULL
-// stream is the current device's already).
+// Makes the device of `stream` current for the launches of a call.  The implicit
+// streams are the current device's already, and their handles no objects that the
+// runtime could be asked about.
 struct OnDeviceOf {
   int was = -1;
   bool ok = true;
   explicit OnDeviceOf(hipStream_t stream) {
-    if (stream == nullptr) return;
+    if (stream == nullptr || stream == hipStreamPerThread) return;
     int cur = -1, dev = -1;
     ok = hipGetDevice(&cur) == hipSuccess && hipStreamGetDevice(stream, &dev) == hipSuccess;
     if (ok && cur != dev) {
@@ -33,7 +34,7 @@ struct OnDeviceOf {
 
 template <class F>
 int launch_on(void* stream, F launch) {
-  const hipStream_t s = hipStream_t(stream);
+  const hipStream_t s = hipStream_t(stream) == hipStreamLegacy ? nullptr : hipStream_t(stream);
   OnDeviceOf dev(s);
   return dev.ok ? launch_status(launch(s)) : KVC_EDEVICE;
 }

@@ -269,6 +269,28 @@ def test_two_streams_and_two_threads():
         assert torch.equal(a[0].view(torch.int16), b[0].view(torch.int16)) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("handle", [0, 1, 2], ids=["null", "legacy", "per_thread"])
+def test_implicit_streams_of_the_c_entries(handle):
+    """The runtime's implicit streams: their handles are numbers, not objects."""
+    c = _cache(20, [700, 20])
+    g = u.to_gpu(c)
+    q = u.dev_bf16(u.random_rows(21, 4, 4, 1, 128))
+    want = kvc.q8_attend(g, q)
+    out, ws = torch.zeros_like(q), torch.empty(g.attend_workspace_bytes(4), dtype=torch.uint8, device="cuda")
+    refs = torch.zeros(c.n, dtype=torch.int32, device="cuda")
+    pages = kvc.PageTable(torch.full((2, 3), -1, dtype=torch.int32, device="cuda"), g.seq_len, refs, 16)
+    lens = torch.tensor([33, 5], dtype=torch.int32, device="cuda")
+    status, pws = torch.full_like(lens, 7), torch.empty(pages.workspace_bytes(), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    print(f"[case] stream handle {handle}", flush=True)
+    L = kvc.lib()
+    assert L.kvc_q8_attend(g._ref, 4, 1, 0.0, q.data_ptr(), out.data_ptr(), None, ws.data_ptr(), ws.numel(), handle) == 0
+    assert L.kvc_pages_alloc(pages._ref, lens.data_ptr(), status.data_ptr(), pws.data_ptr(), pws.numel(), handle) == 0
+    torch.cuda.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    assert status.tolist() == [0, 0] and pages.table.tolist() == [[0, 1, 2], [3, -1, -1]]
+
+
 def test_two_graphs_replayed_at_once():
     """Two captured steps over one cache, each with workspaces of its own, on two
     streams."""
