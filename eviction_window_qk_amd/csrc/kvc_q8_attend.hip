@@ -15,8 +15,9 @@
 // A weight carries its page's value scale inside the exponent, so one exp2 a
 // score gives a number in (0, 64] whatever the scales are; the denominator
 // takes the scale out again, in fp32.  The scale is taken relative to the
-// largest of the workgroup's keys: hundreds of zero values (scale 2^-126) weigh
-// in the denominator as much as any others, and 2^126 each would overflow it.
+// largest of the workgroup's keys, and is at least kQuiet: hundreds of zero values
+// (scale 2^-126) weigh in the denominator as much as any others, and 2^126 each
+// would overflow it.
 //
 // Both products are taken transposed, S' = K Q' and O' = V' P': the lane that
 // holds eight scores of a query row (keys 4g..4g+3 of two 16-key tiles, g its
@@ -64,6 +65,15 @@ struct __align__(16) Where {
 // row and wave, not at every new maximum (20 rows on ragged drafts 57.6 us, 55.2 so).
 constexpr float kSlack = 6.0f;
 constexpr float kMost = 0x1.fffffep127f;
+// A value scale further than kQuiet below the piece's largest (an empty page's)
+// counts as kQuiet of it.  The denominator is held in units of kUnit: a key adds
+// 1 / kUnit to 2^6 / (kUnit kQuiet) = 2^58, so a row that sees quiet keys only
+// stays below 2^88 over the 2^30 keys of the longest table.  Sums are scaled by the
+// square root of a power of two, twice: in one step the factor would vanish at
+// 2^-126 before a quiet key's sum does.  The exp2 of a key vanishes there, and
+// takes at most 2^-26 of the row's sum with it.
+constexpr float kQuiet = 0x1p-100f;
+constexpr float kUnit = 0x1p48f;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 
 struct Args {
@@ -149,13 +159,18 @@ __device__ __forceinline__ float block_max(float x, float* sh) {
   return x;
 }
 
-// Four output values of a row, and its sum of weights l relative to 2^m.
+// log2 of a sum in kUnit: multiplied first, an ordinary sum loses no bits to the 48.
+__device__ __forceinline__ float log2_sum(float l) {
+  return l < 1.0f ? __builtin_amdgcn_logf(l * kUnit) : __builtin_amdgcn_logf(l) + 48.0f;
+}
+
+// Four output values of a row, and its sum of weights l (in kUnit) relative to 2^m.
 __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim, f32x4 out,
                                        float l, float m) {
   *reinterpret_cast<u16x4*>(A.out + row * D + dim) =
       u16x4{to_bf16(out.x), to_bf16(out.y), to_bf16(out.z), to_bf16(out.w)};
   if (A.lse && dim == 0)
-    A.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    A.lse[row] = l == 0.0f ? -INFINITY : (m + log2_sum(l)) * 0.6931471805599453f;
 }
 
 // Four waves a SIMD: a tile of each in flight covers the latency of HBM, and
@@ -290,13 +305,11 @@ __global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_atten
   }
   vtop = fmaxf(block_max(vtop, top_of), 0x1p-126f);
   vtop = __uint_as_float(uint32_t(__builtin_amdgcn_readfirstlane(int(__float_as_uint(vtop)))));
-  // A value scale more than 2^40 below the piece's largest (an empty page's)
-  // counts as that far below it: the weights span fp32, not more.
   const float by_top = 1.0f / vtop;
   for (int i = tid; i < lookups; i += kThreads) {
-    const float r = fmaxf(where[i].iv * by_top, 0x1p-40f);
+    const float r = fmaxf(where[i].iv * by_top, kQuiet);
     if (where[i].lv == 0.0f) where[i].lv = __builtin_amdgcn_logf(r);
-    where[i].iv = __builtin_amdgcn_rcpf(r);
+    where[i].iv = __builtin_amdgcn_rcpf(r * kUnit);
   }
 
   // Queries to fp16 fragments of rows scaled by a power of two.
@@ -400,10 +413,10 @@ __global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_atten
 #pragma unroll
         for (int off = 16; off <= 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
         const float up = top > most[mt] ? top : 0.0f;
-        const float f = most[mt] == -INFINITY ? 1.0f : fast_exp2(-up);
-        l[mt] *= f;
+        const float f = most[mt] == -INFINITY ? 1.0f : fast_exp2(-0.5f * up);
+        l[mt] = l[mt] * f * f;
 #pragma unroll
-        for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f;
+        for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f * f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] -= up;
         base[mt] += up;
@@ -469,11 +482,11 @@ __global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_atten
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float* aw = at + w * A.lds_rows * kRowF;
-        const float f = fast_exp2(aw[D] - base);
-        sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
-        L += aw[D + 1] * f;
+        const float f = fast_exp2(0.5f * (aw[D] - base));
+        sum += *reinterpret_cast<const f32x4*>(aw + dim) * (f * f);
+        L += aw[D + 1] * f * f;
       }
-      sum = L == 0.0f ? f32x4{0, 0, 0, 0} : sum * __builtin_amdgcn_rcpf(L) * vtop;
+      sum = L == 0.0f ? f32x4{0, 0, 0, 0} : sum * (1.0f / kUnit) * __builtin_amdgcn_rcpf(L) * vtop;
       const size_t row = size_t(n) * A.R + r0 + r;
       if (alone) {
         finish(A, row, D, dim, sum, L, base);
@@ -510,9 +523,11 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
   const float base = M == -INFINITY ? 0.0f : M;
-  float L = ml.y * fast_exp2(ml.x - base);
-  for (int p = lane + 64; p < pieces; p += 64)
-    L = __builtin_fmaf(st[p].y, fast_exp2(st[p].x - base), L);
+  float f = fast_exp2(0.5f * (ml.x - base)), L = ml.y * f * f;
+  for (int p = lane + 64; p < pieces; p += 64) {
+    f = fast_exp2(0.5f * (st[p].x - base));
+    L = __builtin_fmaf(st[p].y * f, f, L);
+  }
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off);
   const float by_L = L == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(L);
@@ -521,7 +536,8 @@ __global__ __launch_bounds__(kThreads) void k_q8_join(Args A) {
   for (int p = group; p < pieces; p += kAtOnce) {
     const f32x4 x = *reinterpret_cast<const f32x4*>(part + size_t(p) * D);
     const f32x2 w = st[p];
-    sum += x * (w.y * fast_exp2(w.x - base) * by_L);
+    const float f = fast_exp2(0.5f * (w.x - base));
+    sum += x * (w.y * f * f * by_L);
   }
   *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
   __syncthreads();
