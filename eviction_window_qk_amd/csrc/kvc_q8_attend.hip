@@ -5,15 +5,17 @@
 //   x = c * ks * <q, code_k> + log2 r,  w = 2^(x - m),
 //   l = sum w / r,  out = top * sum w * code_v / l
 // with c = scale * log2(e), ks and vs the page scales, top the largest vs among
-// the keys that a workgroup takes and r = vs / top, m within kSlack below the
-// running maximum of x.  Each cached byte is read once for all R rows; with the few rows of a
+// the keys that a workgroup takes and r = vs / top, m kHead to kHead + kSlack below
+// the running maximum of x.  Each cached byte is read once for all R rows; with the few rows of a
 // decode step the bound is HBM: 2*d bytes per key.
 //
 // Both products run on fp16 matrix instructions, 16x16x32: e4m3 and int8 codes
 // are exact in fp16, so is a bf16 query scaled by a power of two (elements
-// below 2^-29 of the row's largest lose bits), and the weights keep 11 bits.
+// below 2^-29 of the row's largest lose bits), and the weights keep 11 bits down to
+// 2^-23 of the row's largest, below that a step of 2^-33 of it (bf16 outputs
+// need 9).
 // A weight carries its page's value scale inside the exponent, so one exp2 a
-// score gives a number in (0, 64] whatever the scales are; the denominator
+// score gives a number in (0, 2^15] whatever the scales are; the denominator
 // takes the scale out again, in fp32.  The scale is taken relative to the
 // largest of the workgroup's keys, and is at least kQuiet: hundreds of zero values
 // (scale 2^-126) weigh in the denominator as much as any others, and 2^126 each
@@ -60,18 +62,20 @@ struct __align__(16) Where {
   float ks, lv, iv;
 };
 
-// How far a score may pass its row's m before m and the sums follow: the weights
-// stay below 2^6, fp16 as exact as below 1, and the sums are scaled once or twice a
-// row and wave, not at every new maximum (20 rows on ragged drafts 57.6 us, 55.2 so).
-constexpr float kSlack = 6.0f;
+// m is set kHead below a row's maximum, and follows once a score is kSlack past that
+// maximum: the sums are scaled once or twice a row and wave, not at every new
+// maximum (20 rows on ragged drafts 57.6 us, 55.2 so).  Weights reach 2^15, fp16's
+// last binade, so that they are whole down to 2^-23 of the largest (2^-14 with m at
+// the maximum), where fp16 turns subnormal.
+constexpr float kSlack = 6.0f, kHead = 9.0f;
 constexpr float kMost = 0x1.fffffep127f;
 // A value scale further than kQuiet below the piece's largest (an empty page's)
-// counts as kQuiet of it.  The denominator is held in units of kUnit: a key adds
-// 1 / kUnit to 2^6 / (kUnit kQuiet) = 2^58, so a row that sees quiet keys only
-// stays below 2^88 over the 2^30 keys of the longest table.  Sums are scaled by the
+// counts as kQuiet of it.  The denominator is held in units of kUnit: a key adds at
+// most 2^15 / (kUnit kQuiet) = 2^67, so a row that sees quiet keys only stays below
+// 2^97 over the 2^30 keys of the longest table.  Sums are scaled by the
 // square root of a power of two, twice: in one step the factor would vanish at
 // 2^-126 before a quiet key's sum does.  The exp2 of a key vanishes there, and
-// takes at most 2^-26 of the row's sum with it.
+// takes at most 2^-35 of the row's sum with it.
 constexpr float kQuiet = 0x1p-100f;
 constexpr float kUnit = 0x1p48f;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
@@ -412,7 +416,7 @@ __global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_atten
       if (__any(top > most[mt])) {
 #pragma unroll
         for (int off = 16; off <= 32; off <<= 1) top = fmaxf(top, __shfl_xor(top, off));
-        const float up = top > most[mt] ? top : 0.0f;
+        const float up = top > most[mt] ? top - kHead : 0.0f;
         const float f = most[mt] == -INFINITY ? 1.0f : fast_exp2(-0.5f * up);
         l[mt] = l[mt] * f * f;
 #pragma unroll
@@ -420,7 +424,7 @@ __global__ __launch_bounds__(kThreads, waves(D, FMT, MT, GROUP)) void k_q8_atten
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] -= up;
         base[mt] += up;
-        most[mt] = top > most[mt] ? kSlack : most[mt];
+        most[mt] = top > most[mt] ? kHead + kSlack : most[mt];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {

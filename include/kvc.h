@@ -394,12 +394,18 @@ int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const int32_t* n_new, c
 /* Attention of the last `window` positions' queries over the cache.  q, out:
  * bf16 [n_seqs * kv_heads][group][window][d] (the layout of q_win); query w
  * sits at position seq_len - window + w and attends to the positions up to
- * its own:  out = sum_t softmax_t(scale * <q, k[t]>) * v[t], in fp32 (the
- * weights enter the matrix products as fp16; a value scale more than 2^100
- * below the largest among the same piece of at most 2048 keys counts as 2^-100
- * of it, too large where a query attends to nothing louder).  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.  lse: optional f32 [n_seqs * kv_heads][group][window],
- * log(sum_t exp(scale * <q, k[t]>)).  A query that attends to nothing gives
- * zeros and lse = -inf.  group 1..64, window >= 1, group * window <= 4096.
+ * its own:  out = sum_t softmax_t(scale * <q, k[t]>) * v[t], in fp32, lse:
+ * optional f32 [n_seqs * kv_heads][group][window], log(sum_t exp(scale *
+ * <q, k[t]>)).  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.  A query
+ * that attends to nothing gives zeros and lse = -inf.  Held in fewer bits: a
+ * query element below 2^-29 of its row's largest loses some; a key's weight *
+ * value scale enters the product with the codes as fp16, 11 bits down to 2^-23 of
+ * the row's largest and within 2^-34 of that largest below (the sum of the weights
+ * is fp32); a value scale more than 2^100 below the largest among the same piece
+ * of at most 2048 keys, attended to or not, counts as 2^-100 of it, too large
+ * where a query attends to nothing louder.  Otherwise keys that a query does not
+ * attend to change its roundings at most.
+ * group 1..64, window >= 1, group * window <= 4096.
  * A head's results depend on its own length, queries and pages alone.
  * ws: at least kvc_q8_attend_workspace_bytes(c, group, window), 256-byte
  * aligned (may be NULL when that is 0). */

@@ -96,3 +96,22 @@ def test_a_loud_key_among_many_quiet_ones(loud_score, fmt):
     out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(bits), want_lse=True)
     torch.cuda.synchronize()
     check(c, bits, out, lse, 2.0 ** -25, 98)
+
+
+@pytest.mark.parametrize("fmt", FMTS, ids=["e4m3", "int8"])
+@pytest.mark.parametrize("bs", [1, 12])
+@pytest.mark.parametrize("apart", [16, 26, 30])
+def test_quiet_values_beside_loud_keys_of_the_same_score(apart, bs, fmt):
+    """Two pages of equal scores, one 2^-apart as loud as the other, whose codes are zero
+    in every other dimension: there the outputs are the quiet page's values, with
+    11 bits down to 2^-23 of the loud ones and within 2^-34 of those below."""
+    H, G, W, d = 2, 2, 1, 64
+    c = u.random_cache(64, 1, H, d, bs, [2 * bs], fmt, poison=False)
+    loud, quiet = c.table[0]
+    c.v[loud, :, :, ::2] = 0
+    c.vs[quiet] = np.float32(1.37)
+    c.vs[loud] = np.float32(1.11 * 2.0 ** apart)
+    bits = np.zeros((H, G, W, d), np.uint16)
+    out, lse = kvc.q8_attend(u.to_gpu(c), u.dev_bf16(bits), want_lse=True)
+    torch.cuda.synchronize()
+    check(c, bits, out, lse, 2.0 ** -34, apart + 1)
