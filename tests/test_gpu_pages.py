@@ -208,3 +208,45 @@ def test_many_buffers_and_holes():
     np.testing.assert_array_equal(got["refs"].cpu().numpy(), refs)
     assert int(got["n_live"][0]) == live
     _check_copies(tensors, before, copies)
+
+
+@pytest.mark.parametrize("n_bufs", [5, 64, 65, 300])
+def test_buffers_side_by_side(n_bufs):
+    """Buffers in any order without a byte between them, the ids and the page table among
+    them: forked, copied and compacted like buffers of their own."""
+    B, tb, bs, n = 6, 4, 8, 20
+    t = u.random_pages(20, B, tb, bs, n, fill=1.0)
+    rng = u.rng_of(21, n_bufs)
+    widths = [int(w) * 4 for w in rng.integers(1, 40, n_bufs)]
+    pieces = [n * w for w in widths] + [B * tb * 4, B * 4, n * 4, 4 * 4, 4 * 4]   # table, lengths, counts, src, dst
+    slab = torch.from_numpy(rng.integers(0, 256, sum(pieces)).astype(np.uint8)).cuda()
+    place, at = {}, 0
+    for i in rng.permutation(len(pieces)):
+        place[int(i)] = slab[at:at + pieces[i]]
+        at += pieces[i]
+    tensors = [place[i].view(n, widths[i]) for i in range(n_bufs)]
+    table, lens, refs, src, dst = (place[n_bufs + i].view(torch.int32) for i in range(5))
+    table = table.view(B, tb)
+    for to, x in ((table, t.table), (lens, t.lens), (refs, t.refs), (src, [0, 1, 2, 3]), (dst, [4, 5, 4, 9])):
+        to.copy_(torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)))
+    g, bufs = kvc.PageTable(table, lens, refs, bs), kvc.PageBuffers(tensors)
+    before = _host(tensors)
+    st = kvc.pages_fork(g, src, dst, bufs)
+    ref, copies = op.fork(t, [0, 1, 2, 3], [4, 5, 4, 9])
+    assert st.cpu().numpy().tolist() == ref.tolist()
+    u.same_pages(g, t)
+    _check_copies(tensors, before, copies)
+    src.copy_(torch.tensor([0, 5, 99, 2]))
+    dst.copy_(torch.tensor([19, 18, 1, -1]))
+    before = _host(tensors)
+    kvc.pages_copy(src, dst, bufs)
+    _check_copies(tensors, before, [(0, 19), (5, 18)])
+    kvc.pages_free(g, torch.tensor([1], dtype=torch.int32, device="cuda"))
+    op.release(t, [1])
+    before = _host(tensors)
+    out = kvc.pages_compact(g, bufs)
+    new_table, new_refs, remap, live, moved = op.compact(t)
+    assert int(out["n_live"]) == live
+    np.testing.assert_array_equal(out["table"].cpu().numpy(), new_table)
+    np.testing.assert_array_equal(out["remap"].cpu().numpy(), remap)
+    _check_copies(tensors, before, moved)

@@ -283,3 +283,55 @@ def test_oracle_pages_by_hand():
     assert n == 3 and moved == [(4, 0)] and table.tolist() == [[-1, -1, -1], [2, 1, 0]]
     assert refs.tolist() == [1, 1, 1, 0, 0] and remap.tolist() == [-1, 1, 2, -1, 0]
     assert op.alloc(t, [12, 0]).tolist() == [1, 0]             # two free, three wanted
+
+
+# --- buffers of many layers -----------------------------------------------------
+
+def _copy_of(spans, n_blocks=16, src=FAKE, dst=FAKE + GB):
+    return kvc.lib().kvc_pages_copy(n_blocks, 1, src, dst, _bufs(*spans), len(spans), None)
+
+
+def _layers(n, seed, n_blocks=16):
+    """n buffers of different page sizes side by side, in random order."""
+    rng = np.random.default_rng(seed)
+    size = rng.integers(1, 5000, n)
+    gap = rng.integers(0, 2, n) * rng.integers(1, 100, n)
+    base = FAKE + 4 * GB + np.concatenate([[0], np.cumsum(size * n_blocks + gap)[:-1]])
+    order = rng.permutation(n)
+    return [(int(base[i]), int(size[i])) for i in order]
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where nothing can be launched")
+@pytest.mark.parametrize("n", [2, 3, 17, 128, 4096])
+def test_one_overlap_among_many_buffers(n):
+    """One byte of two buffers, one inside another, or an id array inside one: refused
+    wherever in the list they stand.  (Disjoint buffers would be launched: those
+    calls are in the GPU tests.)"""
+    for seed in range(6):
+        rng = np.random.default_rng([n, seed])
+        spans = _layers(n, seed)
+        i, j = (int(x) for x in rng.choice(n, 2, replace=False))
+        last = (spans[i][0] + spans[i][1] * 16 - 1, 1)         # 16 bytes from the last one of buffer i on
+        inside = (spans[i][0] + spans[i][1] * 16 // 2, 1)
+        same = spans[i]
+        for other in (last, inside, same):
+            bad = list(spans)
+            bad[j] = other
+            assert _copy_of(bad) == -1
+        assert _copy_of(spans, src=(spans[i][0] + spans[i][1] * 16 - 1) & ~3) == -1
+        assert _copy_of(spans, dst=spans[i][0] & ~3) == -1     # the word of its first byte
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="made-up addresses: only where nothing can be launched")
+def test_checking_many_buffers_is_quick():
+    """The check of 4096 buffers sorts them: comparing all pairs took 9 ms and more."""
+    import time
+    spans = _layers(4096, 1)
+    spans[-1] = (FAKE + 64, 16)                                # over the ids: refused by the last one
+    b = _bufs(*spans)
+    took = []
+    for _ in range(7):
+        t = time.perf_counter()
+        assert kvc.lib().kvc_pages_copy(16, 100, FAKE, FAKE + GB, b, len(spans), None) == -1
+        took.append(time.perf_counter() - t)
+    assert min(took) < 3e-3, took
