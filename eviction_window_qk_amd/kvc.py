@@ -135,8 +135,9 @@ class Params:
         return self.t_stride or self.T
 
 
-# The kvc_params layout and entry-point signatures this binding marshals
-# (KVC_ABI_VERSION in include/kvc.h); a library of another version is refused.
+# The struct layouts and entry-point signatures this binding marshals
+# (KVC_ABI_VERSION in include/kvc.h); a library of another version is refused, and
+# one of this version that lacks an entry point added since it was built.
 ABI_VERSION = 3
 
 _lib = None
@@ -187,17 +188,20 @@ def lib() -> ctypes.CDLL:
         "kvc_strerror": [ctypes.c_int],
         "kvc_abi_version": [],
     }
-    for name, args in sig.items():
+    rebuild = "rebuild with `python -m eviction_window_qk_amd.build`"
+    for name in ("kvc_abi_version", *sig):
+        if not hasattr(L, name):
+            raise RuntimeError(f"{LIB_PATH} has no {name}: {rebuild}")
         fn = getattr(L, name)
-        fn.argtypes = args
+        fn.argtypes = sig[name]
         fn.restype = ctypes.c_int
+        if name == "kvc_abi_version" and fn() != ABI_VERSION:   # before any other name
+            raise RuntimeError(f"{LIB_PATH} has ABI version {fn()}, this binding expects "
+                               f"{ABI_VERSION}: {rebuild}")
     for name in ("kvc_workspace_bytes", "kvc_q8_attend_workspace_bytes",
                  "kvc_pages_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.kvc_strerror.restype = ctypes.c_char_p
-    if L.kvc_abi_version() != ABI_VERSION:
-        raise RuntimeError(f"{LIB_PATH} has ABI version {L.kvc_abi_version()}, this binding "
-                           f"expects {ABI_VERSION}: rebuild with `python -m eviction_window_qk_amd.build`")
     _lib = L
     return L
 

@@ -273,3 +273,21 @@ def test_refresh_pieces_validation():
                                 a + (4 << 32), a + (5 << 32), 7, a + (6 << 32), None) == -2
     assert L.kvc_full_sync(4, 16, 128, a, a + (1 << 32), a + (2 << 32), -1, 100, a + (3 << 32),
                            a + (4 << 32), None) == -1
+
+
+@pytest.mark.parametrize("version,names,says", [
+    (3, ["kvc_score_window", "kvc_strerror"], "kvc_mass_segment"),     # an older build of the same version
+    (2, [], "ABI version 2"),                                          # another version, whatever it exports
+    (None, ["kvc_score_window"], "kvc_abi_version"),
+])
+def test_a_library_of_an_older_build_asks_for_a_rebuild(tmp_path, monkeypatch, version, names, says):
+    src, so = tmp_path / "old.c", tmp_path / "libkvc.so"
+    body = "" if version is None else f"int kvc_abi_version(void) {{ return {version}; }}\n"
+    src.write_text(body + "".join(f"int {n}(void) {{ return 0; }}\n" for n in names))
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    monkeypatch.setattr(kvc, "LIB_PATH", str(so))
+    monkeypatch.setattr(kvc, "_lib", None)
+    with pytest.raises(RuntimeError, match=says) as e:
+        kvc.lib()
+    assert "rebuild" in str(e.value) and str(so) in str(e.value)
+    assert kvc._lib is None
