@@ -571,6 +571,14 @@ def _at(t, dtypes, shape, device, name):
 _I32, _F32 = (torch.int32,), (torch.float32,)
 
 
+def _int(x, name):
+    """A C int32: ctypes would keep the low 32 bits of a larger one."""
+    n = int(x)
+    if n != x or not -0x80000000 <= n <= 0x7fffffff:
+        raise ValueError(f"{name}: {x} is no 32-bit integer")
+    return n
+
+
 def _scratch(ws, n, device):
     """A call's workspace: the given one, or n new bytes of the current stream."""
     if ws is None:
@@ -614,6 +622,7 @@ class Q8Cache(_Handle):
     seq_len (0: the table's room) and sizes the launches."""
 
     def __init__(self, k_pool, v_pool, k_scale, v_scale, table, seq_len, max_len: int = 0):
+        max_len = _int(max_len, "max_len")
         if k_pool.dtype not in _Q8_FORMAT:
             raise TypeError(f"k_pool: dtype {k_pool.dtype} not in {tuple(_Q8_FORMAT)}")
         if k_pool.dim() != 4 or table.dim() != 2:
@@ -622,7 +631,7 @@ class Q8Cache(_Handle):
         B, tb = table.shape
         dev, code = k_pool.device, (k_pool.dtype,)
         c = _CQ8Cache(n_seqs=B, kv_heads=H, head_dim=d, block_size=bs, table_blocks=tb,
-                      max_len=int(max_len), format=_Q8_FORMAT[k_pool.dtype], reserved=0, n_blocks=n)
+                      max_len=max_len, format=_Q8_FORMAT[k_pool.dtype], reserved=0, n_blocks=n)
         c.k_pool = _at(k_pool, code, (n, H, bs, d), dev, "k_pool")
         c.v_pool = _at(v_pool, code, (n, H, bs, d), dev, "v_pool")
         c.k_scale = _at(k_scale, _F32, (n, H), dev, "k_scale")
@@ -639,7 +648,8 @@ class Q8Cache(_Handle):
         """Bytes q8_attend needs for `group` query heads and `window` queries."""
         n = self._ws.get((group, window))
         if n is None:
-            n = int(lib().kvc_q8_attend_workspace_bytes(self._ref, int(group), int(window)))
+            n = int(lib().kvc_q8_attend_workspace_bytes(self._ref, _int(group, "group"),
+                                                        _int(window, "window")))
             if n == ctypes.c_size_t(-1).value:
                 raise KvcError(-4 if group > 64 else -1, "kvc_q8_attend_workspace_bytes")
             self._ws[(group, window)] = n
@@ -659,8 +669,10 @@ def q8_store(cache: Q8Cache, k, v, kept=None, T: int = 0, stream=None):
         raise ValueError("k: 3 dimensions expected, kept: 2")
     shp = (cache.heads, k.shape[1], cache.head_dim)
     n_kept = 0 if kept is None else kept.shape[1]
-    rc = lib().kvc_q8_store(cache._ref, int(T) or shp[1], shp[1],
-                            _at(kept, _I32, (cache.heads, n_kept), dev, "kept"), n_kept,
+    rc = lib().kvc_q8_store(cache._ref, _int(T, "T") or _int(shp[1], "t_stride"),
+                            _int(shp[1], "t_stride"),
+                            _at(kept, _I32, (cache.heads, n_kept), dev, "kept"),
+                            _int(n_kept, "n_kept"),
                             _at(k, _BF16_LIKE, shp, dev, "k"), _at(v, _BF16_LIKE, shp, dev, "v"), s)
     _check(rc, "kvc_q8_store")
     return cache
@@ -674,13 +686,14 @@ def q8_load(cache: Q8Cache, T: int, k_out=None, v_out=None, want_v: bool = True,
     if s is None:
         with _there(dev, stream):
             return q8_load(cache, T, k_out, v_out, want_v)
+    T = _int(T, "T")
     rows = T if k_out is None and v_out is None else (v_out if k_out is None else k_out).shape[1]
     shp = (cache.heads, rows, cache.head_dim)
     k_out, k_ptr = (_new(cache.table, shp, torch.bfloat16) if k_out is None else
                     _given(k_out, _BF16_LIKE, shp, dev, "k_out"))
     v_out, v_ptr = (_new(k_out) if v_out is None and want_v else
                     _given(v_out, _BF16_LIKE, shp, dev, "v_out"))
-    rc = lib().kvc_q8_load(cache._ref, T, rows, k_ptr, v_ptr, s)
+    rc = lib().kvc_q8_load(cache._ref, T, _int(rows, "t_stride"), k_ptr, v_ptr, s)
     _check(rc, "kvc_q8_load")
     return k_out, v_out
 
@@ -697,7 +710,7 @@ def q8_append(cache: Q8Cache, k_new, v_new, n_new=None, stream=None):
     if k_new.dim() != 3:
         raise ValueError("k_new: 3 dimensions expected")
     shp = (cache.heads, k_new.shape[1], cache.head_dim)
-    rc = lib().kvc_q8_append(cache._ref, shp[1],
+    rc = lib().kvc_q8_append(cache._ref, _int(shp[1], "window"),
                              _at(n_new, _I32, cache.seq_len.shape, dev, "n_new"),
                              _at(k_new, _BF16_LIKE, shp, dev, "k_new"),
                              _at(v_new, _BF16_LIKE, shp, dev, "v_new"), s)
@@ -736,25 +749,26 @@ class PageTable(_Handle):
     like Q8Cache."""
 
     def __init__(self, table, seq_len, refs, block_size: int):
+        block_size = _int(block_size, "block_size")
         if table.dim() != 2 or refs.dim() != 1:
             raise ValueError("table: 2 dimensions expected, refs: 1")
         B, tb = table.shape
         dev = table.device
-        c = _CPageTable(n_seqs=B, table_blocks=tb, block_size=int(block_size),
-                        n_blocks=refs.shape[0])
+        c = _CPageTable(n_seqs=B, table_blocks=tb, block_size=block_size,
+                        n_blocks=_int(refs.shape[0], "n_blocks"))
         c.table = _at(table, _I32, (B, tb), dev, "table")
         c.seq_len = _at(seq_len, _I32, (B,), dev, "seq_len")
         c.refs = _at(refs, _I32, (refs.shape[0],), dev, "refs")
         self.device = dev
         self.table, self.seq_len, self.refs = table, seq_len, refs
-        self.block_size, self.n_blocks = int(block_size), refs.shape[0]
+        self.block_size, self.n_blocks = block_size, refs.shape[0]
         self._c, self._ws, self._ref = c, {}, ctypes.addressof(c)
 
     def workspace_bytes(self, n_pairs: int = 0) -> int:
         """Bytes pages_alloc, pages_fork (n_pairs pairs) and pages_compact need."""
         n = self._ws.get(n_pairs)
         if n is None:
-            n = int(lib().kvc_pages_workspace_bytes(self._ref, int(n_pairs)))
+            n = int(lib().kvc_pages_workspace_bytes(self._ref, _int(n_pairs, "n_pairs")))
             if n == 0:
                 raise KvcError(-1, "kvc_pages_workspace_bytes")
             self._ws[n_pairs] = n
@@ -825,7 +839,7 @@ def pages_free(pages: PageTable, ids, stream=None):
     if s is None:
         with _there(dev, stream):
             return pages_free(pages, ids)
-    n = ids.shape[0]
+    n = _int(ids.shape[0], "ids")
     _check(lib().kvc_pages_free(pages._ref, n, _at(ids, _I32, (n,), dev, "ids"), s),
            "kvc_pages_free")
 
@@ -839,9 +853,9 @@ def pages_copy(src, dst, bufs: PageBuffers, stream=None):
     if s is None:
         with _there(dev, stream):
             return pages_copy(src, dst, bufs)
-    n = src.shape[0]
+    n = _int(src.shape[0], "src")
     ref, n_bufs = bufs._for(bufs.n_blocks, dev)
-    _check(lib().kvc_pages_copy(max(1, bufs.n_blocks), n, _at(src, _I32, (n,), dev, "src"),
+    _check(lib().kvc_pages_copy(max(1, _int(bufs.n_blocks, "n_blocks")), n, _at(src, _I32, (n,), dev, "src"),
                                 _at(dst, _I32, (n,), dev, "dst"), ref, n_bufs, s),
            "kvc_pages_copy")
 

@@ -125,3 +125,22 @@ def test_page_copies_past_32_bits():
     assert torch.equal(big[2], big[319]) and torch.equal(big[300], big[317])
     assert torch.equal(odd[2], odd[319]) and torch.equal(odd[300], odd[317])
     assert int(big[:2].max()) == 0 and int(big[3:300].max()) == 0 and int(big[301:317].max()) == 0
+
+
+@pytest.mark.parametrize("n", [(1 << 32) + 4, 1 << 31, -(1 << 32) + 4, 4.5])
+def test_integers_that_c_would_wrap_are_refused(n):
+    """2^32 + 4 rows are not 4 of them."""
+    c = u.to_gpu(u.random_cache(6, 1, 1, 64, 16, [16], oq.INT8, poison=False))
+    before = u.bits8(c.k_pool).copy()
+    rows = torch.zeros((1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="T"):
+        kvc.q8_store(c, rows, rows, T=n)
+    with pytest.raises(ValueError, match="T"):
+        kvc.q8_load(c, n, k_out=rows, want_v=False)
+    for group, window in ((n, 1), (1, n)):
+        with pytest.raises(ValueError, match="group|window"):
+            c.attend_workspace_bytes(group, window)
+    pages = kvc.PageTable(c.table, c.seq_len, _i32([1] * 8), 16)
+    with pytest.raises(ValueError, match="n_pairs"):
+        pages.workspace_bytes(n)
+    np.testing.assert_array_equal(u.bits8(c.k_pool), before)

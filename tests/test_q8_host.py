@@ -335,3 +335,14 @@ def test_checking_many_buffers_is_quick():
         assert kvc.lib().kvc_pages_copy(16, 100, FAKE, FAKE + GB, b, len(spans), None) == -1
         took.append(time.perf_counter() - t)
     assert min(took) < 3e-3, took
+
+
+@pytest.mark.parametrize("n", [(1 << 32) + 16, 1 << 31, -(1 << 32) + 16, 16.5])
+def test_binding_refuses_integers_that_c_would_wrap(n):
+    i32 = dict(dtype=torch.int32)
+    f8 = torch.zeros((4, 2, 16, 64), dtype=torch.float8_e4m3fn)
+    sc, tab, ln = torch.zeros((4, 2)), torch.zeros((1, 3), **i32), torch.zeros(1, **i32)
+    with pytest.raises(ValueError, match="block_size"):
+        kvc.PageTable(tab, ln, torch.zeros(4, **i32), n)
+    with pytest.raises(ValueError, match="max_len"):
+        kvc.Q8Cache(f8, f8, sc, sc, tab, ln, max_len=n)
