@@ -721,8 +721,9 @@ def q8_append(cache: Q8Cache, k_new, v_new, n_new=None, stream=None):
 def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, scale: float = 0.0,
               ws=None, stream=None):
     """Attention of the last `window` positions' queries q (bf16 [heads, group,
-    window, d]) over the cache.  Returns out (bf16, like q), or (out, lse) with
-    want_lse or an lse tensor (fp32 [heads, group, window])."""
+    window, d]) over the cache, scores times scale (0: 1 / sqrt(d)).  Returns out
+    (bf16, like q), or (out, lse) with want_lse or an lse tensor (fp32 [heads,
+    group, window])."""
     dev = cache.device
     s = _here(dev, stream)
     if s is None:
@@ -730,6 +731,8 @@ def q8_attend(cache: Q8Cache, q, out=None, lse=None, want_lse: bool = False, sca
             return q8_attend(cache, q, out, lse, want_lse, scale, ws)
     if q.dim() != 4:
         raise ValueError("q: 4 dimensions expected")
+    if scale != 0.0 and abs(scale) < 2.0 ** -149:
+        raise ValueError(f"scale: {scale} is zero in fp32, which stands for 1 / sqrt(d)")
     G, W = q.shape[1], q.shape[2]
     shp = (cache.heads, G, W, cache.head_dim)
     q_ptr = _at(q, _BF16_LIKE, shp, dev, "q")

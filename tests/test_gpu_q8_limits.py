@@ -144,3 +144,15 @@ def test_integers_that_c_would_wrap_are_refused(n):
     with pytest.raises(ValueError, match="n_pairs"):
         pages.workspace_bytes(n)
     np.testing.assert_array_equal(u.bits8(c.k_pool), before)
+
+
+@pytest.mark.parametrize("scale", [1e-50, -1e-50, 2.0 ** -150])
+def test_scales_that_fp32_takes_for_zero_are_refused(scale):
+    """0 stands for 1 / sqrt(d); a scale that vanishes in fp32 does not."""
+    c = u.to_gpu(u.random_cache(7, 1, 1, 64, 16, [16], oq.INT8, poison=False))
+    q = u.dev_bf16(u.random_rows(8, 1, 2, 1, 64))
+    with pytest.raises(ValueError, match="scale"):
+        kvc.q8_attend(c, q, scale=scale)
+    out = kvc.q8_attend(c, q, scale=2.0 ** -149)               # the smallest: every key weighs the same
+    v = kvc.q8_load(c, 16)[1].float().mean(1)
+    torch.testing.assert_close(out[0, :, 0].float(), v.expand(2, -1), rtol=2.0 ** -7, atol=2.0 ** -7)
