@@ -7,7 +7,8 @@
 namespace kvc {
 
 // Quotient by a divisor known at launch: q = (mulhi(x, m) + x) >> s, exact for
-// 0 <= x < 2^31 (m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d)).
+// 0 <= x < 2^31 (m = floor(2^32 (2^s - d) / d) + 1, s = ceil(log2 d)); Granlund and
+// Montgomery, Division by Invariant Integers using Multiplication, 1994.
 struct FastDiv {
   uint32_t d, m, s;
 };

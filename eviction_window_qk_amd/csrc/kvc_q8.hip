@@ -5,8 +5,8 @@
 // stays in registers between the two (one wave for small pages, a workgroup
 // for larger ones), so every row is read once; only pages past what a
 // workgroup holds are read twice.  All three are bound by HBM: 1792 heads' 256
-// kept rows of 768 are stored in 69 us (5.1 TB/s), a 16384-row cache of 32 heads
-// in 60 (5.8 TB/s).
+// kept rows of 768 are stored in 70 us (5.0 TB/s), a 16384-row cache of 32 heads
+// in 61 (5.8 TB/s).
 //
 // The arithmetic is one rounding at a time (this unit is compiled without
 // contraction): e4m3 scales are powers of two, so x / scale is exact and the

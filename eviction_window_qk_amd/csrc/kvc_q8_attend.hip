@@ -185,7 +185,8 @@ __device__ __forceinline__ void finish(const Args& A, size_t row, int D, int dim
 // at D = 128 need the registers of two waves (at three they spill: 146 us
 // became 269 on 128 heads of 16384 keys).
 // Look-ups of single keys take up to ten registers more: asked for four waves the
-// compiler spills some of them where it needs none for three (and four fit).
+// compiler spills some of them where it needs none for three (and four fit, but for
+// e4m3 at D = 128 with 130 registers).
 constexpr int waves(int D, int FMT, int MT, int GROUP) {
   if (D == 128 && MT == 2) return 2;
   return GROUP == 1 && (D == 128 || (MT == 2 && FMT == KVC_Q8_INT8)) ? 3 : 4;

@@ -618,7 +618,8 @@ class Q8Cache(_Handle):
     (torch.float8_e4m3fn or torch.int8), k_scale, v_scale fp32 [n_blocks,
     kv_heads], table int32 [n_seqs, table_blocks], seq_len int32 [n_seqs].
     A handle that the calls below share: the tensors are checked once, here,
-    and kept; change their contents freely, not the handle.  max_len bounds
+    and kept; change their contents freely, not the handle nor where they lie
+    (resize_, set_).  max_len bounds
     seq_len (0: the table's room) and sizes the launches."""
 
     def __init__(self, k_pool, v_pool, k_scale, v_scale, table, seq_len, max_len: int = 0):

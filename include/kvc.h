@@ -365,8 +365,9 @@ typedef struct kvc_q8_cache {
  * [0, T)) and L = min(seq_len, n_kept); kept NULL (n_kept 0) stores the last L
  * = min(seq_len, T) rows: slot j is row T - L + j, the left-padded layout of
  * kvc_params.valid_len.  A page's scale covers the slots written to it; rows
- * past L in the last page are left as they were.  Precondition: the rows are
- * finite.  No workspace. */
+ * past L in the last page are left as they were.  Heads times the pages that
+ * min(T or n_kept, cap) slots fill, K and V counted, at most 2^32 - 256.
+ * Precondition: the rows are finite.  No workspace. */
 int kvc_q8_store(const kvc_q8_cache* c, int32_t T, int32_t t_stride, const int32_t* kept,
                  int32_t n_kept, const void* k, const void* v, void* stream);
 
@@ -387,7 +388,9 @@ int kvc_q8_load(const kvc_q8_cache* c, int32_t T, int32_t t_stride, void* k_out,
  * earlier rows keeps its scale unless the new rows alone need a larger one;
  * then its earlier rows are coded again under the larger scale (e4m3: code *
  * old / new rounded to nearest even; int8: rint(code * (old * (1 / new)))).
- * The same call repeated changes nothing.  No workspace. */
+ * The same call repeated changes nothing.  Heads times the pages that window
+ * positions can touch: at most 2^32 - 256.  Precondition: the rows are finite.
+ * No workspace. */
 int kvc_q8_append(const kvc_q8_cache* c, int32_t window, const int32_t* n_new, const void* k_new,
                   const void* v_new, void* stream);
 
