@@ -40,6 +40,11 @@ SOURCES = {
     "kvc_q8.hip": ["-ffp-contract=off"],       # scales and codes: one rounding at a time
     "kvc_q8_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "kvc_pages.hip": [],
+    "kvc_paged_host.cpp": [],
+    "kvc_rope.hip": [],
+    "kvc_attend.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "kvc_attend_tiles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "kvc_evict.hip": [],
 }
 EXPORTS = ["kvc_score_window", "kvc_mass_segment", "kvc_select", "kvc_gather_compact",
            "kvc_gather_paged", "kvc_qc_trigger", "kvc_partial_init", "kvc_partial_append",
@@ -48,7 +53,10 @@ EXPORTS = ["kvc_score_window", "kvc_mass_segment", "kvc_select", "kvc_gather_com
            "kvc_check_params", "kvc_strerror", "kvc_abi_version",
            "kvc_q8_store", "kvc_q8_load", "kvc_q8_append", "kvc_q8_attend",
            "kvc_q8_attend_workspace_bytes", "kvc_pages_alloc", "kvc_pages_fork",
-           "kvc_pages_free", "kvc_pages_copy", "kvc_pages_compact", "kvc_pages_workspace_bytes"]
+           "kvc_pages_free", "kvc_pages_copy", "kvc_pages_compact", "kvc_pages_workspace_bytes",
+           "kvc_pages_trim", "kvc_rope", "kvc_paged_append", "kvc_paged_attend",
+           "kvc_paged_attend_workspace_bytes", "kvc_prompt_attend", "kvc_paged_evict",
+           "kvc_paged_evict_workspace_bytes"]
 
 
 def _compile(src: str, extra: list) -> str:

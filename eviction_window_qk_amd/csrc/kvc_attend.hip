@@ -1,0 +1,460 @@
+// Attention of a few new tokens per sequence over the bf16 paged cache on gfx950.
+//
+// For every (sequence, KV head) the G query heads' n new tokens form the R = G*n rows
+// (row r: token r / G, head r % G of the group) of two products against the same
+// keys and values:
+//   x = c * <q, k>,  w = 2^(x - m),  l = sum w,  out = sum w * v / l
+// with c = scale * log2(e).  Each cached byte is read once for all R rows; with the few
+// rows of a decode step the bound is HBM: 4*d bytes a key.
+//
+// Both products run on bf16 matrix instructions, 16x16x32, and are taken transposed,
+// S' = K Q' and O' = V' P': the lane that holds eight scores of a query row (keys
+// 4g..4g+3 of two 16-key tiles, g its 16-lane group) holds exactly the eight weights
+// that the second product wants from it, so the weights never leave their lane.  K
+// fragments are loaded as they lie in memory; V is read eight keys deep and D/16
+// values wide per lane and turned in registers by byte permutes.  Weights enter the
+// second product as bf16, their sum is fp32.
+//
+// m is a reference, not the running maximum: any value serves as long as no sum
+// overflows, so a tile is summed against the present one and m moves to the row's maximum
+// only when a lane's sum passes 2^32 (the first tile always does).
+//
+// The keys of a head are cut into pieces by its own length (few_chunk); the four
+// waves of a workgroup take the 32-key tiles of a piece in turn, and their sums meet
+// in LDS.  A second kernel joins the pieces where there are several.  Where a piece's
+// keys are is looked up once, into LDS, four keys at a time where the page size is a
+// multiple of four.
+#include "kvc_paged.h"
+
+namespace kvc {
+namespace {
+
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
+constexpr float kFar = 0x1p64f;          // -m of a row that has seen nothing
+
+struct Args {
+  AttendCall a;
+  int pieces, rows;  // of the longest length and the longest chunk: the grid's and the partials'
+  int blocks;        // row blocks
+  FastDiv by_G, by_pieces, by_H, by_blocks, by_rows;
+  int units, unit0;  // (head, piece) pairs of n0's heads, first one of this launch
+  int n0;            // first head of this launch
+  float* part;       // [n][row][piece][D] outputs of a piece
+  float* stat;       // [n][row][piece] log2 of its sum of 2^x
+};
+
+__device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  return uint32_t(to_bf16(a)) | uint32_t(to_bf16(b)) << 16;
+}
+
+// Four output values of row r of a head, and log2 of its sum of 2^x.
+__device__ __forceinline__ void finish(const Args& A, int token, int head, int dim, f32x4 out, float b) {
+  *reinterpret_cast<u16x4*>(A.a.out.p + token * A.a.out.ts + head * A.a.out.hs + dim) =
+      u16x4{to_bf16(out.x), to_bf16(out.y), to_bf16(out.z), to_bf16(out.w)};
+  if (A.a.lse && dim == 0)
+    A.a.lse[size_t(token) * (A.a.G * A.a.c.H) + head] = b * 0.6931471805599453f;
+}
+
+template <int D, int MT, int GROUP>
+__global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
+  constexpr int kSteps = D / 32;        // matrix steps over the head dimension
+  constexpr int kTiles = D / 16;        // 16-value tiles of the output
+  constexpr int kVWords = D / 32;       // words of one key's values in a lane
+  constexpr int kRowF = D + 4;          // floats of one merged row: sums, m, l
+  constexpr int kPerTile = 32 / GROUP;  // look-ups of a tile
+  extern __shared__ __align__(16) unsigned char lds_raw[];
+  uint32_t* const where = reinterpret_cast<uint32_t*>(lds_raw);  // rows of the look-ups, then the waves' sums
+  float* const lds = reinterpret_cast<float*>(lds_raw);
+  __shared__ uint32_t none_of[kFewMaxChunk / 32];  // which look-ups of a tile found no page
+
+  const Paged& c = A.a.c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int col = lane & 15, g = lane >> 4;
+  // Pieces of one head together, each head's rotated by one: workgroups go to the XCDs
+  // in turn, and where only the first pieces of a long table have keys they would all
+  // be one XCD's.  The row blocks of a piece follow each other on one XCD, whose L2 then
+  // reads its keys once.
+  const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
+  const int rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
+  const uint32_t unit = uint32_t(A.unit0) + eight * 8 + (blockIdx.x & 7);
+  if (unit >= uint32_t(A.units)) return;
+  const int nth = int(quot(A.by_pieces, unit));
+  int piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
+  piece -= piece >= A.pieces ? A.pieces : 0;
+  const int n = A.n0 + nth;
+  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
+
+  const int2 mine = chunk_of(A.a.k, b);
+  const int R = mine.y * A.a.G, row0 = rb * MT * 16;
+  if (row0 >= R) return;
+  const int len = paged_len(c, b);
+  const int chunk = few_chunk(len);
+  const int t0 = piece * chunk;
+  if (t0 >= len && piece > 0) return;
+  const int keys = len - t0 < chunk ? len - t0 : chunk;  // of this piece, 0 for an empty sequence
+  const bool alone = len <= chunk;
+
+  // Queries, on their way while the keys are looked up.
+  u32x4 qf[MT][kSteps];
+  int last[MT];  // last key of this piece that the row attends to
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int r = row0 + mt * 16 + col;
+    const int i = int(quot(A.by_G, uint32_t(r)));
+    last[mt] = r < R ? len - mine.y + i - t0 : -1;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      qf[mt][s] = u32x4{0, 0, 0, 0};
+      if (r < R)
+        qf[mt][s] = *reinterpret_cast<const u32x4*>(
+            A.a.q.p + int64_t(mine.x + i) * A.a.q.ts + int64_t(h * A.a.G + r - i * A.a.G) * A.a.q.hs + s * 32 + g * 8);
+    }
+  }
+  // Where the keys of this piece are.  A look-up that finds no page (or lies past
+  // the end) points to row 0, whose bytes are dropped later.
+  const int padded = (keys + 31) & ~31, lookups = padded / GROUP;
+  for (int i = tid; i < ((lookups + 63) & ~63); i += kThreads) {
+    uint32_t row = kNone;
+    if (i * GROUP < keys) {
+      const int64_t at = paged_row(c, b, h, t0 + i * GROUP);
+      row = at < 0 ? kNone : uint32_t(at);
+    }
+    const uint64_t none = __ballot(row == kNone);
+    if (i < lookups) {
+      where[i] = row == kNone ? 0 : row;
+      if (lane % kPerTile == 0) none_of[i / kPerTile] = uint32_t(none >> lane) & (0xffffffffu >> (32 - kPerTile));
+    }
+  }
+  __syncthreads();
+
+  // One tile of 32 keys as it is loaded.  K: this lane's keys are col of either half,
+  // its values s*32 + g*8..; V: keys 4g..4g+3 of both halves, D/16 values of each.
+  struct Tile {
+    u32x4 k[2][kSteps];
+    uint32_t v[8][kVWords];
+  };
+  auto fetch = [&](int tile, Tile& x) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int key = tile + half * 16 + col;
+      const uint16_t* at = c.k + (size_t(where[key / GROUP]) + key % GROUP) * D + g * 8;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) x.k[half][s] = *reinterpret_cast<const u32x4*>(at + s * 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int key = tile + (i >> 2) * 16 + 4 * g + (i & 3);
+      const uint16_t* at = c.v + (size_t(where[key / GROUP]) + key % GROUP) * D + col * (D / 16);
+      if constexpr (kVWords == 4) {
+        const u32x4 y = *reinterpret_cast<const u32x4*>(at);
+        x.v[i][0] = y.x, x.v[i][1] = y.y, x.v[i][2] = y.z, x.v[i][3] = y.w;
+      } else {
+        const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+        x.v[i][0] = y.x, x.v[i][1] = y.y;
+      }
+    }
+  };
+
+  float nm[MT], l[MT];  // -m, sum of this lane's weights
+  f32x4 acc[MT][kTiles];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    nm[mt] = kFar;
+    l[mt] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) acc[mt][i] = f32x4{0, 0, 0, 0};
+  }
+  const int low = len - mine.y - t0;  // the first token's last key: all rows see the keys up to it
+  const float by = A.a.c_log2;
+
+  auto work = [&](int tile, Tile& x, bool checked) {
+    float y[MT][8];
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) a = mfma(x.k[half][s], qf[mt][s], a);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[mt][half * 4 + i] = a[i];
+      }
+    if (checked) {  // the same for the whole wave
+      const uint32_t none = none_of[tile >> 5];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = (j >> 2) * 16 + 4 * g + (j & 3);
+        const bool gone = (none >> (at / GROUP)) & 1;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+          if (tile + at > last[mt] || gone) y[mt][j] = -INFINITY;
+#pragma unroll
+        for (int u = 0; u < kVWords; ++u)
+          if (tile + at >= keys || gone) x.v[j][u] = 0;
+      }
+    }
+    u32x4 w[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      float e[8], sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        e[j] = fast_exp2(__builtin_fmaf(y[mt][j], by, nm[mt]));
+        sum += e[j];
+      }
+      if (__any(!(sum <= 0x1p32f))) {
+        float top = y[mt][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, y[mt][j]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float now = fminf(nm[mt], -top * by);
+        const float f = fast_exp2(now - nm[mt]);
+        nm[mt] = now;
+        l[mt] *= f;
+#pragma unroll
+        for (int i = 0; i < kTiles; ++i) acc[mt][i] *= f;
+        sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          e[j] = fast_exp2(__builtin_fmaf(y[mt][j], by, now));
+          sum += e[j];
+        }
+      }
+      l[mt] += sum;
+      w[mt] = u32x4{pack(e[0], e[1]), pack(e[2], e[3]), pack(e[4], e[5]), pack(e[6], e[7])};
+    }
+#pragma unroll
+    for (int u = 0; u < kTiles; ++u) {
+      const uint32_t pick = u & 1 ? 0x07060302u : 0x05040100u;  // the high or the low values of two words
+      u32x4 vf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vf[i] = __builtin_amdgcn_perm(x.v[2 * i + 1][u >> 1], x.v[2 * i][u >> 1], pick);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) acc[mt][u] = mfma(vf, w[mt], acc[mt][u]);
+    }
+  };
+  for (int tile = wave * 32; tile < keys; tile += kWaves * 32) {
+    Tile cur;
+    fetch(tile, cur);
+    work(tile, cur, tile + 31 > low || none_of[tile >> 5] != 0);
+  }
+
+  // The waves' sums meet in LDS (over the look-ups), 16 rows at a time.
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    __syncthreads();
+    l[mt] += __shfl_xor(l[mt], 16);
+    l[mt] += __shfl_xor(l[mt], 32);
+    const int r0 = row0 + mt * 16, rows_here = R - r0 < 16 ? R - r0 : 16;
+    float* to = lds + (wave * 16 + col) * kRowF;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)  // values of row 4g + r of tile i: dim (4g + r) * kTiles + i
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
+    if (g == 0) {
+      to[D] = -nm[mt];
+      to[D + 1] = l[mt];
+    }
+    __syncthreads();
+    for (int e = tid; e < rows_here * (D / 4); e += kThreads) {
+      const int r = e / (D / 4), dim = e % (D / 4) * 4;
+      const float* at = lds + r * kRowF;
+      float M = -kFar;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * 16 * kRowF + D]);
+      f32x4 sum = {0, 0, 0, 0};
+      float L = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float* aw = at + w * 16 * kRowF;
+        const float f = fast_exp2(aw[D] - M);
+        sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
+        L = __builtin_fmaf(aw[D + 1], f, L);
+      }
+      const bool any = L > 0.0f;
+      sum = any ? sum * (1.0f / L) : f32x4{0, 0, 0, 0};
+      const float bsum = any ? M + fast_log2(L) : -INFINITY;
+      if (alone) {
+        const int i = int(quot(A.by_G, uint32_t(r0 + r)));
+        finish(A, mine.x + i, h * A.a.G + r0 + r - i * A.a.G, dim, sum, bsum);
+      } else {
+        const size_t at_piece = (size_t(n) * A.rows + r0 + r) * A.pieces + piece;
+        *reinterpret_cast<f32x4*>(A.part + at_piece * D + dim) = sum;
+        if (dim == 0) A.stat[at_piece] = bsum;
+      }
+    }
+  }
+}
+
+// Joins the pieces of one row, each weighted by its sum: D/4 lanes read one piece's
+// outputs, the workgroup 1024/D pieces at a time.
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_join_few(Args A) {
+  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+  __shared__ __align__(16) float sums[kAtOnce][D];
+  const int nth = int(quot(A.by_rows, blockIdx.x)), n = A.n0 + nth;
+  const int r = int(blockIdx.x) - nth * A.rows;
+  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
+  const int2 mine = chunk_of(A.a.k, b);
+  if (r >= mine.y * A.a.G) return;
+  const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
+  if (len <= chunk) return;
+  const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
+  const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
+  const size_t row = size_t(n) * A.rows + r;
+  const float* st = A.stat + row * A.pieces;
+  const float* part = A.part + row * A.pieces * D + dim;
+  const float first = lane < pieces ? st[lane] : -INFINITY;  // the lane's piece of the first 64
+  float M = first;
+  for (int p = lane + 64; p < pieces; p += 64) M = fmaxf(M, st[p]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = fast_exp2(first - base);
+  for (int p = lane + 64; p < pieces; p += 64) L += fast_exp2(st[p] - base);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off);
+  const float by_L = L > 0.0f ? 1.0f / L : 0.0f;
+  f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int p = group; p < pieces; p += kAtOnce)
+    sum += *reinterpret_cast<const f32x4*>(part + size_t(p) * D) * (fast_exp2(st[p] - base) * by_L);
+  *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  f32x4 out = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kAtOnce; ++i) out += *reinterpret_cast<const f32x4*>(&sums[i][dim]);
+  const int i = int(quot(A.by_G, uint32_t(r)));
+  finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, out, L > 0.0f ? base + fast_log2(L) : -INFINITY);
+}
+
+template <int D, int MT, int GROUP>
+void attend_few(Args A, hipStream_t s) {
+  // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits), in
+  // whole eights of units.
+  const int heads = A.a.c.B * A.a.c.H;
+  A.blocks = (A.rows + MT * 16 - 1) / (MT * 16);
+  const int room = ((1 << 23) / A.blocks) & ~7;
+  const int most = room / A.pieces > 0 ? room / A.pieces : 1;
+  A.by_blocks = fast_div(uint32_t(A.blocks));
+  const size_t keys = size_t(A.a.c.cap < kFewMaxChunk ? ((A.a.c.cap < kFewChunk ? kFewChunk : A.a.c.cap) + 127) & ~127 : kFewMaxChunk) / GROUP * 4;
+  const size_t sums = size_t(kWaves) * 16 * (D + 4) * sizeof(float);
+  for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
+    const int nh = heads - A.n0 < most ? heads - A.n0 : most;
+    A.units = nh * A.pieces;
+    for (A.unit0 = 0; A.unit0 < A.units; A.unit0 += room) {
+      const int here = A.units - A.unit0 < room ? A.units - A.unit0 : room;
+      k_attend_few<D, MT, GROUP><<<unsigned((here + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
+                                   keys > sums ? keys : sums, s>>>(A);
+    }
+  }
+  if (A.pieces == 1) return;
+  const int most_joined = (1 << 23) / A.rows > 0 ? (1 << 23) / A.rows : 1;
+  for (A.n0 = 0; A.n0 < heads; A.n0 += most_joined) {
+    const int nh = heads - A.n0 < most_joined ? heads - A.n0 : most_joined;
+    k_join_few<D><<<unsigned(nh) * unsigned(A.rows), kThreads, 0, s>>>(A);
+  }
+}
+
+template <int D>
+void attend_rows(const Args& A, hipStream_t s) {
+  const bool fours = A.a.c.bs % 4 == 0;
+  if (A.rows <= 16) {
+    if (fours) attend_few<D, 1, 4>(A, s);
+    else attend_few<D, 1, 1>(A, s);
+  } else {
+    if (fours) attend_few<D, 2, 4>(A, s);
+    else attend_few<D, 2, 1>(A, s);
+  }
+}
+
+// The column sums of the softmax weights, one thread a slot.
+__global__ __launch_bounds__(kThreads) void k_weights(AttendCall a, const float* lse) {
+  const Paged& c = a.c;
+  const float by = a.c_log2;
+  for (int n = blockIdx.y; n < c.B * c.H; n += gridDim.y) {
+  const int b = n / c.H, h = n - b * c.H;
+  const int2 mine = chunk_of(a.k, b);
+  const int len = paged_len(c, b);
+  for (int t = blockIdx.x * kThreads + threadIdx.x; t < len; t += gridDim.x * kThreads) {
+    const int64_t row = paged_row(c, b, h, t);
+    if (row < 0) continue;
+    const uint16_t* kr = c.k + row * c.D;
+    float total = 0.0f;
+    int i0 = t - (len - mine.y);
+    for (int i = i0 < 0 ? 0 : i0; i < mine.y; ++i)
+      for (int g = 0; g < a.G; ++g) {
+        const int head = h * a.G + g;
+        const uint16_t* qr = a.q.p + int64_t(mine.x + i) * a.q.ts + int64_t(head) * a.q.hs;
+        float x = 0.0f;
+        for (int e = 0; e < c.D; ++e)
+          x = __builtin_fmaf(__uint_as_float(uint32_t(qr[e]) << 16), __uint_as_float(uint32_t(kr[e]) << 16), x);
+        const float z = lse[size_t(mine.x + i) * (a.G * c.H) + head];
+        total += fast_exp2(__builtin_fmaf(x, by, -z * 1.4426950408889634f));
+      }
+    c.weight[size_t(n) * c.room + t] += total;
+  }
+  }
+}
+
+}  // namespace
+
+AttendWs attend_ws(const Paged& c, const Chunks& k, int G) {
+  AttendWs w{};
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = (off + n + 63) & ~size_t(63);
+    return at;
+  };
+  w.few_rows = G * k.max_new;
+  w.few_pieces = few_max_pieces(c.cap);
+  const size_t n = w.few_pieces > 1 ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : 0;
+  w.few_part = take(n * c.D);
+  w.few_stat = take(n);
+  w.lse = take(c.weight ? size_t(k.n_tokens) * G * c.H : 0);
+  w.total = off;
+  return w;
+}
+
+hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
+  const AttendWs w = attend_ws(a.c, a.k, a.G);
+  Args A{};
+  A.a = a;
+  if (a.c.weight && !a.lse) A.a.lse = ws + w.lse;
+  A.pieces = w.few_pieces;
+  A.rows = w.few_rows;
+  A.by_G = fast_div(uint32_t(a.G));
+  A.by_pieces = fast_div(uint32_t(A.pieces));
+  A.by_H = fast_div(uint32_t(a.c.H));
+  A.by_rows = fast_div(uint32_t(A.rows));
+  A.part = ws + w.few_part;
+  A.stat = ws + w.few_stat;
+  if (a.c.D == 128) attend_rows<128>(A, s);
+  else attend_rows<64>(A, s);
+  if (a.c.weight) {
+    const int blocks = (a.c.cap + kThreads - 1) / kThreads;
+    k_weights<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), unsigned(a.c.B * a.c.H < 32768 ? a.c.B * a.c.H : 32768)), kThreads, 0, s>>>(A.a, A.a.lse);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace kvc

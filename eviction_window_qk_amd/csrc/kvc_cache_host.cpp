@@ -13,33 +13,6 @@
 namespace kvc {
 namespace {
 
-// Makes the device of `stream` current for the launches of a call.  The implicit
-// streams are the current device's already, and their handles no objects that the
-// runtime could be asked about.
-struct OnDeviceOf {
-  int was = -1;
-  bool ok = true;
-  explicit OnDeviceOf(hipStream_t stream) {
-    if (stream == nullptr || stream == hipStreamPerThread) return;
-    int cur = -1, dev = -1;
-    ok = hipGetDevice(&cur) == hipSuccess && hipStreamGetDevice(stream, &dev) == hipSuccess;
-    if (ok && cur != dev) {
-      ok = hipSetDevice(dev) == hipSuccess;
-      was = cur;
-    }
-  }
-  ~OnDeviceOf() {
-    if (was >= 0) (void)hipSetDevice(was);
-  }
-};
-
-template <class F>
-int launch_on(void* stream, F launch) {
-  const hipStream_t s = hipStream_t(stream) == hipStreamLegacy ? nullptr : hipStream_t(stream);
-  OnDeviceOf dev(s);
-  return dev.ok ? launch_status(launch(s)) : KVC_EDEVICE;
-}
-
 size_t pool_bytes(const kvc_q8_cache* c) {
   return size_t(c->n_blocks) * c->kv_heads * c->block_size * c->head_dim;
 }
@@ -397,6 +370,18 @@ int kvc_pages_free(const kvc_page_table* t, int32_t n_ids, const int32_t* ids, v
   const Range in[] = {{ids, size_t(n_ids) * 4}};
   if (any_alias(in, 1, out, 3)) return KVC_EINVAL;
   return launch_on(stream, [&](hipStream_t s) { return launch_pages_free(p, n_ids, ids, s); });
+}
+
+int kvc_pages_trim(const kvc_page_table* t, void* stream) {
+  Pages p;
+  int rc = pages_shape(t, &p);
+  if (rc != KVC_OK) return rc;
+  if (p.B == 0) return KVC_OK;
+  if ((rc = pages_pointers(t)) != KVC_OK) return rc;
+  Range r[3];
+  pages_ranges(t, r);
+  if (any_alias(r, 0, r, 3)) return KVC_EINVAL;
+  return launch_on(stream, [&](hipStream_t s) { return launch_pages_trim(p, s); });
 }
 
 int kvc_pages_copy(int32_t n_blocks, int32_t n_pairs, const int32_t* src, const int32_t* dst,

@@ -34,4 +34,31 @@ inline int launch_status(hipError_t e) {
   return hipGetLastError() == hipSuccess ? KVC_OK : KVC_EDEVICE;
 }
 
+// Makes the device of `stream` current for the launches of a call.  The implicit
+// streams are the current device's already, and their handles no objects that the
+// runtime could be asked about.
+struct OnDeviceOf {
+  int was = -1;
+  bool ok = true;
+  explicit OnDeviceOf(hipStream_t stream) {
+    if (stream == nullptr || stream == hipStreamPerThread) return;
+    int cur = -1, dev = -1;
+    ok = hipGetDevice(&cur) == hipSuccess && hipStreamGetDevice(stream, &dev) == hipSuccess;
+    if (ok && cur != dev) {
+      ok = hipSetDevice(dev) == hipSuccess;
+      was = cur;
+    }
+  }
+  ~OnDeviceOf() {
+    if (was >= 0) (void)hipSetDevice(was);
+  }
+};
+
+template <class F>
+int launch_on(void* stream, F launch) {
+  const hipStream_t s = hipStream_t(stream) == hipStreamLegacy ? nullptr : hipStream_t(stream);
+  OnDeviceOf dev(s);
+  return dev.ok ? launch_status(launch(s)) : KVC_EDEVICE;
+}
+
 }  // namespace kvc

@@ -1,0 +1,142 @@
+// bf16 paged cache: declarations shared by its kernels and host code.
+#pragma once
+
+#include "kvc_div.h"
+#include "kvc_internal.h"
+
+namespace kvc {
+
+// A cache after validation.
+struct Paged {
+  int B, H, D, bs, tb, cap, room;  // cap: bound on a length; room: tb * bs, a head's stride in weight and pos
+  uint32_t n_blocks;
+  FastDiv div;  // by bs
+  uint16_t* k;
+  uint16_t* v;
+  const int32_t* table;
+  int32_t* seq_len;
+  float* weight;
+  int32_t* pos;
+};
+
+// Rows of tokens, strides in values.
+struct Rows {
+  uint16_t* p;
+  int64_t ts, hs;
+};
+
+// New tokens packed by sequence.
+struct Chunks {
+  const int32_t* starts;
+  int B, n_tokens, max_new;
+};
+
+// A rotation after validation.
+struct RopePlan {
+  const double* freq;
+  int r;            // rotated values of a row, 0: none
+  int interleaved;
+  float mscale;
+  float sign;       // of the angles
+};
+
+__device__ __forceinline__ int paged_len(const Paged& c, int b) {
+  const int len = c.seq_len[b];
+  return len < 0 ? 0 : (len < c.cap ? len : c.cap);
+}
+
+// Page of logical block j of sequence b, or -1.
+__device__ __forceinline__ int paged_page(const Paged& c, int b, int j) {
+  const int32_t p = c.table[size_t(b) * c.tb + j];
+  return uint32_t(p) < c.n_blocks ? p : -1;
+}
+
+// Row in the pools of slot t of head h of sequence b, or -1: rows are below 2^32 - 1.
+__device__ __forceinline__ int64_t paged_row(const Paged& c, int b, int h, int t) {
+  const uint32_t j = quot(c.div, uint32_t(t));
+  const int page = paged_page(c, b, int(j));
+  return page < 0 ? -1
+                  : (int64_t(page) * c.H + h) * c.bs + int64_t(uint32_t(t) - j * uint32_t(c.bs));
+}
+
+// First token and token count of sequence b, whatever starts holds.
+__device__ __forceinline__ int2 chunk_of(const Chunks& k, int b) {
+  int a = k.starts[b], e = k.starts[b + 1];
+  a = a < 0 ? 0 : (a < k.n_tokens ? a : k.n_tokens);
+  e = e < a ? a : (e < k.n_tokens ? e : k.n_tokens);
+  return make_int2(a, e - a < k.max_new ? e - a : k.max_new);
+}
+
+// The last b in [0, B) with f(starts[b], b) <= x (0 if there is none), f ascending in
+// both: 64 candidates a step, one for each lane.
+template <class F>
+__device__ __forceinline__ int last_at_or_below(const int32_t* starts, int B, int x, F f) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 63) >> 6, i = lane * step;
+    const bool in = i < n && f(starts[lo + i], lo + i) <= x;
+    const uint64_t m = __ballot(in);
+    const int at = m ? (63 - __builtin_clzll(m)) * step : 0;
+    lo += at;
+    n = n - at < step ? n - at : step;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float x) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
+}
+
+// Keys per workgroup of the attention of few rows, for a sequence of len slots: pieces of at most
+// kFewChunk, doubled to kFewMaxChunk while there are more than 64; equal pieces, in
+// multiples of the workgroup's 128-key stride.  A piece depends on the sequence's own
+// length only, so a head's sums are taken in the same order whatever else is in the
+// launch.
+constexpr int kFewChunk = 512, kFewMaxChunk = 2048;
+static_assert(kFewChunk % 128 == 0 && kFewMaxChunk % 128 == 0, "pieces are whole strides");
+__host__ __device__ inline int few_chunk(int len) {
+  int c = kFewChunk;
+  while (c < kFewMaxChunk && len > 64 * c) c *= 2;
+  const int pieces = (len + c - 1) / c;
+  return pieces > 1 ? ((len + pieces - 1) / pieces + 127) & ~127 : c;
+}
+// The most pieces that any length up to cap is cut into.
+inline int few_max_pieces(int cap) {
+  if (cap <= 64 * kFewChunk) return cap > 0 ? (cap + kFewChunk - 1) / kFewChunk : 1;
+  const int n = (cap + kFewMaxChunk - 1) / kFewMaxChunk;
+  return n > 64 ? n : 64;
+}
+
+// A call of the attention over the cache.
+struct AttendCall {
+  Paged c;
+  Chunks k;
+  int G;
+  float c_log2;     // scale * log2(e)
+  Rows q, out;
+  float* lse;       // [n_tokens][G * H] or NULL
+};
+
+// Workspace carve-up, in floats.
+struct AttendWs {
+  size_t few_part, few_stat, lse, total;
+  int few_rows, few_pieces;
+};
+AttendWs attend_ws(const Paged& c, const Chunks& k, int G);
+
+hipError_t launch_rope(const RopePlan& f, int n_tokens, int heads, int D, const int32_t* positions,
+                       const Rows& x, const Rows& y, hipStream_t s);
+hipError_t launch_paged_append(const Paged& c, const Chunks& k, const int32_t* positions,
+                               const RopePlan& f, int q_heads, const Rows& q, const Rows& q_out,
+                               const Rows& k_new, const Rows& v_new, hipStream_t s);
+hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s);
+hipError_t launch_weights(const AttendCall& a, const float* lse, hipStream_t s);
+hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_log2, const Rows& q,
+                                const Rows& k_rows, const Rows& v_rows, const Rows& out,
+                                float* lse, hipStream_t s);
+size_t evict_ws(const Paged& c, int budget);
+hipError_t launch_paged_evict(const Paged& c, const int32_t* seen, int K, int sinks, int recent,
+                              int32_t* ws, hipStream_t s);
+
+}  // namespace kvc

@@ -40,6 +40,7 @@ hipError_t launch_pages_fork(const Pages& t, int n_pairs, const int32_t* src, co
                              const Buffers* groups, int n_groups, int32_t* status, int32_t* ws,
                              hipStream_t s);
 hipError_t launch_pages_free(const Pages& t, int n_ids, const int32_t* ids, hipStream_t s);
+hipError_t launch_pages_trim(const Pages& t, hipStream_t s);
 hipError_t launch_pages_copy(int n_blocks, int n_pairs, const int32_t* src, const int32_t* dst,
                              const Buffers* groups, int n_groups, hipStream_t s);
 hipError_t launch_pages_compact(const Pages& t, const Buffers* groups, int n_groups,

@@ -468,6 +468,20 @@ __global__ __launch_bounds__(kThreads) void k_pages_free(Pages t, const int32_t*
   if (threadIdx.x == 0) t.seq_len[b] = 0;
 }
 
+// --- trim --------------------------------------------------------------------
+
+__global__ __launch_bounds__(kThreads) void k_pages_trim(Pages t) {
+  const int b = blockIdx.x, len = t.seq_len[b];
+  int32_t* row = t.table + size_t(b) * t.tb;
+  const int from = len > 0 ? (len - 1) / t.bs + 1 : 0;
+  for (int j = from + threadIdx.x; j < t.tb; j += kThreads) {
+    const int32_t p = row[j];
+    if (!is_page(t, p)) continue;
+    row[j] = -1;
+    atomicSub(&t.refs[p], 1);
+  }
+}
+
 // --- compact -----------------------------------------------------------------
 
 // Free pages below n_live ("holes") and live ones at or past it ("movers"), each
@@ -659,6 +673,11 @@ hipError_t launch_pages_fork(const Pages& t, int n_pairs, const int32_t* src, co
 
 hipError_t launch_pages_free(const Pages& t, int n_ids, const int32_t* ids, hipStream_t s) {
   k_pages_free<<<unsigned(n_ids), kThreads, 0, s>>>(t, ids);
+  return hipGetLastError();
+}
+
+hipError_t launch_pages_trim(const Pages& t, hipStream_t s) {
+  k_pages_trim<<<unsigned(t.B), kThreads, 0, s>>>(t);
   return hipGetLastError();
 }
 

@@ -15,6 +15,7 @@ Tensor conventions (see include/kvc.h for the full layouts):
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass, fields
 
@@ -74,6 +75,27 @@ class _CPageTable(ctypes.Structure):
 
 class _CPageBuffer(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
+class _CPagedCache(ctypes.Structure):
+    _fields_ = [
+        ("n_seqs", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32), ("table_blocks", ctypes.c_int32),
+        ("max_len", ctypes.c_int32), ("n_blocks", ctypes.c_int64),
+        ("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("table", ctypes.c_void_p),
+        ("seq_len", ctypes.c_void_p), ("weight", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+    ]
+
+
+class _CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _CRopePlan(ctypes.Structure):
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
 
 
 @dataclass
@@ -182,6 +204,16 @@ def lib() -> ctypes.CDLL:
         "kvc_pages_copy": [ctypes.c_int32, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp],
         "kvc_pages_compact": [vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp, sz, vp],
         "kvc_pages_workspace_bytes": [vp, ctypes.c_int32],
+        "kvc_pages_trim": [vp, vp],
+        "kvc_rope": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, ctypes.c_int32, vp, vp, vp,
+                     vp],
+        "kvc_paged_append": [vp, ctypes.c_int32, vp, vp, vp, ctypes.c_int32, vp, vp, vp, vp, vp],
+        "kvc_paged_attend": [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp,
+                             ctypes.c_float, vp, vp, vp, vp, sz, vp],
+        "kvc_paged_attend_workspace_bytes": [vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32],
+        "kvc_prompt_attend": [ctypes.c_int32] * 5 + [vp, ctypes.c_float, vp, vp, vp, vp, vp, vp],
+        "kvc_paged_evict": [vp, vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, vp, sz, vp],
+        "kvc_paged_evict_workspace_bytes": [vp, ctypes.c_int32],
         "kvc_workspace_bytes": [P],
         "kvc_segment_capacity": [P],
         "kvc_check_params": [P],
@@ -199,7 +231,8 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} has ABI version {fn()}, this binding expects "
                                f"{ABI_VERSION}: {rebuild}")
     for name in ("kvc_workspace_bytes", "kvc_q8_attend_workspace_bytes",
-                 "kvc_pages_workspace_bytes"):
+                 "kvc_pages_workspace_bytes", "kvc_paged_attend_workspace_bytes",
+                 "kvc_paged_evict_workspace_bytes"):
         getattr(L, name).restype = ctypes.c_size_t
     L.kvc_strerror.restype = ctypes.c_char_p
     _lib = L
@@ -848,6 +881,15 @@ def pages_free(pages: PageTable, ids, stream=None):
            "kvc_pages_free")
 
 
+def pages_trim(pages: PageTable, stream=None):
+    """Gives up the pages behind each sequence's length."""
+    s = _here(pages.device, stream)
+    if s is None:
+        with _there(pages.device, stream):
+            return pages_trim(pages)
+    _check(lib().kvc_pages_trim(pages._ref, s), "kvc_pages_trim")
+
+
 def pages_copy(src, dst, bufs: PageBuffers, stream=None):
     """Copies page src[i] to page dst[i] (int32 [n_pairs]) in every buffer."""
     dev = src.device
@@ -885,3 +927,302 @@ def pages_compact(pages: PageTable, bufs: PageBuffers, out=None, ws=None, stream
                                  ptr["n_live"], *_span(ws), s)
     _check(rc, "kvc_pages_compact")
     return o
+
+
+# ---------------------------------------------------------------------------
+# bf16 paged cache: rotation, append, attention, eviction (include/kvc.h documents
+# each call)
+# ---------------------------------------------------------------------------
+
+_F64 = (torch.float64,)
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = None, factor: float = 1.0,
+                     trained: int = 0, slow: float = 1.0, fast: float = 4.0):
+    """Radians a position of the rot_dim / 2 pairs (fp64, CPU), base^(-2i / rot_dim),
+    and the factor on the rotated values (mscale), stretched to `factor` times the
+    `trained` positions:
+      None      as they are
+      "linear"  all divided by factor
+      "ntk"     of the base times factor^(rot_dim / (rot_dim - 2)): the fastest pair
+                keeps its frequency, the slowest is divided by factor
+      "banded"  a pair that turns more than `fast` times in `trained` positions keeps
+                its frequency, one that turns less than `slow` times is divided by factor, in
+                between a blend, linear in the turns
+      "yarn"    the same with a blend linear in the pair's index (between those that
+                turn `fast` and `slow` times, rounded outwards; usually 32 and 1), and mscale
+                0.1 ln(factor) + 1"""
+    rot_dim = _int(rot_dim, "rot_dim")
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError(f"rot_dim: {rot_dim} is no positive even number")
+    if not base > 1.0 or not factor >= 1.0 or math.isinf(base) or math.isinf(factor):
+        raise ValueError(f"base {base} and factor {factor}: above 1, at least 1, finite")
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim == 2:
+            raise ValueError("scaling ntk: needs more than one pair")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = base ** (-2.0 * i / rot_dim)
+    if scaling in (None, "ntk"):
+        return freq, 1.0
+    if scaling == "linear":
+        return freq / factor, 1.0
+    if scaling not in ("banded", "yarn"):
+        raise ValueError(f"scaling: {scaling!r} is none of None, linear, ntk, banded, yarn")
+    if trained < 1 or not 0.0 < slow < fast:
+        raise ValueError(f"scaling {scaling}: trained {trained} >= 1 and 0 < slow {slow} < fast {fast} expected")
+    if scaling == "banded":
+        keep = ((trained * freq / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        return freq * (keep + (1 - keep) / factor), 1.0
+    pair = lambda turns: rot_dim * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
+    first, last = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot_dim - 1)
+    gone = ((i - first) / max(last - first, 0.001)).clamp(0, 1)
+    return freq * (1 - gone + gone / factor), 0.1 * math.log(factor) + 1.0
+
+
+class Rope(_Handle):
+    """A rotation: freq fp64 [rot_dim / 2] on the GPU (rope_frequencies), pairs (i, i +
+    rot_dim / 2) or, interleaved, (2i, 2i + 1), rotated values times mscale."""
+
+    def __init__(self, freq, interleaved: bool = False, mscale: float = 1.0):
+        if freq.dim() != 1:
+            raise ValueError("freq: 1 dimension expected")
+        c = _CRopePlan(rot_dim=_int(2 * freq.shape[0], "rot_dim"), interleaved=1 if interleaved else 0,
+                       mscale=float(mscale), reserved=0)
+        c.freq = _at(freq, _F64, (freq.shape[0],), freq.device, "freq")
+        self.device, self.freq = freq.device, freq
+        self._c, self._ref = c, ctypes.addressof(c)
+
+
+def _rows(t, shape, device, name):
+    """kvc_rows of a bf16 tensor [n_tokens, heads, d], any strides with whole rows."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dtype not in _BF16_LIKE:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16_LIKE}")
+    if device.type != "cuda" or t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}" if device.type == "cuda" else
+                         f"{name}: must be a GPU tensor, got {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    ts, hs, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    # a stride that no step is taken by may be anything
+    return _CRows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+
+
+def _ref(c):
+    return ctypes.addressof(c)
+
+
+def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
+    """Rotates x (bf16 [n_tokens, heads, d], rows contiguous) by positions (int32
+    [n_tokens]) into y (None: a new tensor; x itself: in place).  backward: by the
+    transposed map.  Returns y."""
+    dev = plan.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return rope(plan, x, positions, y, backward)
+    if x.dim() != 3:
+        raise ValueError("x: 3 dimensions expected")
+    n, heads, d = x.shape
+    cx = _rows(x, x.shape, dev, "x")
+    p_ptr = _at(positions, _I32, (n,), dev, "positions")
+    if y is None:
+        y = torch.empty((n, heads, d), dtype=x.dtype, device=dev)
+    cy = cx if y is x else _rows(y, x.shape, dev, "y")
+    rc = lib().kvc_rope(_int(n, "n_tokens"), _int(heads, "heads"), _int(d, "head_dim"), plan._ref,
+                        1 if backward else 0, p_ptr, _ref(cx), _ref(cy), s)
+    _check(rc, "kvc_rope")
+    return y
+
+
+class PagedCache(_Handle):
+    """A bf16 paged cache: k_pool, v_pool [n_blocks, kv_heads, block_size, d], table int32
+    [n_seqs, table_blocks], seq_len int32 [n_seqs]; weight fp32 and pos int32 [n_seqs *
+    kv_heads, table_blocks * block_size], both or neither: what the attention has
+    given each slot, and the position it holds.  A handle like Q8Cache."""
+
+    def __init__(self, k_pool, v_pool, table, seq_len, weight=None, pos=None, max_len: int = 0):
+        max_len = _int(max_len, "max_len")
+        if k_pool.dim() != 4 or table.dim() != 2:
+            raise ValueError("k_pool: 4 dimensions expected, table: 2")
+        if (weight is None) != (pos is None):
+            raise ValueError("weight and pos: both or neither")
+        n, H, bs, d = k_pool.shape
+        B, tb = table.shape
+        dev, slots = k_pool.device, (B * H, tb * bs)
+        c = _CPagedCache(n_seqs=B, kv_heads=H, head_dim=d, block_size=bs, table_blocks=tb,
+                         max_len=max_len, n_blocks=n)
+        c.k_pool = _at(k_pool, _BF16_LIKE, (n, H, bs, d), dev, "k_pool")
+        c.v_pool = _at(v_pool, _BF16_LIKE, (n, H, bs, d), dev, "v_pool")
+        c.table = _at(table, _I32, (B, tb), dev, "table")
+        c.seq_len = _at(seq_len, _I32, (B,), dev, "seq_len")
+        c.weight = _at(weight, _F32, slots, dev, "weight")
+        c.pos = _at(pos, _I32, slots, dev, "pos")
+        self.device = dev
+        self.k_pool, self.v_pool, self.table, self.seq_len = k_pool, v_pool, table, seq_len
+        self.weight, self.pos = weight, pos
+        self.kv_heads, self.head_dim = H, d
+        self._c, self._ws, self._ref = c, {}, ctypes.addressof(c)
+
+    def attend_workspace_bytes(self, group: int, n_tokens: int, max_new: int = 0) -> int:
+        """Bytes paged_attend needs for n_tokens new tokens, max_new of a sequence at most."""
+        key = (group, n_tokens, max_new)
+        n = self._ws.get(key)
+        if n is None:
+            n = int(lib().kvc_paged_attend_workspace_bytes(
+                self._ref, _int(group, "group"), _int(n_tokens, "n_tokens"), _int(max_new, "max_new")))
+            if n == ctypes.c_size_t(-1).value:
+                raise KvcError(-4 if group > 64 else -1, "kvc_paged_attend_workspace_bytes")
+            if len(self._ws) > 4096:    # prompts bring ever new counts of tokens
+                self._ws.clear()
+            self._ws[key] = n
+        return n
+
+    def evict_workspace_bytes(self, budget: int) -> int:
+        """Bytes paged_evict needs."""
+        n = self._ws.get(budget)
+        if n is None:
+            n = int(lib().kvc_paged_evict_workspace_bytes(self._ref, _int(budget, "budget")))
+            if n == 0:
+                raise KvcError(-1, "kvc_paged_evict_workspace_bytes")
+            self._ws[budget] = n
+        return n
+
+
+def _starts(cache, starts):
+    return _at(starts, _I32, (cache.seq_len.shape[0] + 1,), cache.device, "starts")
+
+
+def _group(q, kv_heads, name):
+    if q.dim() != 3:
+        raise ValueError(f"{name}: 3 dimensions expected")
+    if q.shape[1] % kv_heads:
+        raise ValueError(f"{name}: {q.shape[1]} heads are no multiple of {kv_heads}")
+    return q.shape[1] // kv_heads
+
+
+def paged_append(cache: PagedCache, k, v, starts, positions=None, rope: Rope = None, q=None,
+                 q_out=None, stream=None):
+    """Writes k, v (bf16 [n_tokens, kv_heads, d], rows contiguous) of the new tokens, packed
+    by sequence (starts int32 [n_seqs + 1]), into their slots, k rotated by `rope` at
+    positions (int32 [n_tokens]; None: the slots).  q ([n_tokens, heads, d], with rope) is
+    rotated into q_out (None: a new tensor; q itself: in place).  Returns q_out, or the cache
+    without q."""
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return paged_append(cache, k, v, starts, positions, rope, q, q_out)
+    if k.dim() != 3:
+        raise ValueError("k: 3 dimensions expected")
+    n = k.shape[0]
+    shp = (n, cache.kv_heads, cache.head_dim)
+    ck, cv = _rows(k, shp, dev, "k"), _rows(v, shp, dev, "v")
+    st_ptr = _starts(cache, starts)
+    p_ptr = _at(positions, _I32, (n,), dev, "positions")
+    if rope is not None and rope.device != dev:
+        raise ValueError(f"rope: on {rope.device}, expected {dev}")
+    G, q_ref, o_ref = 0, None, None
+    if q is not None:
+        G = _group(q, cache.kv_heads, "q")
+        q_shp = (n, q.shape[1], cache.head_dim)
+        cq = _rows(q, q_shp, dev, "q")
+        if q_out is None:
+            q_out = torch.empty(q_shp, dtype=q.dtype, device=dev)
+        co = cq if q_out is q else _rows(q_out, q_shp, dev, "q_out")
+        q_ref, o_ref = _ref(cq), _ref(co)
+    elif q_out is not None:
+        raise ValueError("q_out: without q")
+    rc = lib().kvc_paged_append(cache._ref, _int(n, "n_tokens"), st_ptr, p_ptr,
+                                None if rope is None else rope._ref, _int(G, "group"), q_ref, o_ref,
+                                _ref(ck), _ref(cv), s)
+    _check(rc, "kvc_paged_append")
+    return cache if q is None else q_out
+
+
+def _scale(scale):
+    if scale != 0.0 and abs(scale) < 2.0 ** -149:
+        raise ValueError(f"scale: {scale} is zero in fp32, which stands for 1 / sqrt(d)")
+    return scale
+
+
+def paged_attend(cache: PagedCache, q, starts, max_new: int = 0, out=None, lse=None,
+                 want_lse: bool = False, scale: float = 0.0, ws=None, stream=None):
+    """Attention of the new tokens' queries q (bf16 [n_tokens, heads, d], rows contiguous,
+    packed by sequence: starts int32 [n_seqs + 1]) over the cache; in a cache with
+    weight and pos the slots' weights grow by what they receive.  max_new bounds the new
+    tokens of a sequence (0: n_tokens).  Returns out (bf16, like q), or (out, lse) with
+    want_lse or an lse tensor (fp32 [n_tokens, heads])."""
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return paged_attend(cache, q, starts, max_new, out, lse, want_lse, scale, ws)
+    G = _group(q, cache.kv_heads, "q")
+    shp = (q.shape[0], q.shape[1], cache.head_dim)
+    cq = _rows(q, shp, dev, "q")
+    st_ptr = _starts(cache, starts)
+    ws = _scratch(ws, cache.attend_workspace_bytes(G, shp[0], max_new), dev)
+    if out is None:
+        out = torch.empty(shp, dtype=q.dtype, device=dev)
+    co = _rows(out, shp, dev, "out")
+    lse, lse_ptr = (_new(q, shp[:2], torch.float32) if lse is None and want_lse else
+                    _given(lse, _F32, shp[:2], dev, "lse"))
+    rc = lib().kvc_paged_attend(cache._ref, G, shp[0], _int(max_new, "max_new"), st_ptr, _scale(scale),
+                                _ref(cq), _ref(co), lse_ptr, *_span(ws), s)
+    _check(rc, "kvc_paged_attend")
+    return out if lse is None else (out, lse)
+
+
+def prompt_attend(q, k, v, starts, out=None, lse=None, want_lse: bool = False, scale: float = 0.0,
+                  stream=None):
+    """Causal attention within packed prompts: q (bf16 [n_tokens, heads, d]), k, v ([n_tokens,
+    kv_heads, d]), rows contiguous, packed by sequence (starts int32 [n_seqs + 1]).  Returns out
+    (bf16, like q), or (out, lse) with want_lse or an lse tensor (fp32 [n_tokens, heads])."""
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError(f"q: must be a GPU tensor, got {dev}")
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return prompt_attend(q, k, v, starts, out, lse, want_lse, scale)
+    if k.dim() != 3 or starts.dim() != 1 or starts.shape[0] < 1 or k.shape[1] < 1:
+        raise ValueError("k: 3 dimensions and a head expected, starts: 1 dimension with an entry")
+    G = _group(q, k.shape[1], "q")
+    n, heads, d = q.shape
+    kv = (n, k.shape[1], d)
+    cq, ck, cv = _rows(q, q.shape, dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
+    st_ptr = _at(starts, _I32, starts.shape, dev, "starts")
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=q.dtype, device=dev)
+    co = _rows(out, q.shape, dev, "out")
+    lse, lse_ptr = (_new(q, (n, heads), torch.float32) if lse is None and want_lse else
+                    _given(lse, _F32, (n, heads), dev, "lse"))
+    rc = lib().kvc_prompt_attend(_int(starts.shape[0] - 1, "n_seqs"), _int(kv[1], "kv_heads"), G,
+                                 _int(d, "head_dim"), _int(n, "n_tokens"), st_ptr, _scale(scale),
+                                 _ref(cq), _ref(ck), _ref(cv), _ref(co), lse_ptr, s)
+    _check(rc, "kvc_prompt_attend")
+    return out if lse is None else (out, lse)
+
+
+def paged_evict(cache: PagedCache, seen, budget: int, sinks: int = 4, recent: int = 64, ws=None,
+                stream=None):
+    """Cuts every sequence to `budget` slots a head: positions below sinks, the last
+    `recent` of the seen ones (int32 [n_seqs]), then the largest weights.  Returns the cache."""
+    dev = cache.device
+    s = _here(dev, stream)
+    if s is None:
+        with _there(dev, stream):
+            return paged_evict(cache, seen, budget, sinks, recent, ws)
+    if cache.weight is None:
+        raise ValueError("cache: has no weight and pos")
+    seen_ptr = _at(seen, _I32, cache.seq_len.shape, dev, "seen")
+    ws = _scratch(ws, cache.evict_workspace_bytes(budget), dev)
+    rc = lib().kvc_paged_evict(cache._ref, seen_ptr, _int(budget, "budget"), _int(sinks, "sinks"),
+                               _int(recent, "recent"), *_span(ws), s)
+    _check(rc, "kvc_paged_evict")
+    return cache

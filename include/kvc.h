@@ -475,6 +475,11 @@ int kvc_pages_fork(const kvc_page_table* t, int32_t n_pairs, const int32_t* src,
  * entries become -1, their lengths 0.  No workspace. */
 int kvc_pages_free(const kvc_page_table* t, int32_t n_ids, const int32_t* ids, void* stream);
 
+/* Gives up what lies behind the lengths (after an eviction): every entry past the
+ * ceil(seq_len / block_size) first ones of its sequence that names a page becomes
+ * -1, and the page loses one count.  No workspace. */
+int kvc_pages_trim(const kvc_page_table* t, void* stream);
+
 /* Copies page src[i] to page dst[i] in every buffer, i < n_pairs (i32 on the
  * device; a pair with an id outside [0, n_blocks) is skipped).  Precondition:
  * the destinations are distinct and none of them is a source.  No
@@ -496,6 +501,140 @@ int kvc_pages_compact(const kvc_page_table* t, const kvc_page_buffer* bufs, int3
 /* Workspace bytes kvc_pages_alloc, kvc_pages_fork (with up to n_pairs pairs)
  * and kvc_pages_compact need; 0 for invalid arguments.  Pure host function. */
 size_t kvc_pages_workspace_bytes(const kvc_page_table* t, int32_t n_pairs);
+
+/* ---------------------------------------------------------------------------
+ * bf16 paged cache: the pages of kvc_gather_paged with the rotation, append,
+ * attention and eviction that a serving loop runs on them.
+ *
+ * Layout: k_pool, v_pool bf16 [n_blocks][kv_heads][block_size][head_dim]
+ * (16-byte aligned), table i32 [n_seqs][table_blocks], seq_len i32 [n_seqs]
+ * (device arrays).  Slot t of sequence b lives in page table[b][t / block_size],
+ * row t % block_size.  A table entry outside [0, n_blocks) names no page: its
+ * slots are not attended and not written.  seq_len is taken as clamped to
+ * [0, cap] with cap = min(max_len, table_blocks * block_size) (max_len 0: the
+ * second).  Rows of slots at or past seq_len may hold anything.
+ * weight, pos (both or neither; f32 and i32 [n_seqs * kv_heads][table_blocks *
+ * block_size]): what each slot of each head has received from the attention so
+ * far, and the position in the text that it holds (an eviction leaves other
+ * positions to each head, in any order).
+ * Preconditions (not checked): the rows of attended slots are finite, and a page
+ * that is written belongs to one entry of the table. */
+typedef struct kvc_paged_cache {
+  int32_t n_seqs;        /* B sequences; 0 = nothing to do                   */
+  int32_t kv_heads;      /* H KV heads, n_seqs * kv_heads < 2^24             */
+  int32_t head_dim;      /* d, 64 or 128                                     */
+  int32_t block_size;    /* slots per page, 1..4096                          */
+  int32_t table_blocks;  /* table entries per sequence (>= 1),
+                            table_blocks * block_size <= 2^30                */
+  int32_t max_len;       /* 0, or a bound on seq_len that sizes the launches */
+  int64_t n_blocks;      /* pages in the pools, n_blocks * kv_heads *
+                            block_size < 2^32 - 1                            */
+  void* k_pool;
+  void* v_pool;
+  const int32_t* table;
+  int32_t* seq_len;      /* written by kvc_paged_evict only                  */
+  float* weight;
+  int32_t* pos;
+} kvc_paged_cache;
+
+/* Rows of new tokens: value i of head h of token t is the bf16 at data +
+ * t * token_stride + h * head_stride + i (strides in values, multiples of 8, data
+ * 16-byte aligned).  Rows that are written must not share values: either every
+ * token's heads or every head's tokens lie apart.  An input's strides may be 0.
+ * n_tokens: 0..2^23, n_tokens * heads below 2^30.
+ *
+ * Packed sequences: starts i32 [n_seqs + 1] on the device, ascending from 0;
+ * sequence b's new tokens are tokens starts[b]..starts[b+1]-1 and hold its last
+ * slots (seq_len counts them already).  Tokens from starts[n_seqs] on are
+ * nobody's: their rows of the outputs are left as they were. */
+typedef struct kvc_rows {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} kvc_rows;
+
+/* Rotary positions: with a = position * freq[i], i < r / 2, r = rot_dim, a pair
+ * (x0, x1) becomes mscale * (x0 cos a - x1 sin a, x1 cos a + x0 sin a).  The pairs
+ * are values (i, i + r/2) of a row, or (2i, 2i + 1) when interleaved; values from
+ * r on are copied.  Angles in fp64, the rest in fp32, rounded once. */
+typedef struct kvc_rope_plan {
+  const double* freq;    /* f64 [rot_dim / 2] on the device, radians a position */
+  int32_t rot_dim;       /* r, even, 2..head_dim                             */
+  int32_t interleaved;   /* 0 or 1                                           */
+  float mscale;          /* finite                                           */
+  int32_t reserved;      /* 0                                                */
+} kvc_rope_plan;
+
+/* Rotates x into y (which may be x itself: same data and strides), heads 1..2^16.
+ * positions: i32 [n_tokens] on the device.  backward 1:
+ * by the transposed map, mscale * (x0 cos a + x1 sin a, x1 cos a - x0 sin a): the
+ * gradient, or with mscale 1 the rows as they were before the rotation.  No
+ * workspace. */
+int kvc_rope(int32_t n_tokens, int32_t heads, int32_t head_dim, const kvc_rope_plan* rope,
+             int32_t backward, const int32_t* positions, const kvc_rows* x, const kvc_rows* y,
+             void* stream);
+
+/* Appends: k, v ([n_tokens][kv_heads][d]) of the new tokens go into their slots, k
+ * rotated by rope (NULL: as it is).  positions: i32 [n_tokens], or NULL: each
+ * token's position is its slot.  q (NULL, or [n_tokens][group * kv_heads][d],
+ * with rope only) is rotated into q_out in the same launch.  In a cache
+ * with weight and pos the slots start at weight 0 and hold the tokens'
+ * positions.  A token whose slot is negative or in no page is not written (its q
+ * is rotated all the same).  group is looked at with q only, 1..64.  No workspace. */
+int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* starts,
+                     const int32_t* positions, const kvc_rope_plan* rope, int32_t group,
+                     const kvc_rows* q, const kvc_rows* q_out, const kvc_rows* k,
+                     const kvc_rows* v, void* stream);
+
+/* Attention of the new tokens over the cache: query head h * group + g of token i
+ * of sequence b, in slot t_i = seq_len - n_new + i, attends to slots 0..t_i of KV
+ * head h:  out = sum_t softmax_t(scale * <q, k[t]>) * v[t].  q, out: [n_tokens]
+ * [group * kv_heads][d]; lse: optional f32 [n_tokens][group * kv_heads], log(sum_t
+ * exp(scale * <q, k[t]>)).  In a cache with weight and pos, weight[t] of each KV head
+ * grows by the softmax weights that slot t receives, summed over the new tokens
+ * and the group.  fp32 softmax; weights enter the product with V as bf16, whose
+ * step is 2^-8 of each.  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.
+ * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
+ * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
+ * (a sequence with more counts its first max_new).  group 1..64.  Preconditions (not
+ * checked): q is finite, so are scores times log2(e) in fp32.  A head's results depend on its own length, queries
+ * and slots alone.  ws: at least kvc_paged_attend_workspace_bytes(c, group,
+ * n_tokens, max_new), 256-byte aligned (may be NULL when that is 0). */
+int kvc_paged_attend(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int32_t max_new,
+                     const int32_t* starts, float scale, const kvc_rows* q, const kvc_rows* out,
+                     float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes kvc_paged_attend needs; (size_t)-1 for invalid arguments (of
+ * the device pointers only weight is looked at, for being NULL).  Pure host
+ * function. */
+size_t kvc_paged_attend_workspace_bytes(const kvc_paged_cache* c, int32_t group,
+                                        int32_t n_tokens, int32_t max_new);
+
+/* Causal attention within packed prompts, without a cache: token i of a sequence
+ * attends to its tokens 0..i.  q, out: [n_tokens][group * kv_heads][d], k, v:
+ * [n_tokens][kv_heads][d], otherwise as kvc_paged_attend.  k and v finite.
+ * kv_heads 1..65536, n_seqs * kv_heads < 2^22.  No workspace. */
+int kvc_prompt_attend(int32_t n_seqs, int32_t kv_heads, int32_t group, int32_t head_dim,
+                      int32_t n_tokens, const int32_t* starts, float scale, const kvc_rows* q,
+                      const kvc_rows* k, const kvc_rows* v, const kvc_rows* out, float* lse,
+                      void* stream);
+
+/* Evicts: every sequence longer than budget keeps budget slots of each head: first
+ * those of positions below sinks (lower ones first), then those of the last
+ * `recent` of its seen[b] positions (later ones first), then by weight, ties to
+ * the lower position (a NaN weight counts as -inf).  seen: i32 [n_seqs] on the
+ * device, positions so far; positions of a head are distinct, 0..2^30-1.  Kept slots at
+ * or past budget move, in ascending order, to the given-up slots below it, with
+ * their rows, weight and pos; slots from budget on are left as they were.
+ * seq_len becomes budget.  Needs weight and pos.  budget >= 1, sinks, recent >= 0.
+ * A move from or to a slot in no page carries weight and pos only.
+ * ws: at least kvc_paged_evict_workspace_bytes(c, budget), 256-byte aligned. */
+int kvc_paged_evict(const kvc_paged_cache* c, const int32_t* seen, int32_t budget, int32_t sinks,
+                    int32_t recent, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes kvc_paged_evict needs; 0 for invalid arguments.  Pure host
+ * function. */
+size_t kvc_paged_evict_workspace_bytes(const kvc_paged_cache* c, int32_t budget);
 
 /* Workspace bytes any entry point that takes a kvc_params needs for these parameters (0 when
  * the parameters are invalid).  Pure host function. */

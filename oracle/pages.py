@@ -109,3 +109,12 @@ def compact(t: Pages):
         refs[remap[p]] = t.refs[p]
     table = np.array([[remap[p] if t.ok(p) else -1 for p in row] for row in t.table], np.int32)
     return table.reshape(t.table.shape), refs, remap, n, [(m, to[m]) for m in movers]
+
+
+def trim(t: Pages):
+    for b in range(t.B):
+        first = -(-max(int(t.lens[b]), 0) // t.bs)
+        for j in range(first, t.tb):
+            if t.ok(t.table[b, j]):
+                t.refs[t.table[b, j]] -= 1
+                t.table[b, j] = -1
