@@ -48,6 +48,8 @@ struct Args {
   int n0;            // first head of this launch
   float* part;       // [n][row][piece][D] outputs of a piece
   float* stat;       // [n][row][piece] log2 of its sum of 2^x
+  float* scores;     // NULL, or [n][row][score_stride] x
+  int score_stride;
 };
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -101,7 +103,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
 
   const int2 mine = chunk_of(A.a.k, b);
   const int R = mine.y * A.a.G, row0 = rb * MT * 16;
-  if (row0 >= R) return;
+  if (row0 >= R || R > kFewRows) return;
   const int len = paged_len(c, b);
   const int chunk = few_chunk(len);
   const int t0 = piece * chunk;
@@ -206,6 +208,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
 #pragma unroll
         for (int u = 0; u < kVWords; ++u)
           if (tile + at >= keys || gone) x.v[j][u] = 0;
+      }
+    }
+    if (A.scores) {  // for the sums of the weights, once the rows' sums are known
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int r = row0 + mt * 16 + col;
+        if (r < R) {
+          float* to = A.scores + (size_t(n) * A.rows + r) * A.score_stride + t0 + tile + 4 * g;
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            *reinterpret_cast<f32x4*>(to + half * 16) =
+                f32x4{y[mt][half * 4] * by, y[mt][half * 4 + 1] * by, y[mt][half * 4 + 2] * by, y[mt][half * 4 + 3] * by};
+        }
       }
     }
     u32x4 w[MT];
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(kThreads) void k_join_few(Args A) {
   const int r = int(blockIdx.x) - nth * A.rows;
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
   const int2 mine = chunk_of(A.a.k, b);
-  if (r >= mine.y * A.a.G) return;
+  if (r >= mine.y * A.a.G || mine.y * A.a.G > kFewRows) return;
   const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
   if (len <= chunk) return;
   const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
@@ -386,32 +401,38 @@ void attend_rows(const Args& A, hipStream_t s) {
   }
 }
 
-// The column sums of the softmax weights, one thread a slot.
-__global__ __launch_bounds__(kThreads) void k_weights(AttendCall a, const float* lse) {
-  const Paged& c = a.c;
-  const float by = a.c_log2;
+// What each slot receives from a sequence's few rows: the sum down the rows of
+// 2^(x - log2 of the row's sum), four slots a thread.  The scores come from the first
+// kernel (4 bytes a row and slot; the keys would be 2 * d bytes a slot again).
+__global__ __launch_bounds__(kThreads) void k_weights_few(Args A) {
+  __shared__ float base[kFewRows];
+  const Paged& c = A.a.c;
   for (int n = blockIdx.y; n < c.B * c.H; n += gridDim.y) {
-  const int b = n / c.H, h = n - b * c.H;
-  const int2 mine = chunk_of(a.k, b);
-  const int len = paged_len(c, b);
-  for (int t = blockIdx.x * kThreads + threadIdx.x; t < len; t += gridDim.x * kThreads) {
-    const int64_t row = paged_row(c, b, h, t);
-    if (row < 0) continue;
-    const uint16_t* kr = c.k + row * c.D;
-    float total = 0.0f;
-    int i0 = t - (len - mine.y);
-    for (int i = i0 < 0 ? 0 : i0; i < mine.y; ++i)
-      for (int g = 0; g < a.G; ++g) {
-        const int head = h * a.G + g;
-        const uint16_t* qr = a.q.p + int64_t(mine.x + i) * a.q.ts + int64_t(head) * a.q.hs;
-        float x = 0.0f;
-        for (int e = 0; e < c.D; ++e)
-          x = __builtin_fmaf(__uint_as_float(uint32_t(qr[e]) << 16), __uint_as_float(uint32_t(kr[e]) << 16), x);
-        const float z = lse[size_t(mine.x + i) * (a.G * c.H) + head];
-        total += fast_exp2(__builtin_fmaf(x, by, -z * 1.4426950408889634f));
+    const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
+    const int2 mine = chunk_of(A.a.k, b);
+    const int R = mine.y * A.a.G, len = paged_len(c, b);
+    if (R > kFewRows || R == 0) continue;          // the same for the whole workgroup
+    __syncthreads();
+    if (threadIdx.x < R) {
+      const int i = int(quot(A.by_G, threadIdx.x));
+      const float z = A.a.lse[size_t(mine.x + i) * (A.a.G * c.H) + h * A.a.G + int(threadIdx.x) - i * A.a.G];
+      base[threadIdx.x] = z == -INFINITY ? -INFINITY : -z * 1.4426950408889634f;   // a row that sees nothing gives nothing
+    }
+    __syncthreads();
+    const float* x = A.scores + size_t(n) * A.rows * A.score_stride;
+    float* to = c.weight + size_t(n) * c.room;
+    for (int t = (blockIdx.x * kThreads + threadIdx.x) * 4; t < len; t += gridDim.x * kThreads * 4) {
+      f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
+      for (int r = 0; r < R; ++r) {
+        const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride + t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + base[r]);
       }
-    c.weight[size_t(n) * c.room + t] += total;
-  }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (t + i < len && sum[i] > 0.0f) to[t + i] += sum[i];
+    }
   }
 }
 
@@ -425,11 +446,17 @@ AttendWs attend_ws(const Paged& c, const Chunks& k, int G) {
     off = (off + n + 63) & ~size_t(63);
     return at;
   };
-  w.few_rows = G * k.max_new;
+  w.few_rows = int64_t(G) * k.max_new < kFewRows ? G * k.max_new : kFewRows;
   w.few_pieces = few_max_pieces(c.cap);
   const size_t n = w.few_pieces > 1 ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : 0;
   w.few_part = take(n * c.D);
   w.few_stat = take(n);
+  w.score_stride = (c.cap + 31) & ~31;
+  w.scores = take(c.weight ? size_t(c.B) * c.H * w.few_rows * w.score_stride : 0);
+  w.slots = int64_t(G) * k.max_new > kFewRows ? first_slot(k.n_tokens, c.B, G) + 1 : 0;
+  const size_t m = tile_max_pieces(c.cap) > 1 ? size_t(c.H) * w.slots * kTileRows : 0;
+  w.part = take(m * c.D);
+  w.stat = take(m);
   w.lse = take(c.weight ? size_t(k.n_tokens) * G * c.H : 0);
   w.total = off;
   return w;
@@ -448,11 +475,19 @@ hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
   A.by_rows = fast_div(uint32_t(A.rows));
   A.part = ws + w.few_part;
   A.stat = ws + w.few_stat;
+  A.scores = a.c.weight ? ws + w.scores : nullptr;
+  A.score_stride = w.score_stride;
   if (a.c.D == 128) attend_rows<128>(A, s);
   else attend_rows<64>(A, s);
+  if (w.slots > 0) {
+    AttendCall t = a;
+    t.lse = A.a.lse;
+    const hipError_t e = launch_attend_tiles(t, ws + w.part, ws + w.stat, w.slots, s);
+    if (e != hipSuccess) return e;
+  }
   if (a.c.weight) {
-    const int blocks = (a.c.cap + kThreads - 1) / kThreads;
-    k_weights<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), unsigned(a.c.B * a.c.H < 32768 ? a.c.B * a.c.H : 32768)), kThreads, 0, s>>>(A.a, A.a.lse);
+    const int heads = a.c.B * a.c.H, blocks = (a.c.cap + kThreads * 4 - 1) / (kThreads * 4);
+    k_weights_few<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), unsigned(heads < 32768 ? heads : 32768)), kThreads, 0, s>>>(A);
   }
   return hipGetLastError();
 }

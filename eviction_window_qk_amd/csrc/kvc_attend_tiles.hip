@@ -32,26 +32,35 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
-constexpr int kRows = kWaves * 32;   // rows of a workgroup
+constexpr int kRows = kTileRows;     // rows of a workgroup, 32 a wave
 constexpr int kTile = 64;            // keys of a tile
 constexpr int kXcds = 8;
 constexpr float kFar = 0x1p64f;      // -m of a row that has seen nothing
+static_assert(kRows == kWaves * 32, "32 rows a wave");
 
 struct Args {
+  Paged c;            // of a call over a cache
   Chunks k;
   int G, H;
   float c_log2;
-  Rows q, kr, vr, out;
+  Rows q, kr, vr, out;  // kr, vr: keys and values of a call without a cache
   float* lse;
   FastDiv by_G;
-  int tiles;          // row tiles of the call, counting one spare a sequence
-  int parts, per;     // ways a head's row tiles are dealt out to the XCDs, tiles in each
+  int slots;          // workgroups of a head
+  int parts, per;     // ways a head's slots are dealt out to the XCDs, slots in each
   FastDiv by_per, by_parts;
+  float* part;        // [H][slots][kRows][D] outputs of a piece
+  float* stat;        // [H][slots][kRows] log2 of its sum of 2^x
 };
+
+// Rows past the end, or in no page, are read from here.
+__device__ const u32x4 zeros[16] = {};
 
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
@@ -84,48 +93,75 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
       u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at));
 }
 
-// What a row tile works on: its sequence, KV head and rows.
+// What a workgroup works on: its sequence, KV head, rows and piece of the keys.
 struct Where {
-  int b, h, r0, R;   // first row, rows of the sequence
-  int token0, n;     // first new token and their count
+  int b, h, slot;
+  int r0, R;          // first row, rows of the sequence
+  int token0, n;      // first new token and their count
+  int len;            // keys of the sequence
+  int piece, pieces, tiles;
 };
 
-// Row tiles are numbered through: those of sequence b start at floor(starts[b] * G /
-// kRows) + b, which leaves room for all of them.  Workgroups go to the XCDs in turn;
-// an XCD takes whole parts of heads (all tiles of one head, or every parts-th where
-// the heads do not fill the XCDs evenly), the last rows first: they see most keys.
+// A head's work is numbered through in slots, (piece, row tile) pairs: those of
+// sequence b start at first_slot, which leaves room for all of them.  Workgroups go to
+// the XCDs in turn; an XCD takes whole parts of heads (all slots of one head, or every
+// parts-th where the heads do not fill the XCDs evenly), the last rows first: they see
+// most keys.  The row tiles of a piece follow each other on one XCD, whose L2 then reads
+// the keys once.
+template <bool PAGED>
 __device__ __forceinline__ bool find(const Args& A, Where& w) {
   const uint32_t x = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
   const uint32_t nth = quot(A.by_per, i);
   const uint32_t unit = nth * kXcds + x;                 // (head, part)
   const uint32_t h = quot(A.by_parts, unit);
   if (h >= uint32_t(A.H)) return false;
-  const int tile = A.tiles - 1 - (int(i - nth * A.per) * A.parts + int(unit - h * A.parts));
-  if (tile < 0) return false;
+  const int at = int(i - nth * A.per) * A.parts + int(unit - h * A.parts);
+  w.slot = A.slots - 1 - at;
+  if (w.slot < 0) return false;
   const int G = A.G;
-  const auto first = [G](int s, int b) { return int(int64_t(s) * G / kRows) + b; };
-  w.b = last_at_or_below(A.k.starts, A.k.B, tile, first);
+  const auto first = [G](int s, int b) { return PAGED ? first_slot(s, b, G) : first_tile(s, b, G); };
+  w.b = last_at_or_below(A.k.starts, A.k.B, w.slot, first);
   const int2 mine = chunk_of(A.k, w.b);
   w.h = int(h);
   w.token0 = mine.x;
   w.n = mine.y;
   w.R = mine.y * G;
-  w.r0 = (tile - first(A.k.starts[w.b], w.b)) * kRows;
-  return w.r0 >= 0 && w.r0 < w.R;
+  const int s = w.slot - first(A.k.starts[w.b], w.b);
+  w.tiles = (w.R + kRows - 1) / kRows;
+  if (PAGED) {
+    if (w.R <= kFewRows || s < 0) return false;
+    w.len = paged_len(A.c, w.b);
+    w.pieces = tile_pieces(w.len, w.tiles);
+    w.piece = s / w.tiles;
+    if (w.piece >= w.pieces || w.slot - s + w.tiles * w.pieces > A.slots) return false;
+    w.r0 = (s - w.piece * w.tiles) * kRows;
+    return true;
+  }
+  w.len = w.n;
+  w.piece = 0;
+  w.pieces = 1;
+  w.r0 = s * kRows;
+  return s >= 0 && w.r0 < w.R;
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void k_prompt(Args A) {
+// GROUP: keys that a look-up in the table covers, of a wave's load all where pages hold
+// whole loads, or one; 0: no cache.
+template <int D, int GROUP>
+__global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
+  constexpr bool PAGED = GROUP != 0;
   constexpr int kPieces = D / 8;             // 16-byte pieces of a row
   constexpr int kRowsPerLoad = 64 / kPieces; // rows one wave's load covers
   constexpr int kLoads = kTile / kWaves / kRowsPerLoad;
   constexpr int kSteps = D / 16;             // matrix steps over the head dimension
   constexpr int kDims = D / 32;              // 32-value blocks of the output
+  constexpr int kPerTile = PAGED ? kTile / GROUP : 1;    // look-ups of a tile
+  constexpr int kBatch = PAGED ? 64 / kPerTile : 1;      // tiles that a wave's 64 look-ups cover
+  static_assert(GROUP == 0 || GROUP == 1 || GROUP == kRowsPerLoad, "a load's rows, or one");
   __shared__ __align__(16) uint16_t ks[2][kTile * D];
   __shared__ __align__(16) uint16_t vs[2][kTile * D];
 
   Where w;
-  if (!find(A, w)) return;
+  if (!find<PAGED>(A, w)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 31, hh = lane >> 5;
@@ -133,29 +169,62 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt(Args A) {
   const int rc = r < w.R ? r : w.R - 1;      // rows that are none repeat the last one, never written
   const int i = int(quot(A.by_G, uint32_t(rc)));
   const int head = w.h * A.G + rc - i * A.G;
-  const int limit = i;                       // last key this row sees
+  const int limit = w.len - w.n + i;         // last key this row sees
   const int low = __builtin_amdgcn_readfirstlane(limit);
   const int high = __builtin_amdgcn_readlane(limit, 31);
   const int last_row = w.r0 + kRows <= w.R ? w.r0 + kRows - 1 : w.R - 1;
-  const int keys = int(quot(A.by_G, uint32_t(last_row))) + 1;   // that any row of the tile sees
+  // Keys that any row of the tile sees, of these the piece's.
+  const int seen = w.len - w.n + int(quot(A.by_G, uint32_t(last_row))) + 1;
+  const int span = PAGED ? tile_span(w.len, w.pieces) : 0;
+  const int from = w.piece * span;
+  const int to = PAGED && from + span < seen ? from + span : seen;
 
   u32x4 qf[kSteps];
   const uint16_t* qp = A.q.p + int64_t(w.token0 + i) * A.q.ts + int64_t(head) * A.q.hs + hh * 8;
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) qf[s] = *reinterpret_cast<const u32x4*>(qp + s * 16);
 
+  // Where the keys are.  Without a cache, rows past the sequence's end repeat its last
+  // one: they are in bounds, and no row sees them.  In a cache a wave's 64 lanes look up
+  // kBatch tiles at a time, one batch ahead: the row in the pools, or kNone.
+  constexpr uint32_t kNone = 0xffffffffu;
   const uint16_t* kb = A.kr.p + int64_t(w.token0) * A.kr.ts + int64_t(w.h) * A.kr.hs;
   const uint16_t* vb = A.vr.p + int64_t(w.token0) * A.vr.ts + int64_t(w.h) * A.vr.hs;
-  // Rows past the sequence's end repeat its last one: they are in bounds, and no row
-  // sees them.
-  auto fetch = [&](int t0, int buf) {
+  uint32_t rows = kNone, rows_next = kNone;
+  auto look_up = [&](int t) {                // of the batch that starts at key t
+    const int key = t + lane * (PAGED ? GROUP : 1);
+    if (key >= w.len) return kNone;
+    const int64_t at = paged_row(A.c, w.b, w.h, key);
+    return at < 0 ? kNone : uint32_t(at);
+  };
+  auto fetch = [&](int t0, int nth, uint32_t of, int buf) {   // nth: tile of the batch
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
       const int first = wave * (kTile / kWaves) + x * kRowsPerLoad, row = first + lane / kPieces;
-      const int t = t0 + row < w.n ? t0 + row : w.n - 1;
       const int piece = (lane % kPieces) ^ swizzle<D>(row);
-      to_lds(kb + int64_t(t) * A.kr.ts + piece * 8, ks[buf] + first * D);
-      to_lds(vb + int64_t(t) * A.vr.ts + piece * 8, vs[buf] + first * D);
+      if constexpr (!PAGED) {
+        const int t = t0 + row < w.n ? t0 + row : w.n - 1;
+        to_lds(kb + int64_t(t) * A.kr.ts + piece * 8, ks[buf] + first * D);
+        to_lds(vb + int64_t(t) * A.vr.ts + piece * 8, vs[buf] + first * D);
+      } else if constexpr (GROUP > 1) {
+        const uint32_t at = __builtin_amdgcn_readlane(of, nth * kPerTile + first / GROUP);
+        if (at != kNone && t0 + first + GROUP <= w.len) {
+          to_lds(A.c.k + size_t(at) * D + (lane / kPieces) * D + piece * 8, ks[buf] + first * D);
+          to_lds(A.c.v + size_t(at) * D + (lane / kPieces) * D + piece * 8, vs[buf] + first * D);
+        } else {   // rows past the end may hold anything, and nothing times a NaN is one
+          const uint16_t* z = reinterpret_cast<const uint16_t*>(zeros);
+          const size_t inner = size_t(at) * D + (lane / kPieces) * D;
+          const bool in = at != kNone && t0 + row < w.len;
+          to_lds((in ? A.c.k + inner : z) + piece * 8, ks[buf] + first * D);
+          to_lds((in ? A.c.v + inner : z) + piece * 8, vs[buf] + first * D);
+        }
+      } else {
+        const uint32_t at = uint32_t(__shfl(int(of), row));
+        const uint16_t* kp = at == kNone ? reinterpret_cast<const uint16_t*>(zeros) : A.c.k + size_t(at) * D;
+        const uint16_t* vp = at == kNone ? reinterpret_cast<const uint16_t*>(zeros) : A.c.v + size_t(at) * D;
+        to_lds(kp + piece * 8, ks[buf] + first * D);
+        to_lds(vp + piece * 8, vs[buf] + first * D);
+      }
     }
   };
 
@@ -165,13 +234,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt(Args A) {
   float nm = kFar, l = 0.0f;
   const float by = A.c_log2;
 
-  fetch(0, 0);
-  const int n_tiles = (keys + kTile - 1) / kTile;
+  const int n_tiles = to > from ? (to - from + kTile - 1) / kTile : 0;
+  if (PAGED) rows = look_up(from);
+  if (n_tiles > 0) fetch(from, 0, rows, 0);
+  if (PAGED && n_tiles > kBatch) rows_next = look_up(from + kBatch * kTile);
+  uint64_t none = 0;                         // look-ups of the batch in work that found nothing
   for (int tile = 0; tile < n_tiles; ++tile) {
-    const int t0 = tile * kTile;
+    const int t0 = from + tile * kTile;
+    uint32_t gone = 0;                       // GROUP > 1: those of this tile
+    uint64_t gone1 = 0;                      // GROUP 1
+    if constexpr (PAGED) {
+      const int nth = tile % kBatch;
+      if (nth == 0) none = __ballot(rows == kNone);
+      if constexpr (GROUP > 1) gone = uint32_t(none >> (nth * kPerTile)) & ((1u << kPerTile) - 1);
+      else gone1 = none;
+    }
     __builtin_amdgcn_s_waitcnt(0);           // this tile's loads, one tile old
     __syncthreads();
-    if (tile + 1 < n_tiles) fetch(t0 + kTile, (tile + 1) & 1);
+    if (tile + 1 < n_tiles) {
+      const int nth = (tile + 1) % kBatch;
+      if (PAGED && nth == 0) {
+        rows = rows_next;
+        if (tile + 1 + kBatch < n_tiles) rows_next = look_up(t0 + kTile + kBatch * kTile);
+      }
+      fetch(t0 + kTile, nth, rows, (tile + 1) & 1);
+    }
     if (t0 > high) continue;                 // no row of this wave sees it
     const uint16_t* kt = ks[tile & 1];
     const uint16_t* vt = vs[tile & 1];
@@ -186,13 +273,21 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt(Args A) {
         sc[blk] = mfma(*reinterpret_cast<const u32x4*>(kt + row * D + place * 8), qf[s], sc[blk]);
       }
     }
-    if (t0 + kTile - 1 > low) {
+    if (t0 + kTile - 1 > low || gone != 0 || gone1 != 0) {
       const int d = limit - t0 - 4 * hh;
+      // bit k / GROUP: key k + 4 hh of the tile
+      const uint32_t g_lane = GROUP == 4 ? gone >> hh : gone;
+      const uint64_t g_one = gone1 >> (4 * hh);
 #pragma unroll
       for (int blk = 0; blk < 2; ++blk)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (blk * 32 + 8 * (e >> 2) + (e & 3) > d) sc[blk][e] = -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+          const int k = blk * 32 + 8 * (e >> 2) + (e & 3);
+          bool out = k > d;
+          if constexpr (GROUP > 1) out |= (g_lane >> (k / GROUP)) & 1;
+          if constexpr (GROUP == 1) out |= (g_one >> k) & 1;
+          if (out) sc[blk][e] = -INFINITY;
+        }
     }
     float p[32], sum = 0.0f;
     auto weigh = [&]() {
@@ -242,31 +337,205 @@ __global__ __launch_bounds__(kThreads, 2) void k_prompt(Args A) {
   if (r >= w.R) return;
   const bool any = l > 0.0f;
   const float by_l = any ? 1.0f / l : 0.0f;
-  uint16_t* to = A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs;
+  const float b_sum = any ? fast_log2(l) - nm : -INFINITY;   // log2 of the row's sum of 2^x
+  if (PAGED && w.pieces > 1) {
+    const size_t row = (size_t(w.h) * A.slots + w.slot) * kRows + (r - w.r0);
+    float* po = A.part + row * D;
+#pragma unroll
+    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * e + 4 * hh) =
+            f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * by_l;
+    if (hh == 0) A.stat[row] = b_sum;
+    return;
+  }
+  uint16_t* po = A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs;
 #pragma unroll
   for (int d = 0; d < kDims; ++d)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<u16x4*>(to + 32 * d + 8 * e + 4 * hh) =
+      *reinterpret_cast<u16x4*>(po + 32 * d + 8 * e + 4 * hh) =
           u16x4{to_bf16(acc[d][4 * e] * by_l), to_bf16(acc[d][4 * e + 1] * by_l),
                 to_bf16(acc[d][4 * e + 2] * by_l), to_bf16(acc[d][4 * e + 3] * by_l)};
   if (A.lse && hh == 0)
-    A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] =
-        any ? (fast_log2(l) - nm) * 0.6931471805599453f : -INFINITY;
+    A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] = b_sum * 0.6931471805599453f;
 }
 
-// Row tiles, and how the heads' are dealt out to the XCDs.
-void deal(Args& A) {
-  A.tiles = int(int64_t(A.k.n_tokens) * A.G / kRows) + A.k.B;
+// Joins the pieces of 1024 / D rows, each weighted by its sum, four values a lane.
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_join_tiles(Args A) {
+  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+  Where w;
+  if (!find<true>(A, w) || w.piece != 0 || w.pieces == 1) return;
+  const int r = w.r0 + int(blockIdx.y) * kAtOnce + int(threadIdx.x) / kLanes, dim = threadIdx.x % kLanes * 4;
+  if (r >= w.R) return;
+  const size_t row = (size_t(w.h) * A.slots + w.slot) * kRows + (r - w.r0);
+  const size_t step = size_t(w.tiles) * kRows;           // from piece to piece
+  float M = -INFINITY;
+  for (int p = 0; p < w.pieces; ++p) M = fmaxf(M, A.stat[row + p * step]);
+  const float base = M == -INFINITY ? 0.0f : M;
+  float L = 0.0f;
+  f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int p = 0; p < w.pieces; ++p) {
+    const float f = fast_exp2(A.stat[row + p * step] - base);
+    sum += *reinterpret_cast<const f32x4*>(A.part + (row + p * step) * D + dim) * f;
+    L += f;
+  }
+  const float by_l = L > 0.0f ? 1.0f / L : 0.0f;
+  const int i = int(quot(A.by_G, uint32_t(r))), head = w.h * A.G + r - i * A.G;
+  *reinterpret_cast<u16x4*>(A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs + dim) =
+      u16x4{to_bf16(sum.x * by_l), to_bf16(sum.y * by_l), to_bf16(sum.z * by_l), to_bf16(sum.w * by_l)};
+  if (A.lse && dim == 0)
+    A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] =
+        L > 0.0f ? (base + fast_log2(L)) * 0.6931471805599453f : -INFINITY;
+}
+
+// Column sums of the softmax weights of sequences with many rows: keys stationary, 64 a
+// wave as the second operand of S = Q K', query rows streamed through LDS 64 at a time.
+// The accumulator gives a lane one key and 16 rows, so the sum down the rows is
+// lane-local; its order is fixed.
+constexpr int kKeys = kWaves * 64;
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int chunks, int unit0, int units) {
+  constexpr int kPieces = D / 8;
+  constexpr int kRowsPerLoad = 64 / kPieces;
+  constexpr int kLoads = kTile / kWaves / kRowsPerLoad;
+  constexpr int kSteps = D / 16;
+  __shared__ __align__(16) uint16_t qs[2][kTile * D];
+  __shared__ __align__(16) float bs[2][kTile];           // -log2 of the rows' sums
+  __shared__ int lim[2][kTile];                          // the rows' last keys
+  const int unit = unit0 + int(blockIdx.x);
+  if (unit >= units) return;
+  const int n = int(quot(by_chunks, uint32_t(unit))), b = n / A.H, h = n - b * A.H;
+  const int2 mine = chunk_of(A.k, b);
+  const int R = mine.y * A.G, len = paged_len(A.c, b);
+  if (R <= kFewRows) return;
+  const int t0 = (unit - n * chunks) * kKeys;
+  if (t0 >= len) return;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int j = lane & 31, hh = lane >> 5;
+  const int key0 = t0 + wave * 64;
+  u32x4 kf[2][kSteps];
+  bool there[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int t = key0 + x * 32 + j;
+    const int64_t row = t < len ? paged_row(A.c, b, h, t) : -1;
+    there[x] = row >= 0;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      kf[x][s] = there[x] ? *reinterpret_cast<const u32x4*>(A.c.k + row * D + s * 16 + hh * 8) : u32x4{0, 0, 0, 0};
+  }
+  // Rows that see any of the keys: from the first token whose slot is at or past t0.
+  const int first_new = len - mine.y;
+  const int tok = t0 > first_new ? t0 - first_new : 0;
+  const int r_from = tok * A.G, n_tiles = (R - r_from + kTile - 1) / kTile;
+  auto fetch = [&](int tile, int buf) {
+    const int r0 = r_from + tile * kTile;
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) {
+      const int first = wave * (kTile / kWaves) + x * kRowsPerLoad, row = first + lane / kPieces;
+      const int r = r0 + row < R ? r0 + row : R - 1, i = int(quot(A.by_G, uint32_t(r)));
+      const int piece = (lane % kPieces) ^ swizzle<D>(row);
+      to_lds(A.q.p + int64_t(mine.x + i) * A.q.ts + int64_t(h * A.G + r - i * A.G) * A.q.hs + piece * 8, qs[buf] + first * D);
+    }
+    if (threadIdx.x < kTile) {
+      const int r = r0 + int(threadIdx.x), rc = r < R ? r : R - 1, i = int(quot(A.by_G, uint32_t(rc)));
+      const float z = A.lse[size_t(mine.x + i) * (A.G * A.H) + h * A.G + rc - i * A.G];
+      const bool any = r < R && z != -INFINITY;
+      bs[buf][threadIdx.x] = any ? -z * 1.4426950408889634f : 0.0f;
+      lim[buf][threadIdx.x] = any ? first_new + i : -1;
+    }
+  };
+  fetch(0, 0);
+  float total[2] = {0.0f, 0.0f};
+  const float by = A.c_log2;
+  for (int tile = 0; tile < n_tiles; ++tile) {
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    if (tile + 1 < n_tiles) fetch(tile + 1, (tile + 1) & 1);
+    const uint16_t* qt = qs[tile & 1];
+#pragma unroll
+    for (int blk = 0; blk < 2; ++blk) {
+      f32x16 sc[2] = {f32x16{}, f32x16{}};
+      const int row = blk * 32 + j;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const u32x4 qf = *reinterpret_cast<const u32x4*>(qt + row * D + (((2 * s + hh) ^ swizzle<D>(row)) << 3));
+        sc[0] = mfma(qf, kf[0][s], sc[0]);
+        sc[1] = mfma(qf, kf[1][s], sc[1]);
+      }
+#pragma unroll
+      for (int e4 = 0; e4 < 4; ++e4) {
+        const int at = blk * 32 + 8 * e4 + 4 * hh;
+        const f32x4 bz = *reinterpret_cast<const f32x4*>(&bs[tile & 1][at]);
+        const i32x4 lm = *reinterpret_cast<const i32x4*>(&lim[tile & 1][at]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float p = fast_exp2(__builtin_fmaf(sc[x][4 * e4 + e], by, bz[e]));
+            total[x] += key0 + x * 32 + j <= lm[e] ? p : 0.0f;
+          }
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    total[x] += __shfl_xor(total[x], 32);
+    if (hh == 0 && there[x]) A.c.weight[size_t(n) * A.c.room + key0 + x * 32 + j] += total[x];
+  }
+}
+
+// How the heads' slots are dealt out to the XCDs.  Returns the workgroups.
+unsigned deal(Args& A, int slots) {
+  A.slots = slots;
   A.parts = kXcds;
   for (int h = A.H; h % 2 == 0 && A.parts > 1; h /= 2) A.parts /= 2;
-  A.per = (A.tiles + A.parts - 1) / A.parts;
+  A.per = (slots + A.parts - 1) / A.parts;
   A.by_per = fast_div(uint32_t(A.per));
   A.by_parts = fast_div(uint32_t(A.parts));
   A.by_G = fast_div(uint32_t(A.G));
+  return unsigned((int64_t(A.H) * A.parts + kXcds - 1) / kXcds * kXcds * A.per);
+}
+
+template <int D>
+void attend_chunks(Args& A, hipStream_t s) {
+  const unsigned blocks = deal(A, A.slots);
+  if (A.c.bs % (512 / D) == 0) k_attend_tiles<D, 512 / D><<<blocks, kThreads, 0, s>>>(A);
+  else k_attend_tiles<D, 1><<<blocks, kThreads, 0, s>>>(A);
+  if (tile_max_pieces(A.c.cap) > 1)
+    k_join_tiles<D><<<dim3(blocks, kRows * D / 1024), kThreads, 0, s>>>(A);
+  if (!A.c.weight) return;
+  const int chunks = (A.c.cap + kKeys - 1) / kKeys;
+  const int heads = A.c.B * A.H, most = (1 << 23) / chunks > 0 ? (1 << 23) / chunks : 1;
+  for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
+    const int nh = heads - n0 < most ? heads - n0 : most;
+    k_weights_tiles<D><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), chunks, n0 * chunks, (n0 + nh) * chunks);
+  }
 }
 
 }  // namespace
+
+hipError_t launch_attend_tiles(const AttendCall& a, float* part, float* stat, int slots, hipStream_t s) {
+  Args A{};
+  A.c = a.c;
+  A.k = a.k;
+  A.G = a.G;
+  A.H = a.c.H;
+  A.c_log2 = a.c_log2;
+  A.q = a.q, A.out = a.out;
+  A.lse = a.lse;
+  A.part = part;
+  A.stat = stat;
+  A.slots = slots;
+  if (a.c.D == 128) attend_chunks<128>(A, s);
+  else attend_chunks<64>(A, s);
+  return hipGetLastError();
+}
 
 hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_log2, const Rows& q,
                                 const Rows& k_rows, const Rows& v_rows, const Rows& out,
@@ -278,10 +547,9 @@ hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_lo
   A.c_log2 = c_log2;
   A.q = q, A.kr = k_rows, A.vr = v_rows, A.out = out;
   A.lse = lse;
-  deal(A);
-  const unsigned blocks = unsigned((int64_t(H) * A.parts + kXcds - 1) / kXcds * kXcds * A.per);
-  if (D == 128) k_prompt<128><<<blocks, kThreads, 0, s>>>(A);
-  else k_prompt<64><<<blocks, kThreads, 0, s>>>(A);
+  const unsigned blocks = deal(A, int(int64_t(k.n_tokens) * G / kRows) + k.B);
+  if (D == 128) k_attend_tiles<128, 0><<<blocks, kThreads, 0, s>>>(A);
+  else k_attend_tiles<64, 0><<<blocks, kThreads, 0, s>>>(A);
   return hipGetLastError();
 }
 

@@ -108,6 +108,39 @@ inline int few_max_pieces(int cap) {
   return n > 64 ? n : 64;
 }
 
+// Sequences with at most kFewRows rows per KV head (rows: new tokens times group) are
+// attended by the kernel for few rows, the others by the one for tiles of kTileRows.
+constexpr int kFewRows = 32, kTileRows = 128;
+
+// Pieces that the keys of a sequence with `tiles` row tiles are cut into: about kTileWork
+// pairs of a tile and a piece for each KV head (eight heads then fill the chip once, two
+// workgroups a CU), pieces of at least kTileSpan keys.  The sequence's own length and row
+// count decide.
+constexpr int kTileWork = 64, kTileSpan = 512;
+__host__ __device__ inline int tile_pieces(int len, int tiles) {
+  const int most = (len + kTileSpan - 1) / kTileSpan, want = kTileWork / tiles;
+  const int n = want < most ? want : most;
+  return n < 1 ? 1 : n;
+}
+// Keys of a piece, whole tiles of 64: the last pieces may be empty.
+__host__ __device__ inline int tile_span(int len, int pieces) {
+  return ((len + pieces - 1) / pieces + 63) & ~63;
+}
+inline int tile_max_pieces(int cap) { return tile_pieces(cap, 1); }
+
+// Row tiles of packed sequences, numbered through: those of sequence b start here, and
+// floor((s + n) G / 128) - floor(s G / 128) + 1 leaves room for its ceil(n G / 128).
+__host__ __device__ inline int first_tile(int start, int b, int G) {
+  return int(int64_t(start) * G / kTileRows) + b;
+}
+// (piece, row tile) pairs of a head over a cache, numbered through: tiles * pieces <=
+// max(kTileWork, tiles).  Only a sequence of more than kFewRows rows has any, so b or
+// the count of so many rows before it, whichever is less, bounds those before it.
+__host__ __device__ inline int first_slot(int start, int b, int G) {
+  const int64_t rows = int64_t(start) * G, n = rows / (kFewRows + 1);
+  return int(rows / kTileRows + (kTileWork + 1) * (n < b ? n : int64_t(b)));
+}
+
 // A call of the attention over the cache.
 struct AttendCall {
   Paged c;
@@ -120,8 +153,10 @@ struct AttendCall {
 
 // Workspace carve-up, in floats.
 struct AttendWs {
-  size_t few_part, few_stat, lse, total;
-  int few_rows, few_pieces;
+  size_t few_part, few_stat, scores, part, stat, lse, total;
+  int few_rows, few_pieces;  // most rows of a head (at most kFewRows) and pieces
+  int slots;                 // first_slot behind the last token, 0: no sequence has many rows
+  int score_stride;          // keys of a row of scores
 };
 AttendWs attend_ws(const Paged& c, const Chunks& k, int G);
 
@@ -131,7 +166,8 @@ hipError_t launch_paged_append(const Paged& c, const Chunks& k, const int32_t* p
                                const RopePlan& f, int q_heads, const Rows& q, const Rows& q_out,
                                const Rows& k_new, const Rows& v_new, hipStream_t s);
 hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s);
-hipError_t launch_weights(const AttendCall& a, const float* lse, hipStream_t s);
+hipError_t launch_attend_tiles(const AttendCall& a, float* part, float* stat, int slots,
+                               hipStream_t s);
 hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_log2, const Rows& q,
                                 const Rows& k_rows, const Rows& v_rows, const Rows& out,
                                 float* lse, hipStream_t s);

@@ -129,6 +129,7 @@ int attend_shape(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int3
   if (group > 64) return KVC_EUNSUPPORTED;
   if (int64_t(n_tokens) * group * d->H >= (int64_t(1) << 30)) return KVC_EINVAL;
   *k = {nullptr, d->B, n_tokens, max_new > 0 && max_new < n_tokens ? max_new : n_tokens};
+  if (int64_t(first_slot(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23)) return KVC_EINVAL;  // workgroups of a launch
   return KVC_OK;
 }
 

@@ -596,8 +596,9 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
  * step is 2^-8 of each.  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.
  * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
  * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
- * (a sequence with more counts its first max_new).  group 1..64.  Preconditions (not
- * checked): q is finite, so are scores times log2(e) in fp32.  A head's results depend on its own length, queries
+ * (a sequence with more counts its first max_new).  group 1..64; kv_heads * (65 * n +
+ * n_tokens * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
+ * Preconditions (not checked): q is finite, so are scores times log2(e) in fp32.  A head's results depend on its own length, queries
  * and slots alone.  ws: at least kvc_paged_attend_workspace_bytes(c, group,
  * n_tokens, max_new), 256-byte aligned (may be NULL when that is 0). */
 int kvc_paged_attend(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int32_t max_new,
