@@ -21,7 +21,8 @@
 //
 // The keys of a head are cut into pieces by its own length (few_chunk); the four
 // waves of a workgroup take the 32-key tiles of a piece in turn, and their sums meet
-// in LDS.  A second kernel joins the pieces where there are several.  Where a piece's
+// in LDS.  A second kernel joins the pieces where there are several, and adds up what each
+// slot receives where that is asked for.  Where a piece's
 // keys are is looked up once, into LDS, four keys at a time where the page size is a
 // multiple of four.
 #include "kvc_paged.h"
@@ -31,7 +32,6 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -43,7 +43,7 @@ struct Args {
   AttendCall a;
   int pieces, rows;  // of the longest length and the longest chunk: the grid's and the partials'
   int blocks;        // row blocks
-  FastDiv by_G, by_pieces, by_H, by_blocks, by_rows;
+  FastDiv by_G, by_pieces, by_H, by_blocks;
   int units, unit0;  // (head, piece) pairs of n0's heads, first one of this launch
   int n0;            // first head of this launch
   float* part;       // [n][row][piece][D] outputs of a piece
@@ -60,14 +60,11 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  return uint32_t(to_bf16(a)) | uint32_t(to_bf16(b)) << 16;
-}
 
 // Four output values of row r of a head, and log2 of its sum of 2^x.
 __device__ __forceinline__ void finish(const Args& A, int token, int head, int dim, f32x4 out, float b) {
-  *reinterpret_cast<u16x4*>(A.a.out.p + token * A.a.out.ts + head * A.a.out.hs + dim) =
-      u16x4{to_bf16(out.x), to_bf16(out.y), to_bf16(out.z), to_bf16(out.w)};
+  *reinterpret_cast<u32x2*>(A.a.out.p + token * A.a.out.ts + head * A.a.out.hs + dim) =
+      u32x2{pack_bf16(out.x, out.y), pack_bf16(out.z, out.w)};
   if (A.a.lse && dim == 0)
     A.a.lse[size_t(token) * (A.a.G * A.a.c.H) + head] = b * 0.6931471805599453f;
 }
@@ -252,7 +249,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
         }
       }
       l[mt] += sum;
-      w[mt] = u32x4{pack(e[0], e[1]), pack(e[2], e[3]), pack(e[4], e[5]), pack(e[6], e[7])};
+      w[mt] = u32x4{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7])};
     }
 #pragma unroll
     for (int u = 0; u < kTiles; ++u) {
@@ -306,6 +303,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
       const bool any = L > 0.0f;
       sum = any ? sum * (1.0f / L) : f32x4{0, 0, 0, 0};
       const float bsum = any ? M + fast_log2(L) : -INFINITY;
+      if (A.scores && dim == 0) A.stat[(size_t(n) * A.rows + r0 + r) * A.pieces + piece] = bsum;
       if (alone) {
         const int i = int(quot(A.by_G, uint32_t(r0 + r)));
         finish(A, mine.x + i, h * A.a.G + r0 + r - i * A.a.G, dim, sum, bsum);
@@ -318,47 +316,94 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
   }
 }
 
-// Joins the pieces of one row, each weighted by its sum: D/4 lanes read one piece's
-// outputs, the workgroup 1024/D pieces at a time.
-template <int D>
-__global__ __launch_bounds__(kThreads) void k_join_few(Args A) {
-  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  __shared__ __align__(16) float sums[kAtOnce][D];
-  const int nth = int(quot(A.by_rows, blockIdx.x)), n = A.n0 + nth;
-  const int r = int(blockIdx.x) - nth * A.rows;
-  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
-  const int2 mine = chunk_of(A.a.k, b);
-  if (r >= mine.y * A.a.G || mine.y * A.a.G > kFewRows) return;
-  const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
-  if (len <= chunk) return;
-  const int pieces = (len + chunk - 1) / chunk, lane = threadIdx.x & 63;
-  const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
-  const size_t row = size_t(n) * A.rows + r;
-  const float* st = A.stat + row * A.pieces;
-  const float* part = A.part + row * A.pieces * D + dim;
+// log2 of a row's sum of 2^x from its pieces', by a wave.
+__device__ __forceinline__ float whole_sum(const float* st, int pieces, float& base) {
+  const int lane = threadIdx.x & 63;
   const float first = lane < pieces ? st[lane] : -INFINITY;  // the lane's piece of the first 64
   float M = first;
   for (int p = lane + 64; p < pieces; p += 64) M = fmaxf(M, st[p]);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
-  const float base = M == -INFINITY ? 0.0f : M;
+  base = M == -INFINITY ? 0.0f : M;
   float L = fast_exp2(first - base);
   for (int p = lane + 64; p < pieces; p += 64) L += fast_exp2(st[p] - base);
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off);
-  const float by_L = L > 0.0f ? 1.0f / L : 0.0f;
+  return L;
+}
+
+// Joins the pieces of one row, each weighted by its sum: D/4 lanes read one piece's
+// outputs, the workgroup 1024/D pieces at a time.
+template <int D>
+__device__ __forceinline__ void join_row(const Args& A, int n, int r, float* sums) {
+  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
+  const int2 mine = chunk_of(A.a.k, b);
+  if (r >= mine.y * A.a.G || mine.y * A.a.G > kFewRows) return;
+  const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
+  if (len <= chunk) return;
+  const int pieces = (len + chunk - 1) / chunk;
+  const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
+  const size_t row = size_t(n) * A.rows + r;
+  const float* st = A.stat + row * A.pieces;
+  const float* part = A.part + row * A.pieces * D + dim;
+  float base;
+  const float L = whole_sum(st, pieces, base), by_L = L > 0.0f ? 1.0f / L : 0.0f;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 4
   for (int p = group; p < pieces; p += kAtOnce)
     sum += *reinterpret_cast<const f32x4*>(part + size_t(p) * D) * (fast_exp2(st[p] - base) * by_L);
-  *reinterpret_cast<f32x4*>(&sums[group][dim]) = sum;
+  *reinterpret_cast<f32x4*>(sums + group * D + dim) = sum;
   __syncthreads();
   if (threadIdx.x >= kLanes) return;
   f32x4 out = {0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) out += *reinterpret_cast<const f32x4*>(&sums[i][dim]);
+  for (int i = 0; i < kAtOnce; ++i) out += *reinterpret_cast<const f32x4*>(sums + i * D + dim);
   const int i = int(quot(A.by_G, uint32_t(r)));
   finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, out, L > 0.0f ? base + fast_log2(L) : -INFINITY);
+}
+
+// What 1024 slots receive from a sequence's few rows: the sum down the rows of 2^(x -
+// log2 of the row's sum), four slots a thread.  The scores come from the first kernel (4
+// bytes a row and slot; the keys would be 2 * d bytes a slot again).
+__device__ __forceinline__ void weigh_slots(const Args& A, int n, int block, float* less) {
+  const Paged& c = A.a.c;
+  const int b = int(quot(A.by_H, uint32_t(n)));
+  const int R = chunk_of(A.a.k, b).y * A.a.G, len = paged_len(c, b);
+  if (R > kFewRows || block * kThreads * 4 >= len) return;
+  const int chunk = few_chunk(len), pieces = (len + chunk - 1) / chunk;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  for (int r = wave; r < R; r += kWaves) {
+    float base;
+    const float L = whole_sum(A.stat + (size_t(n) * A.rows + r) * A.pieces, pieces, base);
+    if (lane == 0) less[r] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
+  }
+  __syncthreads();
+  const int t = (block * kThreads + int(threadIdx.x)) * 4;
+  if (t >= len) return;
+  const float* x = A.scores + size_t(n) * A.rows * A.score_stride + t;
+  f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int r = 0; r < R; ++r) {
+    const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + less[r]);
+  }
+  float* to = c.weight + size_t(n) * c.room + t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (t + i < len && sum[i] > 0.0f) to[i] += sum[i];
+}
+
+// Both in one launch, as neither needs the other: of a head's workgroups `rows` join a row
+// each (none where no head has several pieces), the others weigh its slots.
+template <int D>
+__global__ __launch_bounds__(kThreads) void k_join_few(Args A, int rows, FastDiv by_per, int unit0) {
+  __shared__ __align__(16) float lds[kThreads * 4];
+  const uint32_t unit = blockIdx.x, nth = quot(by_per, unit);
+  const int n = unit0 + int(nth), i = int(unit - nth * by_per.d);
+  if (i < rows) join_row<D>(A, n, i, lds);
+  else weigh_slots(A, n, i - rows, lds);
 }
 
 template <int D, int MT, int GROUP>
@@ -381,11 +426,13 @@ void attend_few(Args A, hipStream_t s) {
                                    keys > sums ? keys : sums, s>>>(A);
     }
   }
-  if (A.pieces == 1) return;
-  const int most_joined = (1 << 23) / A.rows > 0 ? (1 << 23) / A.rows : 1;
-  for (A.n0 = 0; A.n0 < heads; A.n0 += most_joined) {
-    const int nh = heads - A.n0 < most_joined ? heads - A.n0 : most_joined;
-    k_join_few<D><<<unsigned(nh) * unsigned(A.rows), kThreads, 0, s>>>(A);
+  const int rows = A.pieces > 1 ? A.rows : 0;
+  const int per = rows + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
+  if (per == 0) return;
+  const int most_joined = (1 << 23) / per > 0 ? (1 << 23) / per : 1;
+  for (int n0 = 0; n0 < heads; n0 += most_joined) {
+    const int nh = heads - n0 < most_joined ? heads - n0 : most_joined;
+    k_join_few<D><<<unsigned(nh) * unsigned(per), kThreads, 0, s>>>(A, rows, fast_div(uint32_t(per)), n0);
   }
 }
 
@@ -398,41 +445,6 @@ void attend_rows(const Args& A, hipStream_t s) {
   } else {
     if (fours) attend_few<D, 2, 4>(A, s);
     else attend_few<D, 2, 1>(A, s);
-  }
-}
-
-// What each slot receives from a sequence's few rows: the sum down the rows of
-// 2^(x - log2 of the row's sum), four slots a thread.  The scores come from the first
-// kernel (4 bytes a row and slot; the keys would be 2 * d bytes a slot again).
-__global__ __launch_bounds__(kThreads) void k_weights_few(Args A) {
-  __shared__ float base[kFewRows];
-  const Paged& c = A.a.c;
-  for (int n = blockIdx.y; n < c.B * c.H; n += gridDim.y) {
-    const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
-    const int2 mine = chunk_of(A.a.k, b);
-    const int R = mine.y * A.a.G, len = paged_len(c, b);
-    if (R > kFewRows || R == 0) continue;          // the same for the whole workgroup
-    __syncthreads();
-    if (threadIdx.x < R) {
-      const int i = int(quot(A.by_G, threadIdx.x));
-      const float z = A.a.lse[size_t(mine.x + i) * (A.a.G * c.H) + h * A.a.G + int(threadIdx.x) - i * A.a.G];
-      base[threadIdx.x] = z == -INFINITY ? -INFINITY : -z * 1.4426950408889634f;   // a row that sees nothing gives nothing
-    }
-    __syncthreads();
-    const float* x = A.scores + size_t(n) * A.rows * A.score_stride;
-    float* to = c.weight + size_t(n) * c.room;
-    for (int t = (blockIdx.x * kThreads + threadIdx.x) * 4; t < len; t += gridDim.x * kThreads * 4) {
-      f32x4 sum = {0, 0, 0, 0};
-#pragma unroll 4
-      for (int r = 0; r < R; ++r) {
-        const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride + t);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + base[r]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (t + i < len && sum[i] > 0.0f) to[t + i] += sum[i];
-    }
   }
 }
 
@@ -450,7 +462,7 @@ AttendWs attend_ws(const Paged& c, const Chunks& k, int G) {
   w.few_pieces = few_max_pieces(c.cap);
   const size_t n = w.few_pieces > 1 ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : 0;
   w.few_part = take(n * c.D);
-  w.few_stat = take(n);
+  w.few_stat = take(c.weight ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : n);
   w.score_stride = (c.cap + 31) & ~31;
   w.scores = take(c.weight ? size_t(c.B) * c.H * w.few_rows * w.score_stride : 0);
   w.slots = int64_t(G) * k.max_new > kFewRows ? first_slot(k.n_tokens, c.B, G) + 1 : 0;
@@ -472,7 +484,6 @@ hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
   A.by_G = fast_div(uint32_t(a.G));
   A.by_pieces = fast_div(uint32_t(A.pieces));
   A.by_H = fast_div(uint32_t(a.c.H));
-  A.by_rows = fast_div(uint32_t(A.rows));
   A.part = ws + w.few_part;
   A.stat = ws + w.few_stat;
   A.scores = a.c.weight ? ws + w.scores : nullptr;
@@ -484,10 +495,6 @@ hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
     t.lse = A.a.lse;
     const hipError_t e = launch_attend_tiles(t, ws + w.part, ws + w.stat, w.slots, s);
     if (e != hipSuccess) return e;
-  }
-  if (a.c.weight) {
-    const int heads = a.c.B * a.c.H, blocks = (a.c.cap + kThreads * 4 - 1) / (kThreads * 4);
-    k_weights_few<<<dim3(unsigned(blocks < 4096 ? blocks : 4096), unsigned(heads < 32768 ? heads : 32768)), kThreads, 0, s>>>(A);
   }
   return hipGetLastError();
 }

@@ -23,6 +23,8 @@
 // Tiles go from global memory to LDS without passing registers, one tile ahead, in
 // the order in which the LDS banks serve both kinds of reads: 16-byte piece p of row
 // r sits at place p ^ swizzle(r).
+#include <type_traits>
+
 #include "kvc_paged.h"
 
 namespace kvc {
@@ -30,7 +32,6 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned short u16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -68,9 +69,6 @@ __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_lo
 __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  return uint32_t(to_bf16(a)) | uint32_t(to_bf16(b)) << 16;
 }
 
 // Place of a row's 16-byte pieces: 16 rows' same piece lie in 16 different places of
@@ -197,7 +195,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
     const int64_t at = paged_row(A.c, w.b, w.h, key);
     return at < 0 ? kNone : uint32_t(at);
   };
+  // Bytes of a lane's piece from its tile's (no cache) or its group's first row: below
+  // 2^32, so a load's address is a scalar and these.
+  uint32_t k_off[kLoads], v_off[kLoads];
+#pragma unroll
+  for (int x = 0; x < kLoads; ++x) {
+    const int row = wave * (kTile / kWaves) + x * kRowsPerLoad + lane / kPieces;
+    const int piece = (lane % kPieces) ^ swizzle<D>(row);
+    k_off[x] = PAGED ? uint32_t((lane / kPieces) * D + piece * 8) * 2 : (uint32_t(row) * uint32_t(A.kr.ts) + piece * 8) * 2;
+    v_off[x] = PAGED ? k_off[x] : (uint32_t(row) * uint32_t(A.vr.ts) + piece * 8) * 2;
+  }
+  auto at_off = [](const uint16_t* p, uint32_t off) { return reinterpret_cast<const char*>(p) + off; };
   auto fetch = [&](int t0, int nth, uint32_t of, int buf) {   // nth: tile of the batch
+    if constexpr (!PAGED) {
+      if (t0 + kTile <= w.n) {
+        const uint16_t* kp = kb + int64_t(t0) * A.kr.ts;
+        const uint16_t* vp = vb + int64_t(t0) * A.vr.ts;
+#pragma unroll
+        for (int x = 0; x < kLoads; ++x) {
+          const int first = wave * (kTile / kWaves) + x * kRowsPerLoad;
+          to_lds(at_off(kp, k_off[x]), ks[buf] + first * D);
+          to_lds(at_off(vp, v_off[x]), vs[buf] + first * D);
+        }
+        return;
+      }
+    }
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
       const int first = wave * (kTile / kWaves) + x * kRowsPerLoad, row = first + lane / kPieces;
@@ -209,8 +231,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
       } else if constexpr (GROUP > 1) {
         const uint32_t at = __builtin_amdgcn_readlane(of, nth * kPerTile + first / GROUP);
         if (at != kNone && t0 + first + GROUP <= w.len) {
-          to_lds(A.c.k + size_t(at) * D + (lane / kPieces) * D + piece * 8, ks[buf] + first * D);
-          to_lds(A.c.v + size_t(at) * D + (lane / kPieces) * D + piece * 8, vs[buf] + first * D);
+          to_lds(at_off(A.c.k + size_t(at) * D, k_off[x]), ks[buf] + first * D);
+          to_lds(at_off(A.c.v + size_t(at) * D, k_off[x]), vs[buf] + first * D);
         } else {   // rows past the end may hold anything, and nothing times a NaN is one
           const uint16_t* z = reinterpret_cast<const uint16_t*>(zeros);
           const size_t inner = size_t(at) * D + (lane / kPieces) * D;
@@ -274,7 +296,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
       }
     }
     if (t0 + kTile - 1 > low || gone != 0 || gone1 != 0) {
-      const int d = limit - t0 - 4 * hh;
+      int d = limit - t0 - 4 * hh;
+      asm volatile("" : "+v"(d));            // a branch: not 32 selects in every tile
       // bit k / GROUP: key k + 4 hh of the tile
       const uint32_t g_lane = GROUP == 4 ? gone >> hh : gone;
       const uint64_t g_one = gone1 >> (4 * hh);
@@ -317,8 +340,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
     l += sum;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {            // 16 keys a step
-      const u32x4 pf = {pack(p[8 * s], p[8 * s + 1]), pack(p[8 * s + 2], p[8 * s + 3]),
-                        pack(p[8 * s + 4], p[8 * s + 5]), pack(p[8 * s + 6], p[8 * s + 7])};
+      const u32x4 pf = {pack_bf16(p[8 * s], p[8 * s + 1]), pack_bf16(p[8 * s + 2], p[8 * s + 3]),
+                        pack_bf16(p[8 * s + 4], p[8 * s + 5]), pack_bf16(p[8 * s + 6], p[8 * s + 7])};
 #pragma unroll
       for (int d = 0; d < kDims; ++d) {
         // lane: 4 keys from 16s + 4hh (and 8 further on), values 32d + 16 ((lane >> 4) & 1) +
@@ -355,40 +378,49 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   for (int d = 0; d < kDims; ++d)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<u16x4*>(po + 32 * d + 8 * e + 4 * hh) =
-          u16x4{to_bf16(acc[d][4 * e] * by_l), to_bf16(acc[d][4 * e + 1] * by_l),
-                to_bf16(acc[d][4 * e + 2] * by_l), to_bf16(acc[d][4 * e + 3] * by_l)};
+      *reinterpret_cast<u32x2*>(po + 32 * d + 8 * e + 4 * hh) =
+          u32x2{pack_bf16(acc[d][4 * e] * by_l, acc[d][4 * e + 1] * by_l),
+                pack_bf16(acc[d][4 * e + 2] * by_l, acc[d][4 * e + 3] * by_l)};
   if (A.lse && hh == 0)
     A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] = b_sum * 0.6931471805599453f;
 }
 
-// Joins the pieces of 1024 / D rows, each weighted by its sum, four values a lane.
+// Joins the pieces of 1024 / D rows of a row tile, each weighted by its sum, four values
+// a lane.
 template <int D>
-__global__ __launch_bounds__(kThreads) void k_join_tiles(Args A) {
+__global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tiles) {
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
-  Where w;
-  if (!find<true>(A, w) || w.piece != 0 || w.pieces == 1) return;
-  const int r = w.r0 + int(blockIdx.y) * kAtOnce + int(threadIdx.x) / kLanes, dim = threadIdx.x % kLanes * 4;
-  if (r >= w.R) return;
-  const size_t row = (size_t(w.h) * A.slots + w.slot) * kRows + (r - w.r0);
-  const size_t step = size_t(w.tiles) * kRows;           // from piece to piece
+  const int G = A.G;
+  const int h = int(quot(by_tiles, blockIdx.x)), tile = int(blockIdx.x) - h * int(by_tiles.d);
+  const int b = last_at_or_below(A.k.starts, A.k.B, tile, [G](int s, int i) { return first_tile(s, i, G); });
+  const int2 mine = chunk_of(A.k, b);
+  const int R = mine.y * G, start = A.k.starts[b], t = tile - first_tile(start, b, G);
+  if (R <= kFewRows || t < 0) return;
+  const int tiles = (R + kRows - 1) / kRows, pieces = tile_pieces(paged_len(A.c, b), tiles);
+  const int in_tile = int(blockIdx.y) * kAtOnce + int(threadIdx.x) / kLanes, r = t * kRows + in_tile;
+  const int slot = first_slot(start, b, G) + t;
+  if (pieces == 1 || r >= R || slot + (pieces - 1) * tiles >= A.slots) return;
+  const int dim = threadIdx.x % kLanes * 4;
+  const size_t row = (size_t(h) * A.slots + slot) * kRows + in_tile;
+  const size_t step = size_t(tiles) * kRows;             // from piece to piece
   float M = -INFINITY;
-  for (int p = 0; p < w.pieces; ++p) M = fmaxf(M, A.stat[row + p * step]);
+#pragma unroll 4
+  for (int p = 0; p < pieces; ++p) M = fmaxf(M, A.stat[row + p * step]);
   const float base = M == -INFINITY ? 0.0f : M;
   float L = 0.0f;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int p = 0; p < w.pieces; ++p) {
+  for (int p = 0; p < pieces; ++p) {
     const float f = fast_exp2(A.stat[row + p * step] - base);
     sum += *reinterpret_cast<const f32x4*>(A.part + (row + p * step) * D + dim) * f;
     L += f;
   }
   const float by_l = L > 0.0f ? 1.0f / L : 0.0f;
-  const int i = int(quot(A.by_G, uint32_t(r))), head = w.h * A.G + r - i * A.G;
-  *reinterpret_cast<u16x4*>(A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs + dim) =
-      u16x4{to_bf16(sum.x * by_l), to_bf16(sum.y * by_l), to_bf16(sum.z * by_l), to_bf16(sum.w * by_l)};
+  const int i = int(quot(A.by_G, uint32_t(r))), head = h * G + r - i * G;
+  *reinterpret_cast<u32x2*>(A.out.p + int64_t(mine.x + i) * A.out.ts + int64_t(head) * A.out.hs + dim) =
+      u32x2{pack_bf16(sum.x * by_l, sum.y * by_l), pack_bf16(sum.z * by_l, sum.w * by_l)};
   if (A.lse && dim == 0)
-    A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] =
+    A.lse[size_t(mine.x + i) * (G * A.H) + head] =
         L > 0.0f ? (base + fast_log2(L)) * 0.6931471805599453f : -INFINITY;
 }
 
@@ -398,21 +430,19 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A) {
 // lane-local; its order is fixed.
 constexpr int kKeys = kWaves * 64;
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int chunks, int unit0, int units) {
+__global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int n0) {
   constexpr int kPieces = D / 8;
   constexpr int kRowsPerLoad = 64 / kPieces;
   constexpr int kLoads = kTile / kWaves / kRowsPerLoad;
   constexpr int kSteps = D / 16;
   __shared__ __align__(16) uint16_t qs[2][kTile * D];
   __shared__ __align__(16) float bs[2][kTile];           // -log2 of the rows' sums
-  __shared__ int lim[2][kTile];                          // the rows' last keys
-  const int unit = unit0 + int(blockIdx.x);
-  if (unit >= units) return;
-  const int n = int(quot(by_chunks, uint32_t(unit))), b = n / A.H, h = n - b * A.H;
+  __shared__ __align__(16) int lim[2][kTile];            // the rows' last keys
+  const int nth = int(quot(by_chunks, blockIdx.x)), n = n0 + nth, b = n / A.H, h = n - b * A.H;
   const int2 mine = chunk_of(A.k, b);
   const int R = mine.y * A.G, len = paged_len(A.c, b);
   if (R <= kFewRows) return;
-  const int t0 = (unit - n * chunks) * kKeys;
+  const int t0 = (int(blockIdx.x) - nth * int(by_chunks.d)) * kKeys;
   if (t0 >= len) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -446,8 +476,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
       const int r = r0 + int(threadIdx.x), rc = r < R ? r : R - 1, i = int(quot(A.by_G, uint32_t(rc)));
       const float z = A.lse[size_t(mine.x + i) * (A.G * A.H) + h * A.G + rc - i * A.G];
       const bool any = r < R && z != -INFINITY;
-      bs[buf][threadIdx.x] = any ? -z * 1.4426950408889634f : 0.0f;
-      lim[buf][threadIdx.x] = any ? first_new + i : -1;
+      bs[buf][threadIdx.x] = any ? -z * 1.4426950408889634f : -INFINITY;   // a row that sees nothing gives nothing
+      lim[buf][threadIdx.x] = first_new + i;
     }
   };
   fetch(0, 0);
@@ -468,19 +498,25 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
         sc[0] = mfma(qf, kf[0][s], sc[0]);
         sc[1] = mfma(qf, kf[1][s], sc[1]);
       }
+      auto add = [&](auto checked) {
 #pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const int at = blk * 32 + 8 * e4 + 4 * hh;
-        const f32x4 bz = *reinterpret_cast<const f32x4*>(&bs[tile & 1][at]);
-        const i32x4 lm = *reinterpret_cast<const i32x4*>(&lim[tile & 1][at]);
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const int at = blk * 32 + 8 * e4 + 4 * hh;
+          const f32x4 bz = *reinterpret_cast<const f32x4*>(&bs[tile & 1][at]);
+          i32x4 lm = {0, 0, 0, 0};
+          if constexpr (checked) lm = *reinterpret_cast<const i32x4*>(&lim[tile & 1][at]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float p = fast_exp2(__builtin_fmaf(sc[x][4 * e4 + e], by, bz[e]));
-            total[x] += key0 + x * 32 + j <= lm[e] ? p : 0.0f;
-          }
-      }
+            for (int x = 0; x < 2; ++x) {
+              const float p = fast_exp2(__builtin_fmaf(sc[x][4 * e4 + e], by, bz[e]));
+              total[x] += !checked || key0 + x * 32 + j <= lm[e] ? p : 0.0f;
+            }
+        }
+      };
+      // the tile's first row sees least
+      if (key0 + 63 <= first_new + int(quot(A.by_G, uint32_t(r_from + tile * kTile)))) add(std::false_type{});
+      else add(std::true_type{});
     }
   }
 #pragma unroll
@@ -507,14 +543,16 @@ void attend_chunks(Args& A, hipStream_t s) {
   const unsigned blocks = deal(A, A.slots);
   if (A.c.bs % (512 / D) == 0) k_attend_tiles<D, 512 / D><<<blocks, kThreads, 0, s>>>(A);
   else k_attend_tiles<D, 1><<<blocks, kThreads, 0, s>>>(A);
-  if (tile_max_pieces(A.c.cap) > 1)
-    k_join_tiles<D><<<dim3(blocks, kRows * D / 1024), kThreads, 0, s>>>(A);
+  if (tile_max_pieces(A.c.cap) > 1) {
+    const int tiles = first_tile(A.k.n_tokens, A.k.B, A.G);
+    k_join_tiles<D><<<dim3(unsigned(tiles) * unsigned(A.H), kRows * D / 1024), kThreads, 0, s>>>(A, fast_div(uint32_t(tiles)));
+  }
   if (!A.c.weight) return;
   const int chunks = (A.c.cap + kKeys - 1) / kKeys;
   const int heads = A.c.B * A.H, most = (1 << 23) / chunks > 0 ? (1 << 23) / chunks : 1;
   for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
     const int nh = heads - n0 < most ? heads - n0 : most;
-    k_weights_tiles<D><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), chunks, n0 * chunks, (n0 + nh) * chunks);
+    k_weights_tiles<D><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);
   }
 }
 

@@ -5,11 +5,13 @@
 //   recent    10 | 0 (32)        | position
 //   others    01 | weight (32)   | 2^30 - 1 - position
 // (a weight's bits, turned so that they order as integers).  A workgroup takes one
-// head and finds the K-th largest key digit by digit, eight bits at a time, from counts
-// in LDS; it is done once the slots that share the digits so far are all needed.
-// Then it lists, in ascending order, the given-up slots below K and the kept ones
-// from K on: as many of either.  A second kernel moves the rows from these to those,
-// the only bytes that have to move.
+// head, each wave a range of its slots, and finds the K-th largest key.  Where at most
+// kSingles slots have to go (a decode step), it takes the smallest key that often.
+// Otherwise it goes digit by digit, eleven bits at a time, from counts in LDS, until the
+// slots that share the digits so far are all needed: three digits hold the class and the
+// whole weight.  Then it lists, in ascending order, the given-up slots below K and the
+// kept ones from K on: as many of either.  A second kernel moves the rows from these to
+// those, the only bytes that have to move.
 //
 // Positions of a head are distinct, so keys are; should they not be, equal keys stay in
 // the order of their slots, and both lists still have the same length.
@@ -20,7 +22,7 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kSingles = 4, kBits = 11, kBins = 1 << kBits;
 constexpr int kMoveThreads = 256;
 constexpr int kLastPos = (1 << 30) - 1;
 
@@ -48,118 +50,188 @@ __device__ __forceinline__ void count_bin(int* bins, int bin, bool in) {
   if (!all) return;
   const int first = __shfl(bin, __builtin_ctzll(all));
   const uint64_t same = __ballot(in && bin == first);
-  if ((threadIdx.x & 63) == __builtin_ctzll(all)) atomicAdd(&bins[first], __builtin_popcountll(same));
+  if (int(threadIdx.x & 63) == __builtin_ctzll(all)) atomicAdd(&bins[first], __builtin_popcountll(same));
   if (in && bin != first) atomicAdd(&bins[bin], 1);
 }
 
-__global__ __launch_bounds__(kThreads) void k_evict_plan(Evict E) {
-  __shared__ int bins[256];
+// The smaller of two keys, of equal ones that of the later slot.
+__device__ __forceinline__ bool goes_before(uint64_t a, int at, uint64_t b, int bt) {
+  return a < b || (a == b && at > bt);
+}
+
+// KPT: slots a thread holds in registers, 0: keys are formed again in every pass.
+template <int NT, int KPT>
+__device__ __forceinline__ void plan(const Evict& E, int n, int b, int len, int* bins) {
+  constexpr int kWaves = NT / 64;
   __shared__ int chosen[3];            // digit, slots above it, slots in it
   __shared__ int totals[kWaves][3];    // equal keys, holes, movers of a wave's range
+  __shared__ uint64_t low_key[kWaves];
+  __shared__ int low_slot[kWaves];
   const Paged& c = E.c;
-  const int n = blockIdx.x, b = n / c.H, K = E.K;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int len = paged_len(c, b);
-  if (len <= K) {
-    if (tid == 0) E.count[n] = 0;
-    return;
-  }
+  const int K = E.K, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const float* w = c.weight + size_t(n) * c.room;
   const int32_t* pos = c.pos + size_t(n) * c.room;
   const int64_t recent_from = int64_t(E.seen[b]) - E.recent;
-  auto key = [&](int t) { return key_of(w[t], pos[t], E.sinks, recent_from); };
-
-  // Keys above `prefix` (its digits below `shift` zero) stay, of those that share its
-  // digits `need` do.
-  uint64_t prefix = 0;
-  int shift = 64, need = K;
-  while (shift > 0) {
-    shift -= 8;
-    if (tid < 256) bins[tid] = 0;
-    __syncthreads();
-    for (int t = wave * 64; t < len; t += kThreads) {   // whole waves
-      const int at = t + lane;
-      const uint64_t x = at < len ? key(at) : 0;
-      const bool in = at < len && (shift == 56 || (x >> (shift + 8)) == (prefix >> (shift + 8)));
-      count_bin(bins, int(x >> shift) & 255, in);
-    }
-    __syncthreads();
-    if (wave == 0) {   // the digit that the need-th largest has: four bins a lane, from the top
-      int mine[4], sum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum += mine[i] = bins[255 - 4 * lane - i];
-      int above = sum;
-#pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const int o = __shfl_up(above, off);
-        above += lane >= off ? o : 0;
-      }
-      above -= sum;    // in the bins of the lanes before
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (above < need && above + mine[i] >= need) {
-          chosen[0] = 255 - 4 * lane - i;
-          chosen[1] = above;
-          chosen[2] = mine[i];
-        }
-        above += mine[i];
-      }
-    }
-    __syncthreads();
-    prefix |= uint64_t(chosen[0]) << shift;
-    need -= chosen[1];
-    const bool all = chosen[2] == need;
-    __syncthreads();   // before the bins and the choice are written again
-    if (all) break;
-  }
-
-  // Each wave takes a range of slots, counts, and writes its part of the lists.
-  const int span = ((len + kWaves - 1) / kWaves + 63) & ~63;
+  const int span = ((len + kWaves - 1) / kWaves + 63) & ~63;   // at most KPT * 64
   const int lo = wave * span, hi = lo + span < len ? lo + span : len;
-  const uint64_t cut = prefix >> shift;
-  int equal = 0;
-  for (int t = lo; t < hi; t += 64) {
-    const int at = t + lane;
-    equal += __builtin_popcountll(__ballot(at < hi && (key(at) >> shift) == cut));
+  uint64_t held[KPT > 0 ? KPT : 1];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int i = 0; i < KPT; ++i) {
+      const int t = lo + i * 64 + lane;
+      held[i] = t < hi ? key_of(w[t], pos[t], E.sinks, recent_from) : 0;   // keys are above 0
+    }
   }
+  // f(slot, in, key) for the wave's slots, 64 at a time
+  auto each = [&](auto f) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int i = 0; i < KPT; ++i)
+        if (lo + i * 64 < hi) f(lo + i * 64 + lane, lo + i * 64 + lane < hi, held[i]);
+    } else {
+      for (int t = lo; t < hi; t += 64) {
+        const bool in = t + lane < hi;
+        f(t + lane, in, in ? key_of(w[t + lane], pos[t + lane], E.sinks, recent_from) : 0);
+      }
+    }
+  };
+
+  // Keys from `cut` on stay once shifted by `shift`, of those equal to it `need` do.
+  uint64_t cut = 0;
+  int shift = 0, need = 0;
+  if (len - K <= kSingles) {
+    uint64_t last = 0;
+    int last_slot = 0x7fffffff;
+    for (int m = 0; m < len - K; ++m) {
+      uint64_t key = ~uint64_t(0);
+      int slot = -1;
+      each([&](int t, bool in, uint64_t x) {
+        if (in && goes_before(last, last_slot, x, t) && goes_before(x, t, key, slot)) key = x, slot = t;
+      });
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        const uint64_t o = __shfl_xor(key, off);
+        const int os = __shfl_xor(slot, off);
+        if (goes_before(o, os, key, slot)) key = o, slot = os;
+      }
+      if (lane == 0) low_key[wave] = key, low_slot[wave] = slot;
+      __syncthreads();
+      key = low_key[0], slot = low_slot[0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i)
+        if (goes_before(low_key[i], low_slot[i], key, slot)) key = low_key[i], slot = low_slot[i];
+      __syncthreads();
+      last = key, last_slot = slot;
+    }
+    // Slots of the last one's key that are not past it stay.
+    cut = last;
+    int equal = 0;
+    each([&](int t, bool in, uint64_t x) {
+      equal += __builtin_popcountll(__ballot(in && x == cut && t < last_slot));
+    });
+    if (lane == 0) totals[wave][0] = equal;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) need += totals[i][0];
+    __syncthreads();
+  } else {
+    need = K;
+    shift = 64;
+    while (shift > 0) {
+      const int bits = shift < kBits ? shift : kBits;
+      shift -= bits;
+      for (int i = tid; i < kBins; i += NT) bins[i] = 0;
+      __syncthreads();
+      each([&](int t, bool in, uint64_t x) {
+        // (two shifts: one by all 64 bits is none)
+        count_bin(bins, int(x >> shift) & ((1 << bits) - 1), in && ((x >> shift) >> bits) == cut);
+      });
+      __syncthreads();
+      if (wave == 0) {   // the digit that the need-th largest has: a run of bins a lane, from the top
+        constexpr int kRun = kBins / 64;
+        int sum = 0;
+#pragma unroll 8
+        for (int i = 0; i < kRun; ++i) sum += bins[kBins - 1 - (kRun * lane + i)];
+        int above = sum;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+          const int o = __shfl_up(above, off);
+          above += lane >= off ? o : 0;
+        }
+        above -= sum;    // in the bins of the lanes before
+        if (above < need && above + sum >= need) {   // one lane's
+          int i = kBins - 1 - kRun * lane;
+          while (above + bins[i] < need) above += bins[i--];
+          chosen[0] = i;
+          chosen[1] = above;
+          chosen[2] = bins[i];
+        }
+      }
+      __syncthreads();
+      cut = (cut << bits) | uint64_t(chosen[0]);
+      need -= chosen[1];
+      const bool all = chosen[2] == need;
+      __syncthreads();   // before the bins and the choice are written again
+      if (all) break;
+    }
+  }
+
+  // Each wave counts in its range, and writes its part of the lists.
+  int equal = 0;
+  each([&](int t, bool in, uint64_t x) { equal += __builtin_popcountll(__ballot(in && (x >> shift) == cut)); });
   if (lane == 0) totals[wave][0] = equal;
   __syncthreads();
   int before = 0;
   for (int i = 0; i < wave; ++i) before += totals[i][0];
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  auto stays = [&](int at, bool in, int& eq) {   // eq: equal keys before this wave's 64 slots
-    const uint64_t x = in ? key(at) >> shift : 0;
+  auto stays = [&](bool in, uint64_t x, int& eq) {   // eq: equal keys before these 64 slots
+    x >>= shift;
     const uint64_t m = __ballot(in && x == cut);
     const bool yes = in && (x > cut || (x == cut && eq + __builtin_popcountll(m & below) < need));
     eq += __builtin_popcountll(m);
     return yes;
   };
   int eq = before, holes = 0, movers = 0;
-  for (int t = lo; t < hi; t += 64) {
-    const int at = t + lane;
-    const bool in = at < hi, yes = stays(at, in, eq);
-    holes += __builtin_popcountll(__ballot(in && !yes && at < K));
-    movers += __builtin_popcountll(__ballot(yes && at >= K));
-  }
+  each([&](int t, bool in, uint64_t x) {
+    const bool yes = stays(in, x, eq);
+    holes += __builtin_popcountll(__ballot(in && !yes && t < K));
+    movers += __builtin_popcountll(__ballot(yes && t >= K));
+  });
   if (lane == 0) totals[wave][1] = holes, totals[wave][2] = movers;
   __syncthreads();
   int hole0 = 0, mover0 = 0, total = 0;
+#pragma unroll
   for (int i = 0; i < kWaves; ++i) {
     if (i < wave) hole0 += totals[i][1], mover0 += totals[i][2];
     total += totals[i][2];
   }
   eq = before;
-  for (int t = lo; t < hi; t += 64) {
-    const int at = t + lane;
-    const bool in = at < hi, yes = stays(at, in, eq);
-    const bool hole = in && !yes && at < K, mover = yes && at >= K;
+  int32_t* const to = E.to + size_t(n) * E.most;
+  int32_t* const from = E.from + size_t(n) * E.most;
+  each([&](int t, bool in, uint64_t x) {
+    const bool yes = stays(in, x, eq), hole = in && !yes && t < K, mover = yes && t >= K;
     const uint64_t mh = __ballot(hole), mm = __ballot(mover);
-    if (hole) E.to[size_t(n) * E.most + hole0 + __builtin_popcountll(mh & below)] = at;
-    if (mover) E.from[size_t(n) * E.most + mover0 + __builtin_popcountll(mm & below)] = at;
+    if (hole) to[hole0 + __builtin_popcountll(mh & below)] = t;
+    if (mover) from[mover0 + __builtin_popcountll(mm & below)] = t;
     hole0 += __builtin_popcountll(mh);
     mover0 += __builtin_popcountll(mm);
-  }
+  });
   if (tid == 0) E.count[n] = total;
+}
+
+template <int NT>
+__global__ __launch_bounds__(NT) void k_evict_plan(Evict E) {
+  __shared__ int bins[kBins];
+  const int n = blockIdx.x, b = n / E.c.H, len = paged_len(E.c, b);
+  if (len <= E.K) {
+    if (threadIdx.x == 0) E.count[n] = 0;
+  } else if (len <= 4 * NT) {
+    plan<NT, 4>(E, n, b, len, bins);
+  } else if (len <= 16 * NT) {
+    plan<NT, 16>(E, n, b, len, bins);
+  } else {
+    plan<NT, 0>(E, n, b, len, bins);
+  }
 }
 
 // A row's 16-byte pieces by D/8 lanes; the lists' slots are disjoint, so the order does
@@ -209,7 +281,9 @@ hipError_t launch_paged_evict(const Paged& c, const int32_t* seen, int K, int si
   Evict E{c, seen, K, sinks, recent, most_moves(c, K), ws, nullptr, nullptr};
   E.from = ws + heads;
   E.to = E.from + size_t(heads) * E.most;
-  k_evict_plan<<<unsigned(heads), kThreads, 0, s>>>(E);
+  // By the longest length there can be: few waves meet sooner.
+  if (c.cap <= 2048) k_evict_plan<256><<<unsigned(heads), 256, 0, s>>>(E);
+  else k_evict_plan<1024><<<unsigned(heads), 1024, 0, s>>>(E);
   // About 2048 workgroups where the heads are fewer.
   const int per = kMoveThreads / (c.D / 8), need = (E.most + per - 1) / per;
   int y = heads < 2048 ? 2048 / heads : 1;

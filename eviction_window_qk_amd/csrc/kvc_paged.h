@@ -87,6 +87,11 @@ __device__ __forceinline__ int last_at_or_below(const int32_t* starts, int B, in
 __device__ __forceinline__ uint16_t to_bf16(float x) {
   return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
 }
+// Two values as bf16, the first one low, in one instruction.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
+}
 
 // Keys per workgroup of the attention of few rows, for a sequence of len slots: pieces of at most
 // kFewChunk, doubled to kFewMaxChunk while there are more than 64; equal pieces, in

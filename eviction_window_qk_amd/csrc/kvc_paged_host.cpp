@@ -10,7 +10,7 @@ namespace kvc {
 namespace {
 
 constexpr int kMaxTokens = 1 << 23;   // a workgroup a token, the grid's limit
-constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int64_t kMaxTokenStride = 1 << 24, kMaxHeadStride = int64_t(1) << 40;  // 64 tokens lie within 2^32 bytes
 
 size_t pool_bytes(const kvc_paged_cache* c) {
   return size_t(c->n_blocks) * c->kv_heads * c->block_size * c->head_dim * 2;
@@ -80,8 +80,8 @@ struct Span2 {
 
 int rows_ok(const kvc_rows* r, int64_t n, int64_t heads, int d, bool written, Rows* out, Span2* sp) {
   if (!r || !r->data) return KVC_EINVAL;
-  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > kMaxStride ||
-      r->head_stride > kMaxStride)
+  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > kMaxTokenStride ||
+      r->head_stride > kMaxHeadStride)
     return KVC_EINVAL;
   if (!aligned(r->data, 16) || r->token_stride % 8 != 0 || r->head_stride % 8 != 0) return KVC_EALIGN;
   *out = {static_cast<uint16_t*>(r->data), r->token_stride, r->head_stride};
@@ -129,7 +129,10 @@ int attend_shape(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int3
   if (group > 64) return KVC_EUNSUPPORTED;
   if (int64_t(n_tokens) * group * d->H >= (int64_t(1) << 30)) return KVC_EINVAL;
   *k = {nullptr, d->B, n_tokens, max_new > 0 && max_new < n_tokens ? max_new : n_tokens};
-  if (int64_t(first_slot(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23)) return KVC_EINVAL;  // workgroups of a launch
+  if (int64_t(group) * k->max_new > kFewRows &&   // workgroups of a launch
+      (int64_t(first_slot(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23) ||
+       int64_t(first_tile(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23)))
+    return KVC_EINVAL;
   return KVC_OK;
 }
 

@@ -36,9 +36,6 @@ __device__ __forceinline__ void turn_of(const RopePlan& f, int at, int i, float&
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack(float a, float b) {
-  return uint32_t(to_bf16(a)) | uint32_t(to_bf16(b)) << 16;
-}
 
 // Items of a row that rotates: eight pairs each, then the copied values by eight.
 struct Shape {
@@ -63,7 +60,7 @@ __device__ __forceinline__ void row_item(const RopePlan& f, const Shape& sh, con
       const int i = item * 4 + j;
       if (i < sh.half) {
         const float x0 = lo_f(a[j]), x1 = hi_f(a[j]), c = t.c[i], s = t.s[i];
-        a[j] = pack(x0 * c - x1 * s, x1 * c + x0 * s);
+        a[j] = pack_bf16(x0 * c - x1 * s, x1 * c + x0 * s);
       }
     }
     *reinterpret_cast<u32x4*>(y + item * 8) = a;
@@ -77,8 +74,8 @@ __device__ __forceinline__ void row_item(const RopePlan& f, const Shape& sh, con
         const float a0 = lo_f(a[j]), a1 = hi_f(a[j]), b0 = lo_f(b[j]), b1 = hi_f(b[j]);
         const float c0 = t.c[i0 + 2 * j], c1 = t.c[i0 + 2 * j + 1];
         const float s0 = t.s[i0 + 2 * j], s1 = t.s[i0 + 2 * j + 1];
-        a[j] = pack(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-        b[j] = pack(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
+        a[j] = pack_bf16(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
+        b[j] = pack_bf16(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
       }
       reinterpret_cast<Loose*>(y + i0)->x = a;
       reinterpret_cast<Loose*>(y + sh.half + i0)->x = b;

@@ -995,25 +995,23 @@ class Rope(_Handle):
 
 
 def _rows(t, shape, device, name):
-    """kvc_rows of a bf16 tensor [n_tokens, heads, d], any strides with whole rows."""
+    """kvc_rows of a bf16 tensor [n_tokens, heads, d] on a GPU, any strides with whole rows."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dtype not in _BF16_LIKE:
         raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16_LIKE}")
-    if device.type != "cuda" or t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}" if device.type == "cuda" else
-                         f"{name}: must be a GPU tensor, got {device}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
     ts, hs, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: rows must be contiguous")
     # a stride that no step is taken by may be anything
-    return _CRows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+    return _byref(_CRows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0))
 
 
-def _ref(c):
-    return ctypes.addressof(c)
+_byref = ctypes.byref
 
 
 def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
@@ -1031,10 +1029,10 @@ def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
     cx = _rows(x, x.shape, dev, "x")
     p_ptr = _at(positions, _I32, (n,), dev, "positions")
     if y is None:
-        y = torch.empty((n, heads, d), dtype=x.dtype, device=dev)
+        y = x.new_empty((n, heads, d))
     cy = cx if y is x else _rows(y, x.shape, dev, "y")
     rc = lib().kvc_rope(_int(n, "n_tokens"), _int(heads, "heads"), _int(d, "head_dim"), plan._ref,
-                        1 if backward else 0, p_ptr, _ref(cx), _ref(cy), s)
+                        1 if backward else 0, p_ptr, cx, cy, s)
     _check(rc, "kvc_rope")
     return y
 
@@ -1102,7 +1100,7 @@ def _group(q, kv_heads, name):
         raise ValueError(f"{name}: 3 dimensions expected")
     if q.shape[1] % kv_heads:
         raise ValueError(f"{name}: {q.shape[1]} heads are no multiple of {kv_heads}")
-    return q.shape[1] // kv_heads
+    return _int(q.shape[1] // kv_heads, "group")
 
 
 def paged_append(cache: PagedCache, k, v, starts, positions=None, rope: Rope = None, q=None,
@@ -1126,20 +1124,19 @@ def paged_append(cache: PagedCache, k, v, starts, positions=None, rope: Rope = N
     p_ptr = _at(positions, _I32, (n,), dev, "positions")
     if rope is not None and rope.device != dev:
         raise ValueError(f"rope: on {rope.device}, expected {dev}")
-    G, q_ref, o_ref = 0, None, None
+    G, cq, co = 0, None, None
     if q is not None:
         G = _group(q, cache.kv_heads, "q")
         q_shp = (n, q.shape[1], cache.head_dim)
         cq = _rows(q, q_shp, dev, "q")
         if q_out is None:
-            q_out = torch.empty(q_shp, dtype=q.dtype, device=dev)
+            q_out = q.new_empty(q_shp)
         co = cq if q_out is q else _rows(q_out, q_shp, dev, "q_out")
-        q_ref, o_ref = _ref(cq), _ref(co)
     elif q_out is not None:
         raise ValueError("q_out: without q")
     rc = lib().kvc_paged_append(cache._ref, _int(n, "n_tokens"), st_ptr, p_ptr,
-                                None if rope is None else rope._ref, _int(G, "group"), q_ref, o_ref,
-                                _ref(ck), _ref(cv), s)
+                                None if rope is None else rope._ref, G, cq, co,
+                                ck, cv, s)
     _check(rc, "kvc_paged_append")
     return cache if q is None else q_out
 
@@ -1168,12 +1165,12 @@ def paged_attend(cache: PagedCache, q, starts, max_new: int = 0, out=None, lse=N
     st_ptr = _starts(cache, starts)
     ws = _scratch(ws, cache.attend_workspace_bytes(G, shp[0], max_new), dev)
     if out is None:
-        out = torch.empty(shp, dtype=q.dtype, device=dev)
+        out = q.new_empty(shp)
     co = _rows(out, shp, dev, "out")
     lse, lse_ptr = (_new(q, shp[:2], torch.float32) if lse is None and want_lse else
                     _given(lse, _F32, shp[:2], dev, "lse"))
     rc = lib().kvc_paged_attend(cache._ref, G, shp[0], _int(max_new, "max_new"), st_ptr, _scale(scale),
-                                _ref(cq), _ref(co), lse_ptr, *_span(ws), s)
+                                cq, co, lse_ptr, *_span(ws), s)
     _check(rc, "kvc_paged_attend")
     return out if lse is None else (out, lse)
 
@@ -1198,13 +1195,13 @@ def prompt_attend(q, k, v, starts, out=None, lse=None, want_lse: bool = False, s
     cq, ck, cv = _rows(q, q.shape, dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
     st_ptr = _at(starts, _I32, starts.shape, dev, "starts")
     if out is None:
-        out = torch.empty((n, heads, d), dtype=q.dtype, device=dev)
+        out = q.new_empty((n, heads, d))
     co = _rows(out, q.shape, dev, "out")
     lse, lse_ptr = (_new(q, (n, heads), torch.float32) if lse is None and want_lse else
                     _given(lse, _F32, (n, heads), dev, "lse"))
     rc = lib().kvc_prompt_attend(_int(starts.shape[0] - 1, "n_seqs"), _int(kv[1], "kv_heads"), G,
                                  _int(d, "head_dim"), _int(n, "n_tokens"), st_ptr, _scale(scale),
-                                 _ref(cq), _ref(ck), _ref(cv), _ref(co), lse_ptr, s)
+                                 cq, ck, cv, co, lse_ptr, s)
     _check(rc, "kvc_prompt_attend")
     return out if lse is None else (out, lse)
 

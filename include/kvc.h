@@ -538,8 +538,8 @@ typedef struct kvc_paged_cache {
 } kvc_paged_cache;
 
 /* Rows of new tokens: value i of head h of token t is the bf16 at data +
- * t * token_stride + h * head_stride + i (strides in values, multiples of 8, data
- * 16-byte aligned).  Rows that are written must not share values: either every
+ * t * token_stride + h * head_stride + i (strides in values, multiples of 8, at most
+ * 2^24 and 2^40; data 16-byte aligned).  Rows that are written must not share values: either every
  * token's heads or every head's tokens lie apart.  An input's strides may be 0.
  * n_tokens: 0..2^23, n_tokens * heads below 2^30.
  *
@@ -596,8 +596,9 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
  * step is 2^-8 of each.  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.
  * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
  * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
- * (a sequence with more counts its first max_new).  group 1..64; kv_heads * (65 * n +
- * n_tokens * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
+ * (a sequence with more counts its first max_new).  group 1..64.  Where group * max_new is
+ * past 32: kv_heads * (n_seqs + n_tokens * group / 128) and kv_heads * (65 * n + n_tokens *
+ * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
  * Preconditions (not checked): q is finite, so are scores times log2(e) in fp32.  A head's results depend on its own length, queries
  * and slots alone.  ws: at least kvc_paged_attend_workspace_bytes(c, group,
  * n_tokens, max_new), 256-byte aligned (may be NULL when that is 0). */
