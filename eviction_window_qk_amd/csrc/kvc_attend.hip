@@ -316,51 +316,62 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
   }
 }
 
-// log2 of a row's sum of 2^x from its pieces', by a wave.
+// The sum of a row's pieces relative to 2^base, by N neighbouring lanes.
+template <int N>
 __device__ __forceinline__ float whole_sum(const float* st, int pieces, float& base) {
-  const int lane = threadIdx.x & 63;
-  const float first = lane < pieces ? st[lane] : -INFINITY;  // the lane's piece of the first 64
+  const int lane = threadIdx.x % N;
+  const float first = lane < pieces ? st[lane] : -INFINITY;  // the lane's first piece
   float M = first;
-  for (int p = lane + 64; p < pieces; p += 64) M = fmaxf(M, st[p]);
+#pragma unroll 8
+  for (int p = lane + N; p < pieces; p += N) M = fmaxf(M, st[p]);
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+  for (int off = N / 2; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
   base = M == -INFINITY ? 0.0f : M;
   float L = fast_exp2(first - base);
-  for (int p = lane + 64; p < pieces; p += 64) L += fast_exp2(st[p] - base);
+#pragma unroll 8
+  for (int p = lane + N; p < pieces; p += N) L += fast_exp2(st[p] - base);
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) L += __shfl_xor(L, off);
+  for (int off = N / 2; off > 0; off >>= 1) L += __shfl_xor(L, off);
   return L;
 }
 
-// Joins the pieces of one row, each weighted by its sum: D/4 lanes read one piece's
-// outputs, the workgroup 1024/D pieces at a time.
-template <int D>
-__device__ __forceinline__ void join_row(const Args& A, int n, int r, float* sums) {
-  constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
+// Joins the pieces of a row, each weighted by its sum: D/4 lanes read one piece's
+// outputs.  Where heads have few pieces (SMALL) a wave takes a row, 256/D pieces at a time;
+// otherwise the workgroup takes one, 1024/D pieces at a time.
+template <int D, bool SMALL>
+__device__ __forceinline__ void join_rows(const Args& A, int n, int block, float* sums) {
+  constexpr int kLanes = D / 4, kAtOnce = (SMALL ? 64 : kThreads) / kLanes;
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
   const int2 mine = chunk_of(A.a.k, b);
-  if (r >= mine.y * A.a.G || mine.y * A.a.G > kFewRows) return;
+  const int R = mine.y * A.a.G, r = SMALL ? block * kWaves + int(threadIdx.x >> 6) : block;
   const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
-  if (len <= chunk) return;
+  if (r >= R || R > kFewRows || len <= chunk) return;
   const int pieces = (len + chunk - 1) / chunk;
-  const int group = threadIdx.x / kLanes, dim = threadIdx.x % kLanes * 4;
+  const int group = int(threadIdx.x) % (SMALL ? 64 : kThreads) / kLanes, dim = threadIdx.x % kLanes * 4;
   const size_t row = size_t(n) * A.rows + r;
   const float* st = A.stat + row * A.pieces;
   const float* part = A.part + row * A.pieces * D + dim;
   float base;
-  const float L = whole_sum(st, pieces, base), by_L = L > 0.0f ? 1.0f / L : 0.0f;
+  const float L = whole_sum<SMALL ? 8 : 64>(st, pieces, base), by_L = L > 0.0f ? 1.0f / L : 0.0f;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 4
   for (int p = group; p < pieces; p += kAtOnce)
     sum += *reinterpret_cast<const f32x4*>(part + size_t(p) * D) * (fast_exp2(st[p] - base) * by_L);
-  *reinterpret_cast<f32x4*>(sums + group * D + dim) = sum;
-  __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  f32x4 out = {0, 0, 0, 0};
+  if constexpr (SMALL) {
 #pragma unroll
-  for (int i = 0; i < kAtOnce; ++i) out += *reinterpret_cast<const f32x4*>(sums + i * D + dim);
+    for (int off = kLanes; off < 64; off <<= 1)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] += __shfl_xor(sum[i], off);
+    if (group > 0) return;
+  } else {
+    *reinterpret_cast<f32x4*>(sums + group * D + dim) = sum;
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int i = 1; i < kAtOnce; ++i) sum += *reinterpret_cast<const f32x4*>(sums + i * D + dim);
+  }
   const int i = int(quot(A.by_G, uint32_t(r)));
-  finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, out, L > 0.0f ? base + fast_log2(L) : -INFINITY);
+  finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, sum, L > 0.0f ? base + fast_log2(L) : -INFINITY);
 }
 
 // What 1024 slots receive from a sequence's few rows: the sum down the rows of 2^(x -
@@ -371,39 +382,40 @@ __device__ __forceinline__ void weigh_slots(const Args& A, int n, int block, flo
   const int b = int(quot(A.by_H, uint32_t(n)));
   const int R = chunk_of(A.a.k, b).y * A.a.G, len = paged_len(c, b);
   if (R > kFewRows || block * kThreads * 4 >= len) return;
-  const int chunk = few_chunk(len), pieces = (len + chunk - 1) / chunk;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int r = wave; r < R; r += kWaves) {
-    float base;
-    const float L = whole_sum(A.stat + (size_t(n) * A.rows + r) * A.pieces, pieces, base);
-    if (lane == 0) less[r] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
-  }
-  __syncthreads();
+  static_assert(kThreads == 8 * kFewRows, "eight lanes a row");
+  const int chunk = few_chunk(len), pieces = (len + chunk - 1) / chunk, row = threadIdx.x >> 3;
+  float base;
+  const float L = whole_sum<8>(A.stat + (size_t(n) * A.rows + row) * A.pieces, row < R ? pieces : 0, base);
+  if (threadIdx.x % 8 == 0) less[row] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
   const int t = (block * kThreads + int(threadIdx.x)) * 4;
+  float* to = c.weight + size_t(n) * c.room + t;
+  float was[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) was[i] = t + i < len ? to[i] : 0.0f;
+  __syncthreads();
   if (t >= len) return;
   const float* x = A.scores + size_t(n) * A.rows * A.score_stride + t;
   f32x4 sum = {0, 0, 0, 0};
-#pragma unroll 4
+#pragma unroll 8
   for (int r = 0; r < R; ++r) {
     const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + less[r]);
   }
-  float* to = c.weight + size_t(n) * c.room + t;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    if (t + i < len && sum[i] > 0.0f) to[i] += sum[i];
+    if (t + i < len && sum[i] > 0.0f) to[i] = was[i] + sum[i];
 }
 
-// Both in one launch, as neither needs the other: of a head's workgroups `rows` join a row
-// each (none where no head has several pieces), the others weigh its slots.
-template <int D>
-__global__ __launch_bounds__(kThreads) void k_join_few(Args A, int rows, FastDiv by_per, int unit0) {
+// Both in one launch, as neither needs the other: of a head's workgroups `joins` join rows
+// (none where no head has several pieces), the others weigh its slots.
+template <int D, bool SMALL>
+__global__ __launch_bounds__(kThreads) void k_join_few(Args A, int joins, FastDiv by_per, int n0) {
   __shared__ __align__(16) float lds[kThreads * 4];
   const uint32_t unit = blockIdx.x, nth = quot(by_per, unit);
-  const int n = unit0 + int(nth), i = int(unit - nth * by_per.d);
-  if (i < rows) join_row<D>(A, n, i, lds);
-  else weigh_slots(A, n, i - rows, lds);
+  const int n = n0 + int(nth), i = int(unit - nth * by_per.d);
+  if (i < joins) join_rows<D, SMALL>(A, n, i, lds);
+  else weigh_slots(A, n, i - joins, lds);
 }
 
 template <int D, int MT, int GROUP>
@@ -426,13 +438,16 @@ void attend_few(Args A, hipStream_t s) {
                                    keys > sums ? keys : sums, s>>>(A);
     }
   }
-  const int rows = A.pieces > 1 ? A.rows : 0;
-  const int per = rows + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
+  const bool small = A.pieces <= 8;
+  const int joins = A.pieces == 1 ? 0 : (small ? (A.rows + kWaves - 1) / kWaves : A.rows);
+  const int per = joins + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
   if (per == 0) return;
   const int most_joined = (1 << 23) / per > 0 ? (1 << 23) / per : 1;
   for (int n0 = 0; n0 < heads; n0 += most_joined) {
     const int nh = heads - n0 < most_joined ? heads - n0 : most_joined;
-    k_join_few<D><<<unsigned(nh) * unsigned(per), kThreads, 0, s>>>(A, rows, fast_div(uint32_t(per)), n0);
+    const unsigned grid = unsigned(nh) * unsigned(per);
+    if (small) k_join_few<D, true><<<grid, kThreads, 0, s>>>(A, joins, fast_div(uint32_t(per)), n0);
+    else k_join_few<D, false><<<grid, kThreads, 0, s>>>(A, joins, fast_div(uint32_t(per)), n0);
   }
 }
 

@@ -169,7 +169,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   const int head = w.h * A.G + rc - i * A.G;
   const int limit = w.len - w.n + i;         // last key this row sees
   const int low = __builtin_amdgcn_readfirstlane(limit);
-  const int high = __builtin_amdgcn_readlane(limit, 31);
+  // A wave without rows helps to load.
+  const int high = w.r0 + wave * 32 < w.R ? __builtin_amdgcn_readlane(limit, 31) : -1;
   const int last_row = w.r0 + kRows <= w.R ? w.r0 + kRows - 1 : w.R - 1;
   // Keys that any row of the tile sees, of these the piece's.
   const int seen = w.len - w.n + int(quot(A.by_G, uint32_t(last_row))) + 1;
@@ -312,6 +313,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
           if (out) sc[blk][e] = -INFINITY;
         }
     }
+    // Matrix instructions go first where the SIMD's two waves want to issue: the one in its
+    // softmax fills the gaps (16384-token prompt -1.5 %, 512 tokens over 131072 slots
+    // -4.5 %; the softmax first: +3.6 %, -1 %).
+    __builtin_amdgcn_s_setprio(0);
     float p[32], sum = 0.0f;
     auto weigh = [&]() {
       float s0 = 0.0f, s1 = 0.0f;
@@ -338,6 +343,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
       weigh();
     }
     l += sum;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int s = 0; s < 4; ++s) {            // 16 keys a step
       const u32x4 pf = {pack_bf16(p[8 * s], p[8 * s + 1]), pack_bf16(p[8 * s + 2], p[8 * s + 3]),
