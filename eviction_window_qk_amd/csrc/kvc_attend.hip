@@ -61,6 +61,12 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 
+template <bool STREAM, class T>
+__device__ __forceinline__ T load(const uint16_t* at) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(at));
+  else return *reinterpret_cast<const T*>(at);
+}
+
 // Four output values of row r of a head, and log2 of its sum of 2^x.
 __device__ __forceinline__ void finish(const Args& A, int token, int head, int dim, f32x4 out, float b) {
   *reinterpret_cast<u32x2*>(A.a.out.p + token * A.a.out.ts + head * A.a.out.hs + dim) =
@@ -69,7 +75,7 @@ __device__ __forceinline__ void finish(const Args& A, int token, int head, int d
     A.a.lse[size_t(token) * (A.a.G * A.a.c.H) + head] = b * 0.6931471805599453f;
 }
 
-template <int D, int MT, int GROUP>
+template <int D, int MT, int GROUP, bool STREAM>
 __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
@@ -153,17 +159,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
       const int key = tile + half * 16 + col;
       const uint16_t* at = c.k + (size_t(where[key / GROUP]) + key % GROUP) * D + g * 8;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) x.k[half][s] = *reinterpret_cast<const u32x4*>(at + s * 32);
+      for (int s = 0; s < kSteps; ++s) x.k[half][s] = load<STREAM, u32x4>(at + s * 32);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int key = tile + (i >> 2) * 16 + 4 * g + (i & 3);
       const uint16_t* at = c.v + (size_t(where[key / GROUP]) + key % GROUP) * D + col * (D / 16);
       if constexpr (kVWords == 4) {
-        const u32x4 y = *reinterpret_cast<const u32x4*>(at);
+        const u32x4 y = load<STREAM, u32x4>(at);
         x.v[i][0] = y.x, x.v[i][1] = y.y, x.v[i][2] = y.z, x.v[i][3] = y.w;
       } else {
-        const u32x2 y = *reinterpret_cast<const u32x2*>(at);
+        const u32x2 y = load<STREAM, u32x2>(at);
         x.v[i][0] = y.x, x.v[i][1] = y.y;
       }
     }
@@ -418,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void k_join_few(Args A, int joins, FastDi
   else weigh_slots(A, n, i - joins, lds);
 }
 
-template <int D, int MT, int GROUP>
+template <int D, int MT, int GROUP, bool STREAM>
 void attend_few(Args A, hipStream_t s) {
   // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits), in
   // whole eights of units.
@@ -434,7 +440,7 @@ void attend_few(Args A, hipStream_t s) {
     A.units = nh * A.pieces;
     for (A.unit0 = 0; A.unit0 < A.units; A.unit0 += room) {
       const int here = A.units - A.unit0 < room ? A.units - A.unit0 : room;
-      k_attend_few<D, MT, GROUP><<<unsigned((here + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
+      k_attend_few<D, MT, GROUP, STREAM><<<unsigned((here + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
                                    keys > sums ? keys : sums, s>>>(A);
     }
   }
@@ -454,12 +460,19 @@ void attend_few(Args A, hipStream_t s) {
 template <int D>
 void attend_rows(const Args& A, hipStream_t s) {
   const bool fours = A.a.c.bs % 4 == 0;
+  // Keys and values that one row block reads, out of pools that are a good part of the
+  // last-level cache (256 MB), are read past the caches, which they would only empty: 89
+  // us against 101 on one sequence of 131072 slots (537 MB), 40.3 against 42.6 on 64
+  // sequences of 1100 that the cache does not hold yet (145 MB; found there again by the next
+  // call, 39 against 34).  Two row blocks: no gain.
+  const bool stream = uint64_t(A.a.c.n_blocks) * A.a.c.H * A.a.c.bs * D * 4 > (uint64_t(96) << 20);
   if (A.rows <= 16) {
-    if (fours) attend_few<D, 1, 4>(A, s);
-    else attend_few<D, 1, 1>(A, s);
+    if (fours && stream) attend_few<D, 1, 4, true>(A, s);
+    else if (fours) attend_few<D, 1, 4, false>(A, s);
+    else attend_few<D, 1, 1, false>(A, s);
   } else {
-    if (fours) attend_few<D, 2, 4>(A, s);
-    else attend_few<D, 2, 1>(A, s);
+    if (fours) attend_few<D, 2, 4, false>(A, s);
+    else attend_few<D, 2, 1, false>(A, s);
   }
 }
 
