@@ -5,13 +5,14 @@
 //   recent    10 | 0 (32)        | position
 //   others    01 | weight (32)   | 2^30 - 1 - position
 // (a weight's bits, turned so that they order as integers).  A workgroup takes one
-// head, each wave a range of its slots, and finds the K-th largest key.  Where at most
-// kSingles slots have to go (a decode step), it takes the smallest key that often.
-// Otherwise it goes digit by digit, eleven bits at a time, from counts in LDS, until the
-// slots that share the digits so far are all needed: three digits hold the class and the
-// whole weight.  Then it lists, in ascending order, the given-up slots below K and the
-// kept ones from K on: as many of either.  A second kernel moves the rows from these to
-// those, the only bytes that have to move.
+// head and finds the K-th largest key.  Where at most kSingles slots have to go (a decode
+// step), it takes the smallest key that often.  Otherwise it goes digit by digit, from
+// counts in LDS, until the slots that share the digits so far are all needed.  Digits are
+// of 11, 11 and 10 bits, so that none crosses from a key's upper word (the class and
+// all but two bits of the weight) into the lower.  Then it lists, in ascending order, the
+// given-up slots below K and the kept ones from K on, as many of either: a thread takes
+// neighbouring slots, and a sum over the workgroup says where its own begin.  A second
+// kernel moves the rows from these to those, the only bytes that have to move.
 //
 // Positions of a head are distinct, so keys are; should they not be, equal keys stay in
 // the order of their slots, and both lists still have the same length.
@@ -22,7 +23,12 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kSingles = 4, kBits = 11, kBins = 1 << kBits;
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+template <class T>
+struct __attribute__((packed, aligned(4))) Loose { T v; };  // at any slot
+
+constexpr int kSingles = 4, kBins = 1 << 11, kHeld = 16384;
 constexpr int kMoveThreads = 256;
 constexpr int kLastPos = (1 << 30) - 1;
 
@@ -36,22 +42,13 @@ struct Evict {
 };
 
 __device__ __forceinline__ uint64_t key_of(float w, int pos, int sinks, int64_t recent_from) {
-  const uint64_t p = uint64_t(pos < 0 ? 0 : (pos < kLastPos ? pos : kLastPos));
-  if (pos < sinks) return (uint64_t(3) << 62) | (kLastPos - p);
-  if (pos >= recent_from) return (uint64_t(2) << 62) | p;
+  const uint32_t p = uint32_t(pos < 0 ? 0 : (pos < kLastPos ? pos : kLastPos)), back = kLastPos - p;
   const uint32_t u = w != w ? 0xff800000u : __float_as_uint(w + 0.0f);  // -0 is 0, NaN -inf
   const uint32_t order = u ^ (u >> 31 ? 0xffffffffu : 0x80000000u);
-  return (uint64_t(1) << 62) | (uint64_t(order) << 30) | (kLastPos - p);
-}
-
-// One count for each lane's bin; the lanes that share the first one's add theirs in one.
-__device__ __forceinline__ void count_bin(int* bins, int bin, bool in) {
-  const uint64_t all = __ballot(in);
-  if (!all) return;
-  const int first = __shfl(bin, __builtin_ctzll(all));
-  const uint64_t same = __ballot(in && bin == first);
-  if (int(threadIdx.x & 63) == __builtin_ctzll(all)) atomicAdd(&bins[first], __builtin_popcountll(same));
-  if (in && bin != first) atomicAdd(&bins[bin], 1);
+  const bool sink = pos < sinks, recent = pos >= recent_from;
+  const uint32_t hi = sink ? 3u << 30 : (recent ? 2u << 30 : 1u << 30 | order >> 2);
+  const uint32_t lo = sink ? back : (recent ? p : order << 30 | back);
+  return uint64_t(hi) << 32 | lo;
 }
 
 // The smaller of two keys, of equal ones that of the later slot.
@@ -59,54 +56,112 @@ __device__ __forceinline__ bool goes_before(uint64_t a, int at, uint64_t b, int 
   return a < b || (a == b && at > bt);
 }
 
-// KPT: slots a thread holds in registers, 0: keys are formed again in every pass.
-template <int NT, int KPT>
-__device__ __forceinline__ void plan(const Evict& E, int n, int b, int len, int* bins) {
+// Place of a tile's key in LDS: neighbouring slots of a thread off the other threads' banks.
+__host__ __device__ constexpr int place(int t) { return t + (t >> 4); }
+
+// HELD: all keys of a head fit the LDS (kHeld of them at most); otherwise they are formed
+// again in every pass, and lie there for the lists, a tile of kHeld at a time.  Of a
+// head of 16384 slots the loads take 5 us (four slots a load, all of a thread's on their way
+// at once; one at a time 16), a digit 3.
+template <int NT, bool HELD>
+__global__ __launch_bounds__(NT) void k_evict_plan(Evict E) {
   constexpr int kWaves = NT / 64;
+  extern __shared__ __align__(16) uint64_t held[];
+  __shared__ int bins[kBins];
   __shared__ int chosen[3];            // digit, slots above it, slots in it
-  __shared__ int totals[kWaves][3];    // equal keys, holes, movers of a wave's range
+  __shared__ int totals[kWaves];
   __shared__ uint64_t low_key[kWaves];
   __shared__ int low_slot[kWaves];
   const Paged& c = E.c;
+  const int n = blockIdx.x, b = n / c.H, len = paged_len(c, b);
   const int K = E.K, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (len <= K) {
+    if (tid == 0) E.count[n] = 0;
+    return;
+  }
   const float* w = c.weight + size_t(n) * c.room;
   const int32_t* pos = c.pos + size_t(n) * c.room;
   const int64_t recent_from = int64_t(E.seen[b]) - E.recent;
-  const int span = ((len + kWaves - 1) / kWaves + 63) & ~63;   // at most KPT * 64
-  const int lo = wave * span, hi = lo + span < len ? lo + span : len;
-  uint64_t held[KPT > 0 ? KPT : 1];
-  if constexpr (KPT > 0) {
+  // Keys of the slots from t0 on to LDS.
+  auto hold = [&](int t0, int count) {
+    constexpr int kAhead = 4;
+    for (int t = 4 * tid; t < count; t += kAhead * 4 * NT) {
+      f32x4 x[kAhead];
+      i32x4 p[kAhead];
 #pragma unroll
-    for (int i = 0; i < KPT; ++i) {
-      const int t = lo + i * 64 + lane;
-      held[i] = t < hi ? key_of(w[t], pos[t], E.sinks, recent_from) : 0;   // keys are above 0
-    }
-  }
-  // f(slot, in, key) for the wave's slots, 64 at a time
-  auto each = [&](auto f) {
-    if constexpr (KPT > 0) {
+      for (int a = 0; a < kAhead; ++a) {
+        const int at = t + a * 4 * NT;
+        if (at + 3 < count) {
+          x[a] = reinterpret_cast<const Loose<f32x4>*>(w + t0 + at)->v;
+          p[a] = reinterpret_cast<const Loose<i32x4>*>(pos + t0 + at)->v;
+        } else {
 #pragma unroll
-      for (int i = 0; i < KPT; ++i)
-        if (lo + i * 64 < hi) f(lo + i * 64 + lane, lo + i * 64 + lane < hi, held[i]);
-    } else {
-      for (int t = lo; t < hi; t += 64) {
-        const bool in = t + lane < hi;
-        f(t + lane, in, in ? key_of(w[t + lane], pos[t + lane], E.sinks, recent_from) : 0);
+          for (int i = 0; i < 4; ++i) {
+            x[a][i] = at + i < count ? w[t0 + at + i] : 0.0f;
+            p[a][i] = at + i < count ? pos[t0 + at + i] : 0;
+          }
+        }
       }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (t + a * 4 * NT + i < count)
+            held[place(t + a * 4 * NT + i)] = key_of(x[a][i], p[a][i], E.sinks, recent_from);
+    }
+    __syncthreads();
+  };
+  if (HELD) hold(0, len);
+  // f(slot, key) in any order, four keys read ahead
+  auto each = [&](auto f) {
+    constexpr int kAhead = 4;
+    for (int t0 = tid; t0 < len; t0 += kAhead * NT) {
+      uint64_t x[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        const int t = t0 + a * NT;
+        x[a] = 0;
+        if (t < len) x[a] = HELD ? held[place(t)] : key_of(w[t], pos[t], E.sinks, recent_from);
+      }
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (t0 + a * NT < len) f(t0 + a * NT, x[a]);
     }
   };
+  // Sum over the threads before; all of it in `whole`.
+  auto sum_before = [&](int x, int& whole) {
+    int sum = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(sum, off);
+      sum += lane >= off ? o : 0;
+    }
+    if (lane == 63) totals[wave] = sum;
+    __syncthreads();
+    sum -= x;
+    whole = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      const int o = totals[i];
+      sum += i < wave ? o : 0;
+      whole += o;
+    }
+    __syncthreads();
+    return sum;
+  };
 
-  // Keys from `cut` on stay once shifted by `shift`, of those equal to it `need` do.
+  // Which slots stay.  SINGLES: those whose key is past (cut, cut_slot); ALL: those whose
+  // shifted key is at least cut; else those past cut and the first `need` of it.
+  enum { SINGLES, ALL, SOME } which = SOME;
   uint64_t cut = 0;
-  int shift = 0, need = 0;
+  int shift = 64, need = K, cut_slot = 0x7fffffff;
   if (len - K <= kSingles) {
-    uint64_t last = 0;
-    int last_slot = 0x7fffffff;
+    which = SINGLES;
     for (int m = 0; m < len - K; ++m) {
       uint64_t key = ~uint64_t(0);
       int slot = -1;
-      each([&](int t, bool in, uint64_t x) {
-        if (in && goes_before(last, last_slot, x, t) && goes_before(x, t, key, slot)) key = x, slot = t;
+      each([&](int t, uint64_t x) {
+        if (goes_before(cut, cut_slot, x, t) && goes_before(x, t, key, slot)) key = x, slot = t;
       });
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) {
@@ -121,117 +176,86 @@ __device__ __forceinline__ void plan(const Evict& E, int n, int b, int len, int*
       for (int i = 1; i < kWaves; ++i)
         if (goes_before(low_key[i], low_slot[i], key, slot)) key = low_key[i], slot = low_slot[i];
       __syncthreads();
-      last = key, last_slot = slot;
+      cut = key, cut_slot = slot;
     }
-    // Slots of the last one's key that are not past it stay.
-    cut = last;
-    int equal = 0;
-    each([&](int t, bool in, uint64_t x) {
-      equal += __builtin_popcountll(__ballot(in && x == cut && t < last_slot));
-    });
-    if (lane == 0) totals[wave][0] = equal;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) need += totals[i][0];
-    __syncthreads();
   } else {
-    need = K;
-    shift = 64;
-    while (shift > 0) {
-      const int bits = shift < kBits ? shift : kBits;
+    while (shift > 0 && which != ALL) {
+      const int bits = (shift & 31) == 10 ? 10 : 11;
       shift -= bits;
       for (int i = tid; i < kBins; i += NT) bins[i] = 0;
       __syncthreads();
-      each([&](int t, bool in, uint64_t x) {
-        // (two shifts: one by all 64 bits is none)
-        count_bin(bins, int(x >> shift) & ((1 << bits) - 1), in && ((x >> shift) >> bits) == cut);
+      const bool upper = shift >= 32;
+      const int by = shift & 31;
+      const uint32_t cut_hi = upper ? 0 : uint32_t(cut >> (32 - by - bits));   // the whole upper word, once it is known
+      const uint32_t cut_now = upper ? uint32_t(cut) : uint32_t(cut & ((uint64_t(1) << (32 - by - bits)) - 1));
+      each([&](int, uint64_t x) {
+        const uint32_t word = upper ? uint32_t(x >> 32) : uint32_t(x), digit = word >> by;
+        // the digits above in this word: none for the first
+        const bool same = by + bits == 32 || (word >> (by + bits)) == cut_now;
+        if (same && (upper || uint32_t(x >> 32) == cut_hi)) atomicAdd(&bins[digit & ((1u << bits) - 1)], 1);
       });
       __syncthreads();
-      if (wave == 0) {   // the digit that the need-th largest has: a run of bins a lane, from the top
-        constexpr int kRun = kBins / 64;
-        int sum = 0;
-#pragma unroll 8
-        for (int i = 0; i < kRun; ++i) sum += bins[kBins - 1 - (kRun * lane + i)];
-        int above = sum;
+      // The digit that the need-th largest has: a run of bins a thread, from the top.
+      constexpr int kRun = kBins / NT;
+      int mine[kRun], sum = 0, whole;
 #pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-          const int o = __shfl_up(above, off);
-          above += lane >= off ? o : 0;
-        }
-        above -= sum;    // in the bins of the lanes before
-        if (above < need && above + sum >= need) {   // one lane's
-          int i = kBins - 1 - kRun * lane;
-          while (above + bins[i] < need) above += bins[i--];
-          chosen[0] = i;
+      for (int i = 0; i < kRun; ++i) sum += mine[i] = bins[kBins - 1 - (kRun * tid + i)];
+      int above = sum_before(sum, whole);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (above < need && above + mine[i] >= need) {   // one thread's
+          chosen[0] = kBins - 1 - (kRun * tid + i);
           chosen[1] = above;
-          chosen[2] = bins[i];
+          chosen[2] = mine[i];
         }
+        above += mine[i];
       }
       __syncthreads();
       cut = (cut << bits) | uint64_t(chosen[0]);
       need -= chosen[1];
-      const bool all = chosen[2] == need;
-      __syncthreads();   // before the bins and the choice are written again
-      if (all) break;
+      if (chosen[2] == need) which = ALL;
     }
+    if (which == ALL) cut <<= shift;
   }
 
-  // Each wave counts in its range, and writes its part of the lists.
-  int equal = 0;
-  each([&](int t, bool in, uint64_t x) { equal += __builtin_popcountll(__ballot(in && (x >> shift) == cut)); });
-  if (lane == 0) totals[wave][0] = equal;
-  __syncthreads();
-  int before = 0;
-  for (int i = 0; i < wave; ++i) before += totals[i][0];
-  const uint64_t below = (uint64_t(1) << lane) - 1;
-  auto stays = [&](bool in, uint64_t x, int& eq) {   // eq: equal keys before these 64 slots
-    x >>= shift;
-    const uint64_t m = __ballot(in && x == cut);
-    const bool yes = in && (x > cut || (x == cut && eq + __builtin_popcountll(m & below) < need));
-    eq += __builtin_popcountll(m);
-    return yes;
-  };
-  int eq = before, holes = 0, movers = 0;
-  each([&](int t, bool in, uint64_t x) {
-    const bool yes = stays(in, x, eq);
-    holes += __builtin_popcountll(__ballot(in && !yes && t < K));
-    movers += __builtin_popcountll(__ballot(yes && t >= K));
-  });
-  if (lane == 0) totals[wave][1] = holes, totals[wave][2] = movers;
-  __syncthreads();
-  int hole0 = 0, mover0 = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    if (i < wave) hole0 += totals[i][1], mover0 += totals[i][2];
-    total += totals[i][2];
-  }
-  eq = before;
   int32_t* const to = E.to + size_t(n) * E.most;
   int32_t* const from = E.from + size_t(n) * E.most;
-  each([&](int t, bool in, uint64_t x) {
-    const bool yes = stays(in, x, eq), hole = in && !yes && t < K, mover = yes && t >= K;
-    const uint64_t mh = __ballot(hole), mm = __ballot(mover);
-    if (hole) to[hole0 + __builtin_popcountll(mh & below)] = t;
-    if (mover) from[mover0 + __builtin_popcountll(mm & below)] = t;
-    hole0 += __builtin_popcountll(mh);
-    mover0 += __builtin_popcountll(mm);
-  });
-  if (tid == 0) E.count[n] = total;
-}
-
-template <int NT>
-__global__ __launch_bounds__(NT) void k_evict_plan(Evict E) {
-  __shared__ int bins[kBins];
-  const int n = blockIdx.x, b = n / E.c.H, len = paged_len(E.c, b);
-  if (len <= E.K) {
-    if (threadIdx.x == 0) E.count[n] = 0;
-  } else if (len <= 4 * NT) {
-    plan<NT, 4>(E, n, b, len, bins);
-  } else if (len <= 16 * NT) {
-    plan<NT, 16>(E, n, b, len, bins);
-  } else {
-    plan<NT, 0>(E, n, b, len, bins);
+  int equal = 0, n_holes = 0, n_movers = 0;   // of the tiles before: slots of the cut's key, listed ones
+  for (int t0 = 0; t0 < len; t0 += kHeld) {
+    const int count = len - t0 < kHeld ? len - t0 : kHeld;
+    if (!HELD) hold(t0, count);
+    const int per = (count + NT - 1) / NT, lo = tid * per, hi = lo + per < count ? lo + per : count;
+    uint32_t stay = 0;                 // bit i: slot lo + i; at most kHeld / NT of them
+    if (which == SOME) {
+      int mine = 0, whole;
+      for (int t = lo; t < hi; ++t) mine += held[place(t)] == cut;
+      int at = equal + sum_before(mine, whole);
+      equal += whole;
+      for (int t = lo; t < hi; ++t) {
+        const uint64_t x = held[place(t)];
+        if (x > cut || (x == cut && at++ < need)) stay |= 1u << (t - lo);
+      }
+    } else {
+#pragma unroll 4
+      for (int t = lo; t < hi; ++t) {
+        const uint64_t x = held[place(t)];
+        const bool yes = which == ALL ? x >= cut : goes_before(cut, cut_slot, x, t0 + t);
+        stay |= uint32_t(yes) << (t - lo);
+      }
+    }
+    const int here = hi > lo ? hi - lo : 0, below = K - t0 - lo;     // slots, those below K
+    const uint32_t all = (1u << here) - 1, low = below >= here ? all : (below > 0 ? (1u << below) - 1 : 0);
+    uint32_t holes = ~stay & low, movers = stay & all & ~low;
+    int whole;
+    const int before = sum_before(__builtin_popcount(holes) | __builtin_popcount(movers) << 16, whole);
+    int h = n_holes + (before & 0xffff), m = n_movers + (before >> 16);
+    for (; holes; holes &= holes - 1) to[h++] = t0 + lo + __builtin_ctz(holes);
+    for (; movers; movers &= movers - 1) from[m++] = t0 + lo + __builtin_ctz(movers);
+    n_holes += whole & 0xffff;
+    n_movers += whole >> 16;
+    if (!HELD) __syncthreads();        // before the next tile's keys
   }
+  if (tid == 0) E.count[n] = n_movers;
 }
 
 // A row's 16-byte pieces by D/8 lanes; the lists' slots are disjoint, so the order does
@@ -282,8 +306,10 @@ hipError_t launch_paged_evict(const Paged& c, const int32_t* seen, int K, int si
   E.from = ws + heads;
   E.to = E.from + size_t(heads) * E.most;
   // By the longest length there can be: few waves meet sooner.
-  if (c.cap <= 2048) k_evict_plan<256><<<unsigned(heads), 256, 0, s>>>(E);
-  else k_evict_plan<1024><<<unsigned(heads), 1024, 0, s>>>(E);
+  const auto lds = [](int slots) { return size_t(place(slots)) * 8; };
+  if (c.cap <= 2048) k_evict_plan<256, true><<<unsigned(heads), 256, lds(c.cap), s>>>(E);
+  else if (c.cap <= kHeld) k_evict_plan<1024, true><<<unsigned(heads), 1024, lds(c.cap), s>>>(E);
+  else k_evict_plan<1024, false><<<unsigned(heads), 1024, lds(kHeld), s>>>(E);
   // About 2048 workgroups where the heads are fewer.
   const int per = kMoveThreads / (c.D / 8), need = (E.most + per - 1) / per;
   int y = heads < 2048 ? 2048 / heads : 1;

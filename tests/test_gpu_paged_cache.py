@@ -289,6 +289,11 @@ EVICT = [
     (1, 1, 64, 16, [1000], 3, 10, 10, "random"),           # more sinks than budget
     (2, 1, 64, 16, [90, 80], 50, 0, 100, "random"),        # all are recent
     (1, 3, 64, 256, [5000], 2500, 4, 64, "spread"),
+    (2, 1, 64, 64, [16384, 16380], 5000, 4, 64, "random"),
+    (2, 1, 64, 256, [40000, 16385], 20000, 4, 64, "spread"),
+    (1, 2, 64, 256, [33000], 32996, 4, 64, "random"),
+    (1, 1, 64, 256, [33000], 9000, 0, 0, "ties"),
+    (1, 2, 64, 64, [2049], 2040, 4, 8, "odd"),
 ]
 
 
@@ -327,12 +332,13 @@ def test_evict(case):
 
 def test_evict_with_positions_that_repeat_stays_in_bounds():
     """Against the precondition: the counts still fit, ties stay in the order of the slots."""
-    c, seen, K, sinks, recent = _evict_case((2, 2, 64, 16, [300, 150], 100, 0, 0, "zero"))
-    c.pos[:] = 5
-    g = u.to_gpu(c)
-    kvc.paged_evict(g, u.dev(seen), K, sinks=sinks, recent=recent)
-    og.evict(c, seen, K, sinks, recent)
-    u.same_cache(g, c)
+    for lens, K, sinks in (([300, 150], 100, 0), ([300, 150], 148, 0), ([300, 103], 100, 9), ([20000, 3000], 2500, 0)):
+        c, seen, K, sinks, recent = _evict_case((2, 2, 64, 16, lens, K, sinks, 0, "zero"))
+        c.pos[:] = 5
+        g = u.to_gpu(c)
+        kvc.paged_evict(g, u.dev(seen), K, sinks=sinks, recent=recent)
+        og.evict(c, seen, K, sinks, recent)
+        u.same_cache(g, c)
 
 
 @pytest.mark.parametrize("seed", range(4))
