@@ -342,28 +342,35 @@ __device__ __forceinline__ float whole_sum(const float* st, int pieces, float& b
 }
 
 // Joins the pieces of a row, each weighted by its sum: D/4 lanes read one piece's
-// outputs.  Where heads have few pieces (SMALL) a wave takes a row, 256/D pieces at a time;
-// otherwise the workgroup takes one, 1024/D pieces at a time.
+// outputs.  A row of at most kFewPieces of them is joined by a wave (256/D pieces at a
+// time), one of more by the workgroup (1024/D at a time): the row's own count decides, so that
+// its sums are taken in the same order in every call.  In a call where no head has more
+// (SMALL) a workgroup takes a row a wave, otherwise one.
+constexpr int kFewPieces = 8;
 template <int D, bool SMALL>
 __device__ __forceinline__ void join_rows(const Args& A, int n, int block, float* sums) {
-  constexpr int kLanes = D / 4, kAtOnce = (SMALL ? 64 : kThreads) / kLanes;
+  constexpr int kLanes = D / 4;
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * A.a.c.H;
   const int2 mine = chunk_of(A.a.k, b);
   const int R = mine.y * A.a.G, r = SMALL ? block * kWaves + int(threadIdx.x >> 6) : block;
   const int len = paged_len(A.a.c, b), chunk = few_chunk(len);
   if (r >= R || R > kFewRows || len <= chunk) return;
   const int pieces = (len + chunk - 1) / chunk;
-  const int group = int(threadIdx.x) % (SMALL ? 64 : kThreads) / kLanes, dim = threadIdx.x % kLanes * 4;
+  const bool by_wave = SMALL || pieces <= kFewPieces;
+  if (!SMALL && by_wave && threadIdx.x >= 64) return;
+  const int at_once = (by_wave ? 64 : kThreads) / kLanes, thread = SMALL ? threadIdx.x % 64 : threadIdx.x;
+  const int group = thread / kLanes, dim = thread % kLanes * 4;
   const size_t row = size_t(n) * A.rows + r;
   const float* st = A.stat + row * A.pieces;
   const float* part = A.part + row * A.pieces * D + dim;
   float base;
-  const float L = whole_sum<SMALL ? 8 : 64>(st, pieces, base), by_L = L > 0.0f ? 1.0f / L : 0.0f;
+  const float L = by_wave ? whole_sum<kFewPieces>(st, pieces, base) : whole_sum<64>(st, pieces, base);
+  const float by_L = L > 0.0f ? 1.0f / L : 0.0f;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 4
-  for (int p = group; p < pieces; p += kAtOnce)
+  for (int p = group; p < pieces; p += at_once)
     sum += *reinterpret_cast<const f32x4*>(part + size_t(p) * D) * (fast_exp2(st[p] - base) * by_L);
-  if constexpr (SMALL) {
+  if (by_wave) {
 #pragma unroll
     for (int off = kLanes; off < 64; off <<= 1)
 #pragma unroll
@@ -373,8 +380,7 @@ __device__ __forceinline__ void join_rows(const Args& A, int n, int block, float
     *reinterpret_cast<f32x4*>(sums + group * D + dim) = sum;
     __syncthreads();
     if (group > 0) return;
-#pragma unroll
-    for (int i = 1; i < kAtOnce; ++i) sum += *reinterpret_cast<const f32x4*>(sums + i * D + dim);
+    for (int i = 1; i < at_once; ++i) sum += *reinterpret_cast<const f32x4*>(sums + i * D + dim);
   }
   const int i = int(quot(A.by_G, uint32_t(r)));
   finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, sum, L > 0.0f ? base + fast_log2(L) : -INFINITY);
@@ -444,7 +450,7 @@ void attend_few(Args A, hipStream_t s) {
                                    keys > sums ? keys : sums, s>>>(A);
     }
   }
-  const bool small = A.pieces <= 8;
+  const bool small = A.pieces <= kFewPieces;
   const int joins = A.pieces == 1 ? 0 : (small ? (A.rows + kWaves - 1) / kWaves : A.rows);
   const int per = joins + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
   if (per == 0) return;
