@@ -80,11 +80,15 @@ __device__ __forceinline__ int swizzle(int row) {
   else return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
 }
 
-typedef __attribute__((address_space(3))) void* LdsPtr;
-
-__device__ __forceinline__ void to_lds(const void* from, void* to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
-                                   (LdsPtr)to, 16, 0, 0);
+// 16 bytes a lane from global memory to LDS, lane l's to `to` + 16 l, past the registers.
+// In assembly, as the compiler takes the builtin's store for one that any later read of
+// LDS may want, and waits for the tile on its way before it reads the one that is there
+// (16384-token prompt: 2060 us).  The instruction writes no register; whoever reads the
+// tile waits for it (s_waitcnt) and meets the other waves (barrier) first.
+__device__ __forceinline__ void to_lds(const void* from, const void* to) {
+  const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) const void*)to));
+  asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+               :: "v"(from), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory");
 }
 __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
   return __builtin_bit_cast(
