@@ -83,8 +83,9 @@ __device__ __forceinline__ int swizzle(int row) {
 // 16 bytes a lane from global memory to LDS, lane l's to `to` + 16 l, past the registers.
 // In assembly, as the compiler takes the builtin's store for one that any later read of
 // LDS may want, and waits for the tile on its way before it reads the one that is there
-// (16384-token prompt: 2060 us).  The instruction writes no register; whoever reads the
-// tile waits for it (s_waitcnt) and meets the other waves (barrier) first.
+// (512 tokens over 131072 slots 1220 us for 1147, a 16384-token prompt 2056 for 2025).
+// The instruction writes no register; whoever reads the tile waits for it (s_waitcnt) and
+// meets the other waves (barrier) first.
 __device__ __forceinline__ void to_lds(const void* from, const void* to) {
   const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) const void*)to));
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
@@ -122,13 +123,13 @@ __device__ __forceinline__ bool find(const Args& A, Where& w) {
   if (w.slot < 0) return false;
   const int G = A.G;
   const auto first = [G](int s, int b) { return PAGED ? first_slot(s, b, G) : first_tile(s, b, G); };
-  w.b = last_at_or_below(A.k.starts, A.k.B, w.slot, first);
+  w.b = last_at_or_below(A.k, w.slot, first);
   const int2 mine = chunk_of(A.k, w.b);
   w.h = int(h);
   w.token0 = mine.x;
   w.n = mine.y;
   w.R = mine.y * G;
-  const int s = w.slot - first(A.k.starts[w.b], w.b);
+  const int s = w.slot - first(mine.x, w.b);
   w.tiles = (w.R + kRows - 1) / kRows;
   if (PAGED) {
     if (w.R <= kFewRows || s < 0) return false;
@@ -402,9 +403,9 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
   const int G = A.G;
   const int h = int(quot(by_tiles, blockIdx.x)), tile = int(blockIdx.x) - h * int(by_tiles.d);
-  const int b = last_at_or_below(A.k.starts, A.k.B, tile, [G](int s, int i) { return first_tile(s, i, G); });
+  const int b = last_at_or_below(A.k, tile, [G](int s, int i) { return first_tile(s, i, G); });
   const int2 mine = chunk_of(A.k, b);
-  const int R = mine.y * G, start = A.k.starts[b], t = tile - first_tile(start, b, G);
+  const int R = mine.y * G, start = mine.x, t = tile - first_tile(start, b, G);
   if (R <= kFewRows || t < 0) return;
   const int tiles = (R + kRows - 1) / kRows, pieces = tile_pieces(paged_len(A.c, b), tiles);
   const int in_tile = int(blockIdx.y) * kAtOnce + int(threadIdx.x) / kLanes, r = t * kRows + in_tile;
@@ -559,7 +560,7 @@ void attend_chunks(Args& A, hipStream_t s) {
   }
   if (!A.c.weight) return;
   const int chunks = (A.c.cap + kKeys - 1) / kKeys;
-  const int heads = A.c.B * A.H, most = (1 << 23) / chunks > 0 ? (1 << 23) / chunks : 1;
+  const int heads = A.c.B * A.H, most = (1 << 23) / chunks;
   for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
     const int nh = heads - n0 < most ? heads - n0 : most;
     k_weights_tiles<D><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);

@@ -59,23 +59,29 @@ __device__ __forceinline__ int64_t paged_row(const Paged& c, int b, int h, int t
                   : (int64_t(page) * c.H + h) * c.bs + int64_t(uint32_t(t) - j * uint32_t(c.bs));
 }
 
+// First token of sequence b, whatever starts holds.
+__device__ __forceinline__ int start_of(const Chunks& k, int b) {
+  const int a = k.starts[b];
+  return a < 0 ? 0 : (a < k.n_tokens ? a : k.n_tokens);
+}
+
 // First token and token count of sequence b, whatever starts holds.
 __device__ __forceinline__ int2 chunk_of(const Chunks& k, int b) {
-  int a = k.starts[b], e = k.starts[b + 1];
-  a = a < 0 ? 0 : (a < k.n_tokens ? a : k.n_tokens);
+  const int a = start_of(k, b);
+  int e = k.starts[b + 1];
   e = e < a ? a : (e < k.n_tokens ? e : k.n_tokens);
   return make_int2(a, e - a < k.max_new ? e - a : k.max_new);
 }
 
-// The last b in [0, B) with f(starts[b], b) <= x (0 if there is none), f ascending in
+// The last b in [0, B) with f(start_of(b), b) <= x (0 if there is none), f ascending in
 // both: 64 candidates a step, one for each lane.
 template <class F>
-__device__ __forceinline__ int last_at_or_below(const int32_t* starts, int B, int x, F f) {
+__device__ __forceinline__ int last_at_or_below(const Chunks& k, int x, F f) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, n = B;
+  int lo = 0, n = k.B;
   while (n > 1) {
     const int step = (n + 63) >> 6, i = lane * step;
-    const bool in = i < n && f(starts[lo + i], lo + i) <= x;
+    const bool in = i < n && f(start_of(k, lo + i), lo + i) <= x;
     const uint64_t m = __ballot(in);
     const int at = m ? (63 - __builtin_clzll(m)) * step : 0;
     lo += at;

@@ -121,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void k_paged_append(
     Rows q, Rows q_out, Rows k_new, Rows v_new) {
   __shared__ Turns t;
   const int token = blockIdx.x, D = c.D;
-  const int b = last_at_or_below(k.starts, k.B, token, [](int s, int) { return s; });
+  const int b = last_at_or_below(k, token, [](int s, int) { return s; });
   const int2 mine = chunk_of(k, b);
   const int i_new = token - mine.x;
   if (i_new < 0 || i_new >= mine.y) return;

@@ -208,6 +208,28 @@ def test_attend(case, weights):
         np.testing.assert_allclose(a, b, rtol=0, atol=2.0 ** -8 * max(1.0, float(b.max())))
 
 
+@pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_starts_outside_the_tokens_are_taken_as_clamped(d, weights):
+    """Sequences of few and of many rows, in pieces, over starts below 0 and past n."""
+    lens, n = [1300, 900, 700], 240
+    c = u.random_cache(22, 3, 2, d, 16, lens, weights=weights)
+    q = dev_bf16(random_rows(23, n, 4, d))
+    for bad, good in (([-300, 100, 110, 10 ** 9], [0, 100, 110, n]), ([-2 ** 31, -5, 200, 2 ** 31 - 1], [0, 0, 200, n])):
+        got = []
+        for starts in (good, bad):
+            g = u.to_gpu(c)
+            out = torch.full((n, 4, d), 7.0, dtype=torch.bfloat16, device="cuda")
+            _, lse = kvc.paged_attend(g, q, u.dev(np.int32(starts)), out=out, want_lse=True)
+            kvc.paged_append(g, q[:, :2], q[:, 2:], u.dev(np.int32(starts)))
+            kvc.prompt_attend(q, q[:, :2], q[:, 2:], u.dev(np.int32(starts)), out=(by := torch.zeros_like(out)))
+            torch.cuda.synchronize()
+            got.append([u.bits(out), lse.cpu().numpy(), u.bits(g.k_pool), u.bits(by)] +
+                       ([g.weight.cpu().numpy()] if weights else []))
+        for a, b in zip(*got):
+            np.testing.assert_array_equal(a, b)
+
+
 def test_a_scale_and_scores_that_climb():
     """Scores rise by hundreds from key to key, and the reverse."""
     d, T = 64, 700
