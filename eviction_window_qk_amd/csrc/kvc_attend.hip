@@ -44,8 +44,8 @@ struct Args {
   int pieces, rows;  // of the longest length and the longest chunk: the grid's and the partials'
   int blocks;        // row blocks
   FastDiv by_G, by_pieces, by_H, by_blocks;
-  int units, unit0;  // (head, piece) pairs of n0's heads, first one of this launch
-  int n0;            // first head of this launch
+  int units;         // (head, piece) pairs of this launch
+  int n0;            // its first head
   float* part;       // [n][row][piece][D] outputs of a piece
   float* stat;       // [n][row][piece] log2 of its sum of 2^x
   float* scores;     // NULL, or [n][row][score_stride] x
@@ -59,7 +59,6 @@ __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
                                                  __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-
 
 template <bool STREAM, class T>
 __device__ __forceinline__ T load(const uint16_t* at) {
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
   // reads its keys once.
   const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
   const int rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
-  const uint32_t unit = uint32_t(A.unit0) + eight * 8 + (blockIdx.x & 7);
+  const uint32_t unit = eight * 8 + (blockIdx.x & 7);
   if (unit >= uint32_t(A.units)) return;
   const int nth = int(quot(A.by_pieces, unit));
   int piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
@@ -437,24 +436,21 @@ void attend_few(Args A, hipStream_t s) {
   const int heads = A.a.c.B * A.a.c.H;
   A.blocks = (A.rows + MT * 16 - 1) / (MT * 16);
   const int room = ((1 << 23) / A.blocks) & ~7;
-  const int most = room / A.pieces > 0 ? room / A.pieces : 1;
+  const int most = room / A.pieces;    // a head has 2^19 pieces at most
   A.by_blocks = fast_div(uint32_t(A.blocks));
   const size_t keys = size_t(A.a.c.cap < kFewMaxChunk ? ((A.a.c.cap < kFewChunk ? kFewChunk : A.a.c.cap) + 127) & ~127 : kFewMaxChunk) / GROUP * 4;
   const size_t sums = size_t(kWaves) * 16 * (D + 4) * sizeof(float);
   for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
     const int nh = heads - A.n0 < most ? heads - A.n0 : most;
     A.units = nh * A.pieces;
-    for (A.unit0 = 0; A.unit0 < A.units; A.unit0 += room) {
-      const int here = A.units - A.unit0 < room ? A.units - A.unit0 : room;
-      k_attend_few<D, MT, GROUP, STREAM><<<unsigned((here + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
-                                   keys > sums ? keys : sums, s>>>(A);
-    }
+    k_attend_few<D, MT, GROUP, STREAM><<<unsigned((A.units + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
+                                         keys > sums ? keys : sums, s>>>(A);
   }
   const bool small = A.pieces <= kFewPieces;
   const int joins = A.pieces == 1 ? 0 : (small ? (A.rows + kWaves - 1) / kWaves : A.rows);
   const int per = joins + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
   if (per == 0) return;
-  const int most_joined = (1 << 23) / per > 0 ? (1 << 23) / per : 1;
+  const int most_joined = (1 << 23) / per;   // per: 2^20 + 32 at most
   for (int n0 = 0; n0 < heads; n0 += most_joined) {
     const int nh = heads - n0 < most_joined ? heads - n0 : most_joined;
     const unsigned grid = unsigned(nh) * unsigned(per);

@@ -10,6 +10,7 @@ namespace kvc {
 namespace {
 
 constexpr int kMaxTokens = 1 << 23;   // a workgroup a token, the grid's limit
+constexpr int64_t kMaxHeads = 1 << 24;   // query heads of a token: a workgroup counts their pieces in 31 bits
 constexpr int64_t kMaxTokenStride = 1 << 24, kMaxHeadStride = int64_t(1) << 40;  // 64 tokens lie within 2^32 bytes
 
 size_t pool_bytes(const kvc_paged_cache* c) {
@@ -127,13 +128,22 @@ int attend_shape(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int3
   if (rc != KVC_OK) return rc;
   if (group < 1 || n_tokens < 0 || n_tokens > kMaxTokens || max_new < 0) return KVC_EINVAL;
   if (group > 64) return KVC_EUNSUPPORTED;
-  if (int64_t(n_tokens) * group * d->H >= (int64_t(1) << 30)) return KVC_EINVAL;
+  if (int64_t(group) * d->H > kMaxHeads || int64_t(n_tokens) * group * d->H >= (int64_t(1) << 30))
+    return KVC_EINVAL;
   *k = {nullptr, d->B, n_tokens, max_new > 0 && max_new < n_tokens ? max_new : n_tokens};
   if (int64_t(group) * k->max_new > kFewRows &&   // workgroups of a launch
       (int64_t(first_slot(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23) ||
        int64_t(first_tile(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23)))
     return KVC_EINVAL;
   return KVC_OK;
+}
+
+// What kvc_paged_evict and its workspace are asked for (no pointers).  A launch has
+// below 2^32 work-items, and a long head is planned by 1024 of them.
+int evict_shape(const kvc_paged_cache* c, int32_t budget, Paged* d) {
+  const int rc = paged_shape(c, d);
+  if (rc != KVC_OK) return rc;
+  return budget < 1 || int64_t(d->B) * d->H >= (int64_t(1) << 22) ? KVC_EINVAL : KVC_OK;
 }
 
 bool scale_ok(float scale) { return scale >= 0.0f && scale <= 0x1p127f; }
@@ -190,7 +200,8 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
   if (q && (!rope || group < 1)) return KVC_EINVAL;
   if (q && group > 64) return KVC_EUNSUPPORTED;
   if (!q && q_out) return KVC_EINVAL;
-  if (q && int64_t(n_tokens) * group * d.H >= (int64_t(1) << 30)) return KVC_EINVAL;
+  if (q && (int64_t(group) * d.H > kMaxHeads || int64_t(n_tokens) * group * d.H >= (int64_t(1) << 30)))
+    return KVC_EINVAL;
   if (d.B == 0 || n_tokens == 0) return KVC_OK;
   if ((rc = paged_pointers(c)) != KVC_OK) return rc;
   if (!starts) return KVC_EINVAL;
@@ -304,7 +315,7 @@ int kvc_prompt_attend(int32_t n_seqs, int32_t kv_heads, int32_t group, int32_t h
 
 size_t kvc_paged_evict_workspace_bytes(const kvc_paged_cache* c, int32_t budget) {
   Paged d;
-  if (paged_shape(c, &d) != KVC_OK || budget < 1) return 0;
+  if (evict_shape(c, budget, &d) != KVC_OK) return 0;
   const size_t n = evict_ws(d, budget);
   return n > 0 ? n : 256;
 }
@@ -312,9 +323,9 @@ size_t kvc_paged_evict_workspace_bytes(const kvc_paged_cache* c, int32_t budget)
 int kvc_paged_evict(const kvc_paged_cache* c, const int32_t* seen, int32_t budget, int32_t sinks,
                     int32_t recent, void* ws, size_t ws_bytes, void* stream) {
   Paged d;
-  int rc = paged_shape(c, &d);
+  int rc = evict_shape(c, budget, &d);
   if (rc != KVC_OK) return rc;
-  if (budget < 1 || sinks < 0 || recent < 0) return KVC_EINVAL;
+  if (sinks < 0 || recent < 0) return KVC_EINVAL;
   if (d.B == 0) return KVC_OK;
   if ((rc = paged_pointers(c)) != KVC_OK) return rc;
   if (!c->weight || !seen) return KVC_EINVAL;

@@ -516,7 +516,8 @@ size_t kvc_pages_workspace_bytes(const kvc_page_table* t, int32_t n_pairs);
  * weight, pos (both or neither; f32 and i32 [n_seqs * kv_heads][table_blocks *
  * block_size]): what each slot of each head has received from the attention so
  * far, and the position in the text that it holds (an eviction leaves other
- * positions to each head, in any order).
+ * positions to each head, in any order).  They belong to the sequence, not to its pages:
+ * whoever forks a sequence by kvc_pages_fork copies its rows of them.
  * Preconditions (not checked): the rows of attended slots are finite, and a page
  * that is written belongs to one entry of the table. */
 typedef struct kvc_paged_cache {
@@ -539,9 +540,9 @@ typedef struct kvc_paged_cache {
 
 /* Rows of new tokens: value i of head h of token t is the bf16 at data +
  * t * token_stride + h * head_stride + i (strides in values, multiples of 8, at most
- * 2^24 and 2^40; data 16-byte aligned).  Rows that are written must not share values: either every
- * token's heads or every head's tokens lie apart.  An input's strides may be 0.
- * n_tokens: 0..2^23, n_tokens * heads below 2^30.
+ * 2^24 and 2^40; data 16-byte aligned).  Rows that are written must not share values:
+ * either every token's heads or every head's tokens lie apart.  An input's strides may
+ * be 0.  n_tokens: 0..2^23, heads up to 2^24, n_tokens * heads below 2^30.
  *
  * Packed sequences: starts i32 [n_seqs + 1] on the device, ascending from 0;
  * sequence b's new tokens are tokens starts[b]..starts[b+1]-1 and hold its last
@@ -597,11 +598,12 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
  * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
  * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
  * (a sequence with more counts its first max_new).  group 1..64.  Where group * max_new is
- * past 32: kv_heads * (n_seqs + n_tokens * group / 128) and kv_heads * (65 * n + n_tokens *
- * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
- * Preconditions (not checked): q is finite, so are scores times log2(e) in fp32.  A head's results depend on its own length, queries
- * and slots alone.  ws: at least kvc_paged_attend_workspace_bytes(c, group,
- * n_tokens, max_new), 256-byte aligned (may be NULL when that is 0). */
+ * past 32: kv_heads * (n_seqs + n_tokens * group / 128) and kv_heads * (65 * n +
+ * n_tokens * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
+ * Preconditions (not checked): q is finite, and scores times log2(e) are above -2^63 and
+ * finite in fp32.  A head's results depend on its own length, queries and slots alone.
+ * ws: at least kvc_paged_attend_workspace_bytes(c, group, n_tokens, max_new), 256-byte
+ * aligned (may be NULL when that is 0); calls that share one must not run at once. */
 int kvc_paged_attend(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int32_t max_new,
                      const int32_t* starts, float scale, const kvc_rows* q, const kvc_rows* out,
                      float* lse, void* ws, size_t ws_bytes, void* stream);
@@ -628,9 +630,13 @@ int kvc_prompt_attend(int32_t n_seqs, int32_t kv_heads, int32_t group, int32_t h
  * device, positions so far; positions of a head are distinct, 0..2^30-1.  Kept slots at
  * or past budget move, in ascending order, to the given-up slots below it, with
  * their rows, weight and pos; slots from budget on are left as they were.
- * seq_len becomes budget.  Needs weight and pos.  budget >= 1, sinks, recent >= 0.
+ * Their seq_len becomes budget; shorter sequences are left as they are.  Needs weight
+ * and pos.  budget >= 1, sinks, recent >= 0, n_seqs * kv_heads < 2^22.
  * A move from or to a slot in no page carries weight and pos only.
- * ws: at least kvc_paged_evict_workspace_bytes(c, budget), 256-byte aligned. */
+ * Precondition (not checked): a page of a sequence longer than budget belongs to one
+ * entry of the table.
+ * ws: at least kvc_paged_evict_workspace_bytes(c, budget), 256-byte aligned; calls that
+ * share one must not run at once. */
 int kvc_paged_evict(const kvc_paged_cache* c, const int32_t* seen, int32_t budget, int32_t sinks,
                     int32_t recent, void* ws, size_t ws_bytes, void* stream);
 

@@ -197,6 +197,19 @@ def test_evict_refusals():
     assert _evict(c, ws=FAKE) == -1 and _evict(_cache(seq_len=FAKE + 2 * GB)) == -1
 
 
+def test_launches_past_the_grid_refused():
+    """A workgroup counts a token's query heads in 31 bits; a launch has below 2^32 work-items."""
+    L = kvc.lib()
+    many = _cache(kv_heads=1 << 20)
+    assert _append(many, n=1, G=17) == -1 and _attend(many, n=1, G=17) == -1
+    assert L.kvc_paged_attend_workspace_bytes(_p(many), 17, 1, 0) == BAD
+    assert L.kvc_paged_attend_workspace_bytes(_p(many), 16, 1, 0) != BAD
+    wide = _cache(n_seqs=1 << 20, kv_heads=4)
+    assert _evict(wide) == -1 and L.kvc_paged_evict_workspace_bytes(_p(wide), 50) == 0
+    wide.n_seqs -= 1
+    assert L.kvc_paged_evict_workspace_bytes(_p(wide), 50) >= 4 * ((1 << 20) - 1) * 101 * 4
+
+
 def test_trim_refusals():
     t = kvc._CPageTable(n_seqs=3, table_blocks=10, block_size=16, n_blocks=100, table=FAKE, seq_len=FAKE + GB, refs=FAKE + 2 * GB)
     L = kvc.lib()
