@@ -266,10 +266,7 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(Evict E) {
   const Paged& c = E.c;
   const int n = blockIdx.x, b = n / c.H, h = n - b * c.H;
   const int moves = E.count[n], p = threadIdx.x % kPieces;
-  if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0) {
-    const int len = paged_len(c, b);
-    c.seq_len[b] = len < E.K ? len : E.K;
-  }
+  if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0 && paged_len(c, b) > E.K) c.seq_len[b] = E.K;
   for (int i = blockIdx.y * kAtOnce + threadIdx.x / kPieces; i < moves; i += gridDim.y * kAtOnce) {
     const int from = E.from[size_t(n) * E.most + i], to = E.to[size_t(n) * E.most + i];
     const int64_t rf = paged_row(c, b, h, from), rt = paged_row(c, b, h, to);

@@ -142,7 +142,6 @@ def evict(c: Cache, seen, budget, sinks, recent):
     for b in range(c.B):
         L = c.length(b)
         if L <= budget:
-            c.lens[b] = L
             continue
         for h in range(c.H):
             n = b * c.H + h
