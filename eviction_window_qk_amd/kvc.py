@@ -1016,6 +1016,17 @@ def _rows(t, shape, device, name):
 _pack_rows = struct.Struct("=Qqq").pack
 
 
+def _new_rows(like, n, heads, d):
+    """New contiguous rows beside checked ones, and their kvc_rows."""
+    t = like.new_empty((n, heads, d))
+    return t, _pack_rows(t.data_ptr(), heads * d, d)
+
+
+def _count(n, name):
+    """A dimension as a C int32 (expanded tensors may have more than memory holds)."""
+    return n if n <= 0x7fffffff else _int(n, name)
+
+
 def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
     """Rotates x (bf16 [n_tokens, heads, d], rows contiguous) by positions (int32
     [n_tokens]) into y (None: a new tensor; x itself: in place).  backward: by the
@@ -1028,12 +1039,13 @@ def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
     if x.dim() != 3:
         raise ValueError("x: 3 dimensions expected")
     n, heads, d = x.shape
-    cx = _rows(x, x.shape, dev, "x")
+    cx = _rows(x, (n, heads, d), dev, "x")
     p_ptr = _ints(positions, (n,), dev, "positions")
     if y is None:
-        y = x.new_empty((n, heads, d))
-    cy = cx if y is x else _rows(y, x.shape, dev, "y")
-    rc = lib().kvc_rope(_int(n, "n_tokens"), _int(heads, "heads"), _int(d, "head_dim"), plan._ref,
+        y, cy = _new_rows(x, n, heads, d)
+    else:
+        cy = cx if y is x else _rows(y, (n, heads, d), dev, "y")
+    rc = lib().kvc_rope(_count(n, "n_tokens"), _count(heads, "heads"), _count(d, "head_dim"), plan._ref,
                         1 if backward else 0, p_ptr, cx, cy, s)
     _check(rc, "kvc_rope")
     return y
@@ -1136,11 +1148,12 @@ def paged_append(cache: PagedCache, k, v, starts, positions=None, rope: Rope = N
         q_shp = (n, q.shape[1], cache.head_dim)
         cq = _rows(q, q_shp, dev, "q")
         if q_out is None:
-            q_out = q.new_empty(q_shp)
-        co = cq if q_out is q else _rows(q_out, q_shp, dev, "q_out")
+            q_out, co = _new_rows(q, *q_shp)
+        else:
+            co = cq if q_out is q else _rows(q_out, q_shp, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out: without q")
-    rc = lib().kvc_paged_append(cache._ref, _int(n, "n_tokens"), st_ptr, p_ptr,
+    rc = lib().kvc_paged_append(cache._ref, _count(n, "n_tokens"), st_ptr, p_ptr,
                                 None if rope is None else rope._ref, G, cq, co,
                                 ck, cv, s)
     _check(rc, "kvc_paged_append")
@@ -1171,8 +1184,9 @@ def paged_attend(cache: PagedCache, q, starts, max_new: int = 0, out=None, lse=N
     st_ptr = _ints(starts, cache._starts_shape, dev, "starts")
     ws = _scratch(ws, cache.attend_workspace_bytes(G, shp[0], max_new), dev)
     if out is None:
-        out = q.new_empty(shp)
-    co = _rows(out, shp, dev, "out")
+        out, co = _new_rows(q, *shp)
+    else:
+        co = _rows(out, shp, dev, "out")
     lse, lse_ptr = (_new(q, shp[:2], torch.float32) if lse is None and want_lse else
                     _given(lse, _F32, shp[:2], dev, "lse"))
     rc = lib().kvc_paged_attend(cache._ref, G, shp[0], _int(max_new, "max_new"), st_ptr, _scale(scale),
@@ -1198,15 +1212,16 @@ def prompt_attend(q, k, v, starts, out=None, lse=None, want_lse: bool = False, s
     G = _group(q, k.shape[1], "q")
     n, heads, d = q.shape
     kv = (n, k.shape[1], d)
-    cq, ck, cv = _rows(q, q.shape, dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
+    cq, ck, cv = _rows(q, (n, heads, d), dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
     st_ptr = _ints(starts, starts.shape, dev, "starts")
     if out is None:
-        out = q.new_empty((n, heads, d))
-    co = _rows(out, q.shape, dev, "out")
+        out, co = _new_rows(q, n, heads, d)
+    else:
+        co = _rows(out, (n, heads, d), dev, "out")
     lse, lse_ptr = (_new(q, (n, heads), torch.float32) if lse is None and want_lse else
                     _given(lse, _F32, (n, heads), dev, "lse"))
-    rc = lib().kvc_prompt_attend(_int(starts.shape[0] - 1, "n_seqs"), _int(kv[1], "kv_heads"), G,
-                                 _int(d, "head_dim"), _int(n, "n_tokens"), st_ptr, _scale(scale),
+    rc = lib().kvc_prompt_attend(_count(starts.shape[0] - 1, "n_seqs"), _count(kv[1], "kv_heads"), G,
+                                 _count(d, "head_dim"), _count(n, "n_tokens"), st_ptr, _scale(scale),
                                  cq, ck, cv, co, lse_ptr, s)
     _check(rc, "kvc_prompt_attend")
     return out if lse is None else (out, lse)
