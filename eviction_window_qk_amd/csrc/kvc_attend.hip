@@ -20,11 +20,11 @@
 // only when a lane's sum passes 2^32 (the first tile always does).
 //
 // The keys of a head are cut into pieces by its own length (few_chunk); the four
-// waves of a workgroup take the 32-key tiles of a piece in turn, and their sums meet
-// in LDS.  A second kernel joins the pieces where there are several, and adds up what each
-// slot receives where that is asked for.  Where a piece's
-// keys are is looked up once, into LDS, four keys at a time where the page size is a
-// multiple of four.
+// waves of a piece take its 32-key tiles in turn, and their sums meet in LDS.  A
+// workgroup takes one piece, and a second kernel joins the pieces and adds up what each
+// slot receives, or it takes a head's few pieces and does both itself (whole_heads).  Where a
+// piece's keys are is looked up once, into LDS, four keys at a time where the page size
+// is a multiple of four.
 #include "kvc_paged.h"
 
 namespace kvc {
@@ -38,6 +38,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 constexpr uint32_t kNone = 0xffffffffu;  // no row: past the end or in no page
 constexpr float kFar = 0x1p64f;          // -m of a row that has seen nothing
+constexpr int kWholePieces = 3;          // pieces of a head that one workgroup may take
 
 struct Args {
   AttendCall a;
@@ -74,33 +75,91 @@ __device__ __forceinline__ void finish(const Args& A, int token, int head, int d
     A.a.lse[size_t(token) * (A.a.G * A.a.c.H) + head] = b * 0.6931471805599453f;
 }
 
-template <int D, int MT, int GROUP, bool STREAM>
-__global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
+// What four slots of a head from t on receive from its R rows: the sum down the rows of
+// 2^(x - log2 of the row's sum), less: minus these logarithms.  The scores were kept (4
+// bytes a row and slot; the keys would be 2 * d bytes a slot again).
+__device__ __forceinline__ void weigh_four(const Args& A, int n, int t, int len, int R, const float* less,
+                                           const float* was, float* to) {
+  const float* x = A.scores + size_t(n) * A.rows * A.score_stride + t;
+  f32x4 sum = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int r = 0; r < R; ++r) {
+    const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + less[r]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (t + i < len && sum[i] > 0.0f) to[i] = was[i] + sum[i];
+}
+
+// Joins the pieces of a row that lie in LDS, `step` apart: four values from `dim` on, and
+// log2 of the row's sum.  The sums are those that join_rows takes, in its order.
+template <int D>
+__device__ __forceinline__ float join_here(const float* at, int step, int pieces, int dim, f32x4& out) {
+#pragma clang fp contract(off)
+  constexpr int kAtOnce = 256 / D;
+  float st[kWholePieces], M = -INFINITY;
+#pragma unroll
+  for (int p = 0; p < kWholePieces; ++p) {
+    st[p] = p < pieces ? at[p * step + D + 2] : -INFINITY;
+    M = fmaxf(M, st[p]);
+  }
+  const float base = M == -INFINITY ? 0.0f : M;
+  float e[kWholePieces];
+#pragma unroll
+  for (int p = 0; p < kWholePieces; ++p) e[p] = fast_exp2(st[p] - base);
+  static_assert(kWholePieces == 3, "the sum of eight lanes");
+  const float L = (e[0] + e[2]) + e[1], by_L = L > 0.0f ? 1.0f / L : 0.0f;
+  f32x4 sum[kAtOnce] = {};
+#pragma unroll
+  for (int p = 0; p < kWholePieces; ++p) {
+    if (p >= pieces) break;
+    const f32x4 x = *reinterpret_cast<const f32x4*>(at + p * step + dim);
+    const float f = e[p] * by_L;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum[p % kAtOnce][i] = __builtin_fmaf(x[i], f, sum[p % kAtOnce][i]);
+  }
+  out = sum[0] + sum[1];
+  if constexpr (kAtOnce == 4) out = out + (sum[2] + sum[3]);
+  return L > 0.0f ? base + fast_log2(L) : -INFINITY;
+}
+
+// WHOLE: a workgroup takes all pieces of a head, four waves each, and joins them itself.
+template <int D, int MT, int GROUP, bool STREAM, bool WHOLE>
+__global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ? 1 : 2) void k_attend_few(Args A) {
+  static_assert(!WHOLE || MT == 1, "one row block");
   constexpr int kSteps = D / 32;        // matrix steps over the head dimension
   constexpr int kTiles = D / 16;        // 16-value tiles of the output
   constexpr int kVWords = D / 32;       // words of one key's values in a lane
   constexpr int kRowF = D + 4;          // floats of one merged row: sums, m, l
   constexpr int kPerTile = 32 / GROUP;  // look-ups of a tile
   extern __shared__ __align__(16) unsigned char lds_raw[];
-  uint32_t* const where = reinterpret_cast<uint32_t*>(lds_raw);  // rows of the look-ups, then the waves' sums
   float* const lds = reinterpret_cast<float*>(lds_raw);
-  __shared__ uint32_t none_of[kFewMaxChunk / 32];  // which look-ups of a tile found no page
+  __shared__ uint32_t none_all[kFewMaxChunk / 32];  // which look-ups of a tile found no page
+  static_assert(kWholePieces * kFewChunk <= kFewMaxChunk, "the pieces' tiles side by side");
 
   const Paged& c = A.a.c;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = WHOLE ? threadIdx.x % kThreads : threadIdx.x, lane = tid & 63, wave = tid >> 6;  // of the piece
   const int col = lane & 15, g = lane >> 4;
   // Pieces of one head together, each head's rotated by one: workgroups go to the XCDs
   // in turn, and where only the first pieces of a long table have keys they would all
   // be one XCD's.  The row blocks of a piece follow each other on one XCD, whose L2 then
   // reads its keys once.
-  const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
-  const int rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
-  const uint32_t unit = eight * 8 + (blockIdx.x & 7);
-  if (unit >= uint32_t(A.units)) return;
-  const int nth = int(quot(A.by_pieces, unit));
-  int piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
-  piece -= piece >= A.pieces ? A.pieces : 0;
-  const int n = A.n0 + nth;
+  int n, piece, rb = 0;
+  if constexpr (WHOLE) {
+    n = A.n0 + int(blockIdx.x);
+    piece = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  } else {
+    const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
+    rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
+    const uint32_t unit = eight * 8 + (blockIdx.x & 7);
+    if (unit >= uint32_t(A.units)) return;
+    const int nth = int(quot(A.by_pieces, unit));
+    piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
+    piece -= piece >= A.pieces ? A.pieces : 0;
+    n = A.n0 + nth;
+  }
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
 
   const int2 mine = chunk_of(A.a.k, b);
@@ -109,9 +168,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
   const int len = paged_len(c, b);
   const int chunk = few_chunk(len);
   const int t0 = piece * chunk;
-  if (t0 >= len && piece > 0) return;
-  const int keys = len - t0 < chunk ? len - t0 : chunk;  // of this piece, 0 for an empty sequence
+  if (!WHOLE && t0 >= len && piece > 0) return;
+  const int left = len > t0 ? len - t0 : 0, keys = left < chunk ? left : chunk;  // of this piece
   const bool alone = len <= chunk;
+  // Rows of the look-ups, then the waves' sums.
+  uint32_t* const where = reinterpret_cast<uint32_t*>(lds_raw) + (WHOLE ? piece * (kFewChunk / GROUP) : 0);
+  uint32_t* const none_of = none_all + (WHOLE ? piece * (kFewChunk / 32) : 0);
 
   // Queries, on their way while the keys are looked up.
   u32x4 qf[MT][kSteps];
@@ -280,27 +342,31 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
     l[mt] += __shfl_xor(l[mt], 16);
     l[mt] += __shfl_xor(l[mt], 32);
     const int r0 = row0 + mt * 16, rows_here = R - r0 < 16 ? R - r0 : 16;
-    float* to = lds + (wave * 16 + col) * kRowF;
+    const int kept = WHOLE ? A.rows : 16;                 // rows that a wave leaves
+    float* const of_piece = lds + (WHOLE ? piece * kWaves * kept * kRowF : 0);
+    float* to = of_piece + (wave * kept + col) * kRowF;
+    if (col < rows_here) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r)  // values of row 4g + r of tile i: dim (4g + r) * kTiles + i
+      for (int r = 0; r < 4; ++r)  // values of row 4g + r of tile i: dim (4g + r) * kTiles + i
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
-    if (g == 0) {
-      to[D] = -nm[mt];
-      to[D + 1] = l[mt];
+        for (int i = 0; i < kTiles; ++i) to[(4 * g + r) * kTiles + i] = acc[mt][i][r];
+      if (g == 0) {
+        to[D] = -nm[mt];
+        to[D + 1] = l[mt];
+      }
     }
     __syncthreads();
     for (int e = tid; e < rows_here * (D / 4); e += kThreads) {
       const int r = e / (D / 4), dim = e % (D / 4) * 4;
-      const float* at = lds + r * kRowF;
+      float* at = of_piece + r * kRowF;
       float M = -kFar;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * 16 * kRowF + D]);
+      for (int w = 0; w < kWaves; ++w) M = fmaxf(M, at[w * kept * kRowF + D]);
       f32x4 sum = {0, 0, 0, 0};
       float L = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
-        const float* aw = at + w * 16 * kRowF;
+        const float* aw = at + w * kept * kRowF;
         const float f = fast_exp2(aw[D] - M);
         sum += *reinterpret_cast<const f32x4*>(aw + dim) * f;
         L = __builtin_fmaf(aw[D + 1], f, L);
@@ -308,6 +374,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
       const bool any = L > 0.0f;
       sum = any ? sum * (1.0f / L) : f32x4{0, 0, 0, 0};
       const float bsum = any ? M + fast_log2(L) : -INFINITY;
+      if constexpr (WHOLE) {       // over the first wave's, which nobody else reads any more
+        *reinterpret_cast<f32x4*>(at + dim) = sum;
+        if (dim == 0) at[D + 2] = bsum;
+        continue;
+      }
       if (A.scores && dim == 0) A.stat[(size_t(n) * A.rows + r0 + r) * A.pieces + piece] = bsum;
       if (alone) {
         const int i = int(quot(A.by_G, uint32_t(r0 + r)));
@@ -317,6 +388,28 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_few(Args A) {
         *reinterpret_cast<f32x4*>(A.part + at_piece * D + dim) = sum;
         if (dim == 0) A.stat[at_piece] = bsum;
       }
+    }
+  }
+  if constexpr (WHOLE) {
+    __shared__ float less[16];
+    __syncthreads();
+    const int threads = A.pieces * kThreads, step = kWaves * A.rows * kRowF;
+    for (int e = threadIdx.x; e < R * (D / 4); e += threads) {
+      const int r = e / (D / 4), dim = e % (D / 4) * 4;
+      f32x4 out;
+      const float bsum = join_here<D>(lds + r * kRowF, step, A.pieces, dim, out);
+      const int i = int(quot(A.by_G, uint32_t(r)));
+      finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, out, bsum);
+      if (dim == 0) less[r] = -bsum == INFINITY ? -INFINITY : -bsum;
+    }
+    if (!A.scores) return;
+    __syncthreads();
+    for (int t = int(threadIdx.x) * 4; t < len; t += threads * 4) {
+      float* to = c.weight + size_t(n) * c.room + t;
+      float was[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) was[i] = t + i < len ? to[i] : 0.0f;
+      weigh_four(A, n, t, len, R, less, was, to);
     }
   }
 }
@@ -385,9 +478,7 @@ __device__ __forceinline__ void join_rows(const Args& A, int n, int block, float
   finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, sum, L > 0.0f ? base + fast_log2(L) : -INFINITY);
 }
 
-// What 1024 slots receive from a sequence's few rows: the sum down the rows of 2^(x -
-// log2 of the row's sum), four slots a thread.  The scores come from the first kernel (4
-// bytes a row and slot; the keys would be 2 * d bytes a slot again).
+// What 1024 slots receive from a sequence's few rows, four slots a thread.
 __device__ __forceinline__ void weigh_slots(const Args& A, int n, int block, float* less) {
   const Paged& c = A.a.c;
   const int b = int(quot(A.by_H, uint32_t(n)));
@@ -405,17 +496,7 @@ __device__ __forceinline__ void weigh_slots(const Args& A, int n, int block, flo
   for (int i = 0; i < 4; ++i) was[i] = t + i < len ? to[i] : 0.0f;
   __syncthreads();
   if (t >= len) return;
-  const float* x = A.scores + size_t(n) * A.rows * A.score_stride + t;
-  f32x4 sum = {0, 0, 0, 0};
-#pragma unroll 8
-  for (int r = 0; r < R; ++r) {
-    const f32x4 y = *reinterpret_cast<const f32x4*>(x + size_t(r) * A.score_stride);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] += fast_exp2(y[i] + less[r]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (t + i < len && sum[i] > 0.0f) to[i] = was[i] + sum[i];
+  weigh_four(A, n, t, len, R, less, was, to);
 }
 
 // Both in one launch, as neither needs the other: of a head's workgroups `joins` join rows
@@ -443,7 +524,7 @@ void attend_few(Args A, hipStream_t s) {
   for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
     const int nh = heads - A.n0 < most ? heads - A.n0 : most;
     A.units = nh * A.pieces;
-    k_attend_few<D, MT, GROUP, STREAM><<<unsigned((A.units + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
+    k_attend_few<D, MT, GROUP, STREAM, false><<<unsigned((A.units + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
                                          keys > sums ? keys : sums, s>>>(A);
   }
   const bool small = A.pieces <= kFewPieces;
@@ -459,6 +540,34 @@ void attend_few(Args A, hipStream_t s) {
   }
 }
 
+template <int D, int GROUP, bool STREAM>
+void attend_whole(Args A, hipStream_t s) {
+  const int heads = A.a.c.B * A.a.c.H;
+  const size_t keys = size_t(A.pieces) * kFewChunk / GROUP * 4;
+  const size_t sums = size_t(A.pieces) * kWaves * A.rows * (D + 4) * sizeof(float);
+  constexpr int kMost = 1 << 22;   // heads of a launch: below 2^32 work-items
+  for (A.n0 = 0; A.n0 < heads; A.n0 += kMost) {
+    const int nh = heads - A.n0 < kMost ? heads - A.n0 : kMost;
+    k_attend_few<D, 1, GROUP, STREAM, true>
+        <<<unsigned(nh), unsigned(A.pieces) * kThreads, keys > sums ? keys : sums, s>>>(A);
+  }
+}
+
+// Whether a workgroup takes all pieces of a head, or one (the results are the same
+// bits).  It saves the second launch and the pieces' way through memory, but one that
+// takes several fills a CU: 100 heads or fewer leave CUs without work, and so does a last
+// round of them.  Heads of 1100 slots, 7 rows, us (one launch : two): 64 heads 16.9 : 13.3,
+// 96 heads 17.3 : 18.9, 256 heads 27.4 : 30.8 (with weights 33.1 : 39.6), 288 heads 46.4 :
+// 36.3, 512 heads 53.5 : 56.1, 2048 heads 207 : 228 (with weights the same); 400 slots with
+// weights, 256 heads 16.5 : 19.0.
+bool whole_heads(int heads, int pieces, int rows, bool weights) {
+  if (rows > 16 || pieces > kWholePieces) return false;
+  if (pieces == 1) return weights;
+  constexpr int kCUs = 256;
+  const int64_t rounds = (int64_t(heads) + kCUs - 1) / kCUs;
+  return heads >= 96 && (rounds == 1 || heads * int64_t(8) >= rounds * kCUs * 7);
+}
+
 template <int D>
 void attend_rows(const Args& A, hipStream_t s) {
   const bool fours = A.a.c.bs % 4 == 0;
@@ -468,7 +577,11 @@ void attend_rows(const Args& A, hipStream_t s) {
   // sequences of 1100 that the cache does not hold yet (145 MB; found there again by the next
   // call, 39 against 34).  Two row blocks: no gain.
   const bool stream = uint64_t(A.a.c.n_blocks) * A.a.c.H * A.a.c.bs * D * 4 > (uint64_t(96) << 20);
-  if (A.rows <= 16) {
+  if (whole_heads(A.a.c.B * A.a.c.H, A.pieces, A.rows, A.scores != nullptr)) {
+    if (fours && stream) attend_whole<D, 4, true>(A, s);
+    else if (fours) attend_whole<D, 4, false>(A, s);
+    else attend_whole<D, 1, false>(A, s);
+  } else if (A.rows <= 16) {
     if (fours && stream) attend_few<D, 1, 4, true>(A, s);
     else if (fours) attend_few<D, 1, 4, false>(A, s);
     else attend_few<D, 1, 1, false>(A, s);

@@ -303,6 +303,57 @@ def test_a_head_does_not_depend_on_its_call(d):
         assert torch.equal(o.view(torch.int16), po[rows].view(torch.int16)) and torch.equal(z, pl[rows])
 
 
+# (B, H, G, d, bs, longest, most new, holes, spare pages)
+HEADS = [
+    (14, 8, 3, 128, 16, 1536, 5, 0.0, 3),
+    (14, 8, 3, 64, 24, 1500, 4, 0.2, 3),
+    (32, 4, 7, 128, 5, 1030, 2, 0.2, 3),
+    (33, 3, 1, 64, 7, 1100, 16, 0.0, 3),
+    (58, 8, 2, 64, 16, 600, 3, 0.0, 3),                # more heads than CUs
+    (26, 4, 16, 128, 64, 1300, 1, 0.1, 700),           # pools past the size that is read past the caches
+    (26, 4, 16, 64, 64, 900, 1, 0.0, 1600),
+    (3, 2, 5, 128, 16, 500, 3, 0.1, 3),                # one piece a head
+    (5, 2, 4, 64, 7, 490, 4, 0.0, 3),
+]
+
+
+@pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("case", HEADS, ids=[str(i) for i in range(len(HEADS))])
+def test_many_heads_of_few_pieces(case, weights):
+    """Enough heads that a workgroup takes one whole: the oracle's results, and the bits that
+    each sequence gets alone."""
+    B, H, G, d, bs, longest, most, holes, spare = case
+    print(f"[case] heads {case} {weights}", flush=True)
+    rng = u.rng_of(80, *case[:6])
+    lens = rng.integers(1, longest + 1, B)
+    lens[:6] = [longest, 0, 1, min(512, longest), min(513, longest), longest - 1][: B]
+    new = rng.integers(0, most + 1, B)
+    new[:3] = [most, most, most]                       # the empty sequence has tokens too
+    c = u.random_cache(81, B, H, d, bs, lens, holes=holes, spare=spare, weights=weights)
+    starts = u.starts_of(new)
+    n = int(starts[-1]) + 2
+    q = dev_bf16(random_rows(82, n, G * H, d))
+    g = u.to_gpu(c)
+    out = torch.full((n, G * H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = kvc.paged_attend(g, q, u.dev(starts), max_new=most, out=out, want_lse=True)
+    torch.cuda.synchronize()
+    ref = og.attend(c, og.widen(u.bits(q)), starts)
+    u.check_attention(ref, u.bits(out), lse, longest, untouched=0x40E0)
+    if weights:
+        u.check_weights(ref, c.weight, g.weight.cpu().numpy(), d, G * most)
+    for b in range(B):
+        if not new[b]:
+            continue
+        rows, heads = slice(int(starts[b]), int(starts[b + 1])), slice(b * H, (b + 1) * H)
+        one = kvc.PagedCache(g.k_pool, g.v_pool, g.table[b: b + 1], g.seq_len[b: b + 1],
+                             weight=u.dev(c.weight[heads]) if weights else None,
+                             pos=u.dev(c.pos[heads]) if weights else None)
+        o, z = kvc.paged_attend(one, q[rows], u.dev(u.starts_of([new[b]])), want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[rows].view(torch.int16)) and torch.equal(z, lse[rows])
+        if weights:
+            assert torch.equal(one.weight, g.weight[heads])
+
+
 def test_max_len_bounds_the_lengths():
     c = u.random_cache(73, 2, 1, 64, 16, [300, 90], weights=True, max_len=200)
     c.lens[0] = 300
