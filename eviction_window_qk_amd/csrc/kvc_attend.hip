@@ -43,8 +43,7 @@ constexpr int kWholePieces = 3;          // pieces of a head that one workgroup 
 struct Args {
   AttendCall a;
   int pieces, rows;  // of the longest length and the longest chunk: the grid's and the partials'
-  int blocks;        // row blocks
-  FastDiv by_G, by_pieces, by_H, by_blocks;
+  FastDiv by_G, by_pieces, by_H;
   int units;         // (head, piece) pairs of this launch
   int n0;            // its first head
   float* part;       // [n][row][piece][D] outputs of a piece
@@ -91,6 +90,19 @@ __device__ __forceinline__ void weigh_four(const Args& A, int n, int t, int len,
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     if (t + i < len && sum[i] > 0.0f) to[i] = was[i] + sum[i];
+}
+
+// The head and piece of a workgroup.  Pieces of one head follow each other, each head's
+// rotated by one: workgroups go to the XCDs in turn, and where only the first pieces of a
+// long table have keys they would all be one XCD's.
+__device__ __forceinline__ bool piece_of(const Args& A, int& n, int& piece) {
+  const uint32_t unit = blockIdx.x;
+  if (unit >= uint32_t(A.units)) return false;
+  const int nth = int(quot(A.by_pieces, unit));
+  piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
+  piece -= piece >= A.pieces ? A.pieces : 0;
+  n = A.n0 + nth;
+  return true;
 }
 
 // Joins the pieces of a row that lie in LDS, `step` apart: four values from `dim` on, and
@@ -142,29 +154,18 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
   const Paged& c = A.a.c;
   const int tid = WHOLE ? threadIdx.x % kThreads : threadIdx.x, lane = tid & 63, wave = tid >> 6;  // of the piece
   const int col = lane & 15, g = lane >> 4;
-  // Pieces of one head together, each head's rotated by one: workgroups go to the XCDs
-  // in turn, and where only the first pieces of a long table have keys they would all
-  // be one XCD's.  The row blocks of a piece follow each other on one XCD, whose L2 then
-  // reads its keys once.
-  int n, piece, rb = 0;
+  int n, piece;
   if constexpr (WHOLE) {
     n = A.n0 + int(blockIdx.x);
     piece = __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
-  } else {
-    const uint32_t eight = quot(A.by_blocks, blockIdx.x >> 3);
-    rb = int((blockIdx.x >> 3) - eight * A.by_blocks.d);
-    const uint32_t unit = eight * 8 + (blockIdx.x & 7);
-    if (unit >= uint32_t(A.units)) return;
-    const int nth = int(quot(A.by_pieces, unit));
-    piece = int(unit) - nth * A.pieces + (nth - int(quot(A.by_pieces, uint32_t(nth))) * A.pieces);
-    piece -= piece >= A.pieces ? A.pieces : 0;
-    n = A.n0 + nth;
+  } else if (!piece_of(A, n, piece)) {
+    return;
   }
   const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
 
   const int2 mine = chunk_of(A.a.k, b);
-  const int R = mine.y * A.a.G, row0 = rb * MT * 16;
-  if (row0 >= R || R > kFewRows) return;
+  const int R = mine.y * A.a.G;
+  if (R == 0 || R > kFewRows) return;
   const int len = paged_len(c, b);
   const int chunk = few_chunk(len);
   const int t0 = piece * chunk;
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
   int last[MT];  // last key of this piece that the row attends to
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int r = row0 + mt * 16 + col;
+    const int r = mt * 16 + col;
     const int i = int(quot(A.by_G, uint32_t(r)));
     last[mt] = r < R ? len - mine.y + i - t0 : -1;
 #pragma unroll
@@ -274,10 +275,12 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
           if (tile + at >= keys || gone) x.v[j][u] = 0;
       }
     }
-    if (A.scores) {  // for the sums of the weights, once the rows' sums are known
+    // For the sums of the weights, once the rows' sums are known.  These stores cost more
+    // than their bytes: 4 rows of 131072 slots of 8 heads 24 us for 16.8 MB beside the 537 read.
+    if (A.scores) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int r = row0 + mt * 16 + col;
+        const int r = mt * 16 + col;
         if (r < R) {
           float* to = A.scores + (size_t(n) * A.rows + r) * A.score_stride + t0 + tile + 4 * g;
 #pragma unroll
@@ -341,7 +344,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
     __syncthreads();
     l[mt] += __shfl_xor(l[mt], 16);
     l[mt] += __shfl_xor(l[mt], 32);
-    const int r0 = row0 + mt * 16, rows_here = R - r0 < 16 ? R - r0 : 16;
+    const int r0 = mt * 16, rows_here = R - r0 < 16 ? R - r0 : 16;
     const int kept = WHOLE ? A.rows : 16;                 // rows that a wave leaves
     float* const of_piece = lds + (WHOLE ? piece * kWaves * kept * kRowF : 0);
     float* to = of_piece + (wave * kept + col) * kRowF;
@@ -478,65 +481,64 @@ __device__ __forceinline__ void join_rows(const Args& A, int n, int block, float
   finish(A, mine.x + i, h * A.a.G + r - i * A.a.G, dim, sum, L > 0.0f ? base + fast_log2(L) : -INFINITY);
 }
 
-// What 1024 slots receive from a sequence's few rows, four slots a thread.
-__device__ __forceinline__ void weigh_slots(const Args& A, int n, int block, float* less) {
+// What the slots of a piece receive from a sequence's few rows, four slots a thread.
+__device__ __forceinline__ void weigh_piece(const Args& A, float* less) {
+  int n, piece;
+  if (!piece_of(A, n, piece)) return;
   const Paged& c = A.a.c;
   const int b = int(quot(A.by_H, uint32_t(n)));
   const int R = chunk_of(A.a.k, b).y * A.a.G, len = paged_len(c, b);
-  if (R > kFewRows || block * kThreads * 4 >= len) return;
+  const int chunk = few_chunk(len), t0 = piece * chunk, end = len - t0 < chunk ? len : t0 + chunk;
+  if (R > kFewRows || t0 >= len) return;
   static_assert(kThreads == 8 * kFewRows, "eight lanes a row");
-  const int chunk = few_chunk(len), pieces = (len + chunk - 1) / chunk, row = threadIdx.x >> 3;
+  const int pieces = (len + chunk - 1) / chunk, row = threadIdx.x >> 3;
   float base;
   const float L = whole_sum<8>(A.stat + (size_t(n) * A.rows + row) * A.pieces, row < R ? pieces : 0, base);
   if (threadIdx.x % 8 == 0) less[row] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
-  const int t = (block * kThreads + int(threadIdx.x)) * 4;
-  float* to = c.weight + size_t(n) * c.room + t;
-  float was[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) was[i] = t + i < len ? to[i] : 0.0f;
   __syncthreads();
-  if (t >= len) return;
-  weigh_four(A, n, t, len, R, less, was, to);
+  for (int t = t0 + int(threadIdx.x) * 4; t < end; t += kThreads * 4) {
+    float* to = c.weight + size_t(n) * c.room + t;
+    float was[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) was[i] = t + i < end ? to[i] : 0.0f;
+    weigh_four(A, n, t, end, R, less, was, to);
+  }
 }
 
-// Both in one launch, as neither needs the other: of a head's workgroups `joins` join rows
-// (none where no head has several pieces), the others weigh its slots.
+// Both in one launch, as neither needs the other.  The workgroups that weigh are numbered
+// as those that kept the scores, so that both lie on the same XCD, whose L2 may have them
+// (80 sequences of 1100 slots, 4 heads each, 49.3 -> 46.5 us).
 template <int D, bool SMALL>
-__global__ __launch_bounds__(kThreads) void k_join_few(Args A, int joins, FastDiv by_per, int n0) {
+__global__ __launch_bounds__(kThreads) void k_join_few(Args A, int joins, FastDiv by_joins) {
   __shared__ __align__(16) float lds[kThreads * 4];
-  const uint32_t unit = blockIdx.x, nth = quot(by_per, unit);
-  const int n = n0 + int(nth), i = int(unit - nth * by_per.d);
-  if (i < joins) join_rows<D, SMALL>(A, n, i, lds);
-  else weigh_slots(A, n, i - joins, lds);
+  const int weighs = A.scores ? (A.units + 7) & ~7 : 0;
+  if (int(blockIdx.x) < weighs) {
+    weigh_piece(A, lds);
+  } else {
+    const uint32_t unit = blockIdx.x - weighs, nth = quot(by_joins, unit);
+    join_rows<D, SMALL>(A, A.n0 + int(nth), int(unit - nth * by_joins.d), lds);
+  }
 }
 
 template <int D, int MT, int GROUP, bool STREAM>
 void attend_few(Args A, hipStream_t s) {
-  // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits), in
-  // whole eights of units.
   const int heads = A.a.c.B * A.a.c.H;
-  A.blocks = (A.rows + MT * 16 - 1) / (MT * 16);
-  const int room = ((1 << 23) / A.blocks) & ~7;
-  const int most = room / A.pieces;    // a head has 2^19 pieces at most
-  A.by_blocks = fast_div(uint32_t(A.blocks));
+  const bool small = A.pieces <= kFewPieces;
+  const int joins = A.pieces == 1 ? 0 : (small ? (A.rows + kWaves - 1) / kWaves : A.rows);
+  const FastDiv by_joins = fast_div(uint32_t(joins > 0 ? joins : 1));
+  // At most 2^23 workgroups a launch (the grid counts work-items in 32 bits); a head has
+  // 2^19 pieces and 32 joins at most.
+  const int most = ((1 << 23) - 8) / (A.pieces + joins);
   const size_t keys = size_t(A.a.c.cap < kFewMaxChunk ? ((A.a.c.cap < kFewChunk ? kFewChunk : A.a.c.cap) + 127) & ~127 : kFewMaxChunk) / GROUP * 4;
   const size_t sums = size_t(kWaves) * 16 * (D + 4) * sizeof(float);
   for (A.n0 = 0; A.n0 < heads; A.n0 += most) {
     const int nh = heads - A.n0 < most ? heads - A.n0 : most;
     A.units = nh * A.pieces;
-    k_attend_few<D, MT, GROUP, STREAM, false><<<unsigned((A.units + 7) / 8) * 8u * unsigned(A.blocks), kThreads,
-                                         keys > sums ? keys : sums, s>>>(A);
-  }
-  const bool small = A.pieces <= kFewPieces;
-  const int joins = A.pieces == 1 ? 0 : (small ? (A.rows + kWaves - 1) / kWaves : A.rows);
-  const int per = joins + (A.scores ? (A.a.c.cap + kThreads * 4 - 1) / (kThreads * 4) : 0);
-  if (per == 0) return;
-  const int most_joined = (1 << 23) / per;   // per: 2^20 + 32 at most
-  for (int n0 = 0; n0 < heads; n0 += most_joined) {
-    const int nh = heads - n0 < most_joined ? heads - n0 : most_joined;
-    const unsigned grid = unsigned(nh) * unsigned(per);
-    if (small) k_join_few<D, true><<<grid, kThreads, 0, s>>>(A, joins, fast_div(uint32_t(per)), n0);
-    else k_join_few<D, false><<<grid, kThreads, 0, s>>>(A, joins, fast_div(uint32_t(per)), n0);
+    k_attend_few<D, MT, GROUP, STREAM, false><<<unsigned(A.units), kThreads, keys > sums ? keys : sums, s>>>(A);
+    const unsigned grid = unsigned(A.scores ? (A.units + 7) & ~7 : 0) + unsigned(nh) * unsigned(joins);
+    if (grid == 0) continue;
+    if (small) k_join_few<D, true><<<grid, kThreads, 0, s>>>(A, joins, by_joins);
+    else k_join_few<D, false><<<grid, kThreads, 0, s>>>(A, joins, by_joins);
   }
 }
 
@@ -571,12 +573,13 @@ bool whole_heads(int heads, int pieces, int rows, bool weights) {
 template <int D>
 void attend_rows(const Args& A, hipStream_t s) {
   const bool fours = A.a.c.bs % 4 == 0;
-  // Keys and values that one row block reads, out of pools that are a good part of the
-  // last-level cache (256 MB), are read past the caches, which they would only empty: 89
+  // Keys and values out of pools that are a good part of the last-level cache (256 MB),
+  // or past it, are read past the caches, which they would only empty.  At most 16 rows: 89
   // us against 101 on one sequence of 131072 slots (537 MB), 40.3 against 42.6 on 64
-  // sequences of 1100 that the cache does not hold yet (145 MB; found there again by the next
-  // call, 39 against 34).  Two row blocks: no gain.
-  const bool stream = uint64_t(A.a.c.n_blocks) * A.a.c.H * A.a.c.bs * D * 4 > (uint64_t(96) << 20);
+  // sequences of 1100 that the cache does not hold yet (145 MB; found there again by the
+  // next call, 39 against 34).  17 to 32 rows: 95 against 107, 41 against 37.
+  const uint64_t pools = uint64_t(A.a.c.n_blocks) * A.a.c.H * A.a.c.bs * D * 4;
+  const bool stream = pools > (uint64_t(A.rows <= 16 ? 96 : 256) << 20);
   if (whole_heads(A.a.c.B * A.a.c.H, A.pieces, A.rows, A.scores != nullptr)) {
     if (fours && stream) attend_whole<D, 4, true>(A, s);
     else if (fours) attend_whole<D, 4, false>(A, s);
@@ -586,7 +589,10 @@ void attend_rows(const Args& A, hipStream_t s) {
     else if (fours) attend_few<D, 1, 4, false>(A, s);
     else attend_few<D, 1, 1, false>(A, s);
   } else {
-    if (fours) attend_few<D, 2, 4, false>(A, s);
+    // One row block of 32, not two of 16 that read each key twice: 99.6 us against 107 (13
+    // sequences of 8192 slots, d 128), 36.8 against 35.6 (64 of 1100).
+    if (fours && stream) attend_few<D, 2, 4, true>(A, s);
+    else if (fours) attend_few<D, 2, 4, false>(A, s);
     else attend_few<D, 2, 1, false>(A, s);
   }
 }
