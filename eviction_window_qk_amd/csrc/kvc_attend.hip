@@ -573,11 +573,13 @@ bool whole_heads(int heads, int pieces, int rows, bool weights) {
 template <int D>
 void attend_rows(const Args& A, hipStream_t s) {
   const bool fours = A.a.c.bs % 4 == 0;
-  // Keys and values out of pools that are a good part of the last-level cache (256 MB),
-  // or past it, are read past the caches, which they would only empty.  At most 16 rows: 89
-  // us against 101 on one sequence of 131072 slots (537 MB), 40.3 against 42.6 on 64
-  // sequences of 1100 that the cache does not hold yet (145 MB; found there again by the
-  // next call, 39 against 34).  17 to 32 rows: 95 against 107, 41 against 37.
+  // Keys and values out of pools that are a good part of the last-level cache (256 MB)
+  // are read past the caches, which they would only empty: 89 us against 101 on one
+  // sequence of 131072 slots (537 MB), 40.3 against 42.6 on 64 sequences of 1100 that the
+  // cache does not hold yet (145 MB; found there again by the next call, 39 against 34).
+  // 17 to 32 rows of 128 values: out of pools past it, 95 against 107 (537 MB), 134 against
+  // 147 with weights and 103 against 100 without (436 MB); 41 against 37 (145 MB).  Of 64
+  // values never: 57 against 48 (218 MB), 285 against 282 (805 MB).
   const uint64_t pools = uint64_t(A.a.c.n_blocks) * A.a.c.H * A.a.c.bs * D * 4;
   const bool stream = pools > (uint64_t(A.rows <= 16 ? 96 : 256) << 20);
   if (whole_heads(A.a.c.B * A.a.c.H, A.pieces, A.rows, A.scores != nullptr)) {
@@ -591,7 +593,7 @@ void attend_rows(const Args& A, hipStream_t s) {
   } else {
     // One row block of 32, not two of 16 that read each key twice: 99.6 us against 107 (13
     // sequences of 8192 slots, d 128), 36.8 against 35.6 (64 of 1100).
-    if (fours && stream) attend_few<D, 2, 4, true>(A, s);
+    if (D == 128 && fours && stream) attend_few<128, 2, 4, true>(A, s);
     else if (fours) attend_few<D, 2, 4, false>(A, s);
     else attend_few<D, 2, 1, false>(A, s);
   }
