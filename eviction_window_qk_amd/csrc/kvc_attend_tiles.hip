@@ -56,7 +56,7 @@ struct Args {
   int slots;          // workgroups of a head
   int parts, per;     // ways a head's slots are dealt out to the XCDs, slots in each
   FastDiv by_per, by_parts;
-  float* part;        // [H][slots][kRows][D] outputs of a piece
+  float* part;        // [H][slots][D / 4][kRows][4] outputs of a piece
   float* stat;        // [H][slots][kRows] log2 of its sum of 2^x
 };
 
@@ -373,13 +373,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   const float by_l = any ? 1.0f / l : 0.0f;
   const float b_sum = any ? fast_log2(l) - nm : -INFINITY;   // log2 of the row's sum of 2^x
   if (PAGED && w.pieces > 1) {
-    const size_t row = (size_t(w.h) * A.slots + w.slot) * kRows + (r - w.r0);
-    float* po = A.part + row * D;
+    const size_t tile = size_t(w.h) * A.slots + w.slot, row = tile * kRows + (r - w.r0);
+    float* po = A.part + tile * kRows * D + (r - w.r0) * 4;
 #pragma unroll
     for (int d = 0; d < kDims; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * e + 4 * hh) =
+        *reinterpret_cast<f32x4*>(po + (32 * d + 8 * e + 4 * hh) * kRows) =
             f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * by_l;
     if (hh == 0) A.stat[row] = b_sum;
     return;
@@ -408,11 +408,12 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
   const int R = mine.y * G, start = mine.x, t = tile - first_tile(start, b, G);
   if (R <= kFewRows || t < 0) return;
   const int tiles = (R + kRows - 1) / kRows, pieces = tile_pieces(paged_len(A.c, b), tiles);
-  const int in_tile = int(blockIdx.y) * kAtOnce + int(threadIdx.x) / kLanes, r = t * kRows + in_tile;
+  const int in_tile = int(blockIdx.y) * kAtOnce + int(threadIdx.x) % kAtOnce, r = t * kRows + in_tile;
   const int slot = first_slot(start, b, G) + t;
   if (pieces == 1 || r >= R || slot + (pieces - 1) * tiles >= A.slots) return;
-  const int dim = threadIdx.x % kLanes * 4;
+  const int dim = threadIdx.x / kAtOnce * 4;
   const size_t row = (size_t(h) * A.slots + slot) * kRows + in_tile;
+  const float* part = A.part + (size_t(h) * A.slots + slot) * kRows * D + (dim * kRows + in_tile * 4);
   const size_t step = size_t(tiles) * kRows;             // from piece to piece
   float M = -INFINITY;
 #pragma unroll 4
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
 #pragma unroll 4
   for (int p = 0; p < pieces; ++p) {
     const float f = fast_exp2(A.stat[row + p * step] - base);
-    sum += *reinterpret_cast<const f32x4*>(A.part + (row + p * step) * D + dim) * f;
+    sum += *reinterpret_cast<const f32x4*>(part + p * step * D) * f;
     L += f;
   }
   const float by_l = L > 0.0f ? 1.0f / L : 0.0f;
