@@ -492,16 +492,21 @@ __device__ __forceinline__ void weigh_piece(const Args& A, float* less) {
   if (R > kFewRows || t0 >= len) return;
   static_assert(kThreads == 8 * kFewRows, "eight lanes a row");
   const int pieces = (len + chunk - 1) / chunk, row = threadIdx.x >> 3;
+  float* const to = c.weight + size_t(n) * c.room;
+  float was[4];
+  auto look = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) was[i] = t + i < end ? to[t + i] : 0.0f;
+  };
+  const int first = t0 + int(threadIdx.x) * 4;
+  look(first);
   float base;
   const float L = whole_sum<8>(A.stat + (size_t(n) * A.rows + row) * A.pieces, row < R ? pieces : 0, base);
   if (threadIdx.x % 8 == 0) less[row] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
   __syncthreads();
-  for (int t = t0 + int(threadIdx.x) * 4; t < end; t += kThreads * 4) {
-    float* to = c.weight + size_t(n) * c.room + t;
-    float was[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) was[i] = t + i < end ? to[i] : 0.0f;
-    weigh_four(A, n, t, end, R, less, was, to);
+  for (int t = first; t < end; t += kThreads * 4) {
+    if (t > first) look(t);
+    weigh_four(A, n, t, end, R, less, was, to + t);
   }
 }
 
