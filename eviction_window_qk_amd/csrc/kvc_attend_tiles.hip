@@ -22,7 +22,14 @@
 //
 // Tiles go from global memory to LDS without passing registers, one tile ahead, in
 // the order in which the LDS banks serve both kinds of reads: 16-byte piece p of row
-// r sits at place p ^ swizzle(r).
+// r sits at place p ^ swizzle(r).  Two workgroups share a CU, so that one's softmax runs
+// beside the other's products.
+//
+// Measured: a 16384-token prompt, 8 KV heads of 128, 4 rows a token, 2040 us (1080 TFLOP/s,
+// matrix cores busy 52 % at 1.9 GHz; a library product of 8192^3 reaches 1232); of 64
+// values 1210 us (909).  512 tokens over 131072 slots 1150 us (955).  In copies of the
+// kernel the 16384-token prompt took 1761 us without the loads to LDS, 1961 without exp2, 1844 without
+// both and half of the LDS reads.
 #include <type_traits>
 
 #include "kvc_paged.h"
@@ -397,7 +404,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
 }
 
 // Joins the pieces of 1024 / D rows of a row tile, each weighted by its sum, four values
-// a lane.
+// a lane, in the partials' order: 4 D bytes a row and piece, 15 us of the 255 of a mixed
+// batch (24 sequences of up to 16384 slots of 8 heads of 64, 1183 new tokens).
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tiles) {
   constexpr int kLanes = D / 4, kAtOnce = kThreads / kLanes;
@@ -439,7 +447,9 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
 // Column sums of the softmax weights of sequences with many rows: keys stationary, 64 a
 // wave as the second operand of S = Q K', query rows streamed through LDS 64 at a time.
 // The accumulator gives a lane one key and 16 rows, so the sum down the rows is
-// lane-local; its order is fixed.
+// lane-local; its order is fixed.  It takes the scores again (2 d flops a row and key): kept,
+// they would be 4 bytes of each.  67 us in the mixed batch, bound by exp2 and its FMA and
+// add (16 cycles a score for the products' 8) and by the start of short runs of rows.
 constexpr int kKeys = kWaves * 64;
 template <int D>
 __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int n0) {

@@ -103,7 +103,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // kFewChunk, doubled to kFewMaxChunk while there are more than 64; equal pieces, in
 // multiples of the workgroup's 128-key stride.  A piece depends on the sequence's own
 // length only, so a head's sums are taken in the same order whatever else is in the
-// launch.
+// launch.  Pieces of 256 or 384 start and join too often in batches, of 1024 leave one
+// sequence of some thousand slots on too few CUs.
 constexpr int kFewChunk = 512, kFewMaxChunk = 2048;
 static_assert(kFewChunk % 128 == 0 && kFewMaxChunk % 128 == 0, "pieces are whole strides");
 __host__ __device__ inline int few_chunk(int len) {
@@ -126,7 +127,9 @@ constexpr int kFewRows = 32, kTileRows = 128;
 // Pieces that the keys of a sequence with `tiles` row tiles are cut into: about kTileWork
 // pairs of a tile and a piece for each KV head (eight heads then fill the chip once, two
 // workgroups a CU), pieces of at least kTileSpan keys.  The sequence's own length and row
-// count decide.
+// count decide.  32 pairs (us, 8 heads of 128, 4 rows a token; 64 : 32): one chunk of 512 tokens over
+// 16384 slots 158 : 195, of 128 over 8192 41 : 41, ten of 100 over 8192 277 : 223.  Spans
+// of 512 : 1024 : 2048: one chunk of 32 over 4096 slots 30 : 37 : 58, 32 of 64 315 : 275 : 275.
 constexpr int kTileWork = 64, kTileSpan = 512;
 __host__ __device__ inline int tile_pieces(int len, int tiles) {
   const int most = (len + kTileSpan - 1) / kTileSpan, want = kTileWork / tiles;
