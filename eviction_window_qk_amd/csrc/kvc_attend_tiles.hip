@@ -444,14 +444,13 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
         L > 0.0f ? (base + fast_log2(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-// Column sums of the softmax weights of sequences with many rows: keys stationary, 64 a
+// Column sums of the softmax weights of sequences with many rows: keys stationary, 32 kX a
 // wave as the second operand of S = Q K', query rows streamed through LDS 64 at a time.
 // The accumulator gives a lane one key and 16 rows, so the sum down the rows is
 // lane-local; its order is fixed.  It takes the scores again (2 d flops a row and key): kept,
 // they would be 4 bytes of each.  67 us in the mixed batch, bound by exp2 and its FMA and
 // add (16 cycles a score for the products' 8) and by the start of short runs of rows.
-constexpr int kKeys = kWaves * 64;
-template <int D>
+template <int D, int kX>
 __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int n0) {
   constexpr int kPieces = D / 8;
   constexpr int kRowsPerLoad = 64 / kPieces;
@@ -464,16 +463,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
   const int2 mine = chunk_of(A.k, b);
   const int R = mine.y * A.G, len = paged_len(A.c, b);
   if (R <= kFewRows) return;
-  const int t0 = (int(blockIdx.x) - nth * int(by_chunks.d)) * kKeys;
+  const int t0 = (int(blockIdx.x) - nth * int(by_chunks.d)) * (kWaves * 32 * kX);
   if (t0 >= len) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 31, hh = lane >> 5;
-  const int key0 = t0 + wave * 64;
-  u32x4 kf[2][kSteps];
-  bool there[2];
+  const int key0 = t0 + wave * 32 * kX;
+  u32x4 kf[kX][kSteps];
+  bool there[kX];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < kX; ++x) {
     const int t = key0 + x * 32 + j;
     const int64_t row = t < len ? paged_row(A.c, b, h, t) : -1;
     there[x] = row >= 0;
@@ -481,9 +480,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
     for (int s = 0; s < kSteps; ++s)
       kf[x][s] = there[x] ? *reinterpret_cast<const u32x4*>(A.c.k + row * D + s * 16 + hh * 8) : u32x4{0, 0, 0, 0};
   }
-  // Rows that see any of the keys: from the first token whose slot is at or past t0.
-  const int first_new = len - mine.y;
-  const int tok = t0 > first_new ? t0 - first_new : 0;
+  // Rows that see any of the keys: from the first token whose slot is at or past t0, or
+  // a 256-key boundary before it, so that a key's rows are added in one order whatever kX.
+  const int first_new = len - mine.y, seen_from = t0 & ~255;
+  const int tok = seen_from > first_new ? seen_from - first_new : 0;
   const int r_from = tok * A.G, n_tiles = (R - r_from + kTile - 1) / kTile;
   auto fetch = [&](int tile, int buf) {
     const int r0 = r_from + tile * kTile;
@@ -503,7 +503,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
     }
   };
   fetch(0, 0);
-  float total[2] = {0.0f, 0.0f};
+  float total[kX] = {};
   const float by = A.c_log2;
   for (int tile = 0; tile < n_tiles; ++tile) {
     __builtin_amdgcn_s_waitcnt(0);
@@ -512,13 +512,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
     const uint16_t* qt = qs[tile & 1];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-      f32x16 sc[2] = {f32x16{}, f32x16{}};
+      f32x16 sc[kX] = {};
       const int row = blk * 32 + j;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const u32x4 qf = *reinterpret_cast<const u32x4*>(qt + row * D + (((2 * s + hh) ^ swizzle<D>(row)) << 3));
-        sc[0] = mfma(qf, kf[0][s], sc[0]);
-        sc[1] = mfma(qf, kf[1][s], sc[1]);
+#pragma unroll
+        for (int x = 0; x < kX; ++x) sc[x] = mfma(qf, kf[x][s], sc[x]);
       }
       auto add = [&](auto checked) {
 #pragma unroll
@@ -530,19 +530,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < kX; ++x) {
               const float p = fast_exp2(__builtin_fmaf(sc[x][4 * e4 + e], by, bz[e]));
               total[x] += !checked || key0 + x * 32 + j <= lm[e] ? p : 0.0f;
             }
         }
       };
       // the tile's first row sees least
-      if (key0 + 63 <= first_new + int(quot(A.by_G, uint32_t(r_from + tile * kTile)))) add(std::false_type{});
+      if (key0 + 32 * kX - 1 <= first_new + int(quot(A.by_G, uint32_t(r_from + tile * kTile)))) add(std::false_type{});
       else add(std::true_type{});
     }
   }
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
+  for (int x = 0; x < kX; ++x) {
     total[x] += __shfl_xor(total[x], 32);
     if (hh == 0 && there[x]) A.c.weight[size_t(n) * A.c.room + key0 + x * 32 + j] += total[x];
   }
@@ -560,6 +560,17 @@ unsigned deal(Args& A, int slots) {
   return unsigned((int64_t(A.H) * A.parts + kXcds - 1) / kXcds * kXcds * A.per);
 }
 
+template <int D, int kX>
+void weigh_tiles(const Args& A, hipStream_t s) {
+  constexpr int kKeys = kWaves * 32 * kX;
+  const int chunks = (A.c.cap + kKeys - 1) / kKeys;
+  const int heads = A.c.B * A.H, most = (1 << 23) / chunks;
+  for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
+    const int nh = heads - n0 < most ? heads - n0 : most;
+    k_weights_tiles<D, kX><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);
+  }
+}
+
 template <int D>
 void attend_chunks(Args& A, hipStream_t s) {
   const unsigned blocks = deal(A, A.slots);
@@ -570,12 +581,11 @@ void attend_chunks(Args& A, hipStream_t s) {
     k_join_tiles<D><<<dim3(unsigned(tiles) * unsigned(A.H), kRows * D / 1024), kThreads, 0, s>>>(A, fast_div(uint32_t(tiles)));
   }
   if (!A.c.weight) return;
-  const int chunks = (A.c.cap + kKeys - 1) / kKeys;
-  const int heads = A.c.B * A.H, most = (1 << 23) / chunks;
-  for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
-    const int nh = heads - n0 < most ? heads - n0 : most;
-    k_weights_tiles<D><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);
-  }
+  // A key's sum is the same either way.  Half as many keys a wave where workgroups of twice
+  // as many do not give every CU two: 2048 new tokens in 4096 slots of 8 heads of 128 307 us
+  // against 364 (128 workgroups); 512 over 16384 242 against 234 (512 of them).
+  if (A.c.B * int64_t(A.H) * ((A.c.cap + 255) / 256) < 512) weigh_tiles<D, 1>(A, s);
+  else weigh_tiles<D, 2>(A, s);
 }
 
 }  // namespace

@@ -1116,7 +1116,7 @@ def _ints(t, shape, device, name):
 def _group(q, kv_heads, name):
     if q.dim() != 3:
         raise ValueError(f"{name}: 3 dimensions expected")
-    if q.shape[1] % kv_heads:
+    if kv_heads < 1 or q.shape[1] % kv_heads:
         raise ValueError(f"{name}: {q.shape[1]} heads are no multiple of {kv_heads}")
     return _int(q.shape[1] // kv_heads, "group")
 

@@ -354,6 +354,21 @@ def test_many_heads_of_few_pieces(case, weights):
             assert torch.equal(one.weight, g.weight[heads])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_weights_of_many_rows_alone_and_in_a_batch(d):
+    """One sequence (few workgroups, of fewer keys each) and twelve of them (many) give the same weights."""
+    H, G, T, n = 4, 2, 4000, 300
+    c = u.random_cache(83, 1, H, d, 16, [T], weights=True)
+    q = dev_bf16(random_rows(84, n, G * H, d))
+    one = u.to_gpu(c)
+    kvc.paged_attend(one, q, u.dev(u.starts_of([n])))
+    B = 12
+    many = kvc.PagedCache(one.k_pool, one.v_pool, one.table.repeat(B, 1), one.seq_len.repeat(B),
+                          weight=u.dev(np.tile(c.weight, (B, 1))), pos=u.dev(np.tile(c.pos, (B, 1))))
+    kvc.paged_attend(many, q.repeat(B, 1, 1), u.dev(u.starts_of([n] * B)))
+    assert torch.equal(many.weight, one.weight.repeat(B, 1))
+
+
 def test_max_len_bounds_the_lengths():
     c = u.random_cache(73, 2, 1, 64, 16, [300, 90], weights=True, max_len=200)
     c.lens[0] = 300
