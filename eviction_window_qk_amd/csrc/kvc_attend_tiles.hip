@@ -447,18 +447,25 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
 // Column sums of the softmax weights of sequences with many rows: keys stationary, 32 kX a
 // wave as the second operand of S = Q K', query rows streamed through LDS 64 at a time.
 // The accumulator gives a lane one key and 16 rows, so the sum down the rows is
-// lane-local; its order is fixed.  It takes the scores again (2 d flops a row and key): kept,
+// lane-local; its order is fixed: every fourth tile of rows makes a sum, and the four are
+// added.  kParts 4: by four waves each.  It takes the scores again (2 d flops a row and key): kept,
 // they would be 4 bytes of each.  67 us in the mixed batch, bound by exp2 and its FMA and
 // add (16 cycles a score for the products' 8) and by the start of short runs of rows.
-template <int D, int kX>
-__global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv by_chunks, int n0) {
+constexpr int kRuns = 4;
+template <int D, int kX, int kParts>
+__global__ __launch_bounds__(kParts * kThreads, kParts == 1 ? 2 : 1) void k_weights_tiles(Args A, FastDiv by_chunks, int n0) {
   constexpr int kPieces = D / 8;
   constexpr int kRowsPerLoad = 64 / kPieces;
   constexpr int kLoads = kTile / kWaves / kRowsPerLoad;
   constexpr int kSteps = D / 16;
-  __shared__ __align__(16) uint16_t qs[2][kTile * D];
-  __shared__ __align__(16) float bs[2][kTile];           // -log2 of the rows' sums
-  __shared__ __align__(16) int lim[2][kTile];            // the rows' last keys
+  static_assert(kParts == 1 || kParts == kRuns, "a part takes all runs, or one");
+  __shared__ __align__(16) uint16_t qs_all[kParts][2][kTile * D];
+  __shared__ __align__(16) float bs_all[kParts][2][kTile];   // -log2 of the rows' sums
+  __shared__ __align__(16) int lim_all[kParts][2][kTile];    // the rows' last keys
+  const int part = kParts == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads), tid = threadIdx.x % kThreads;
+  auto& qs = qs_all[part];
+  auto& bs = bs_all[part];
+  auto& lim = lim_all[part];
   const int nth = int(quot(by_chunks, blockIdx.x)), n = n0 + nth, b = n / A.H, h = n - b * A.H;
   const int2 mine = chunk_of(A.k, b);
   const int R = mine.y * A.G, len = paged_len(A.c, b);
@@ -466,7 +473,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
   const int t0 = (int(blockIdx.x) - nth * int(by_chunks.d)) * (kWaves * 32 * kX);
   if (t0 >= len) return;
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane & 31, hh = lane >> 5;
   const int key0 = t0 + wave * 32 * kX;
   u32x4 kf[kX][kSteps];
@@ -494,22 +501,27 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
       const int piece = (lane % kPieces) ^ swizzle<D>(row);
       to_lds(A.q.p + int64_t(mine.x + i) * A.q.ts + int64_t(h * A.G + r - i * A.G) * A.q.hs + piece * 8, qs[buf] + first * D);
     }
-    if (threadIdx.x < kTile) {
-      const int r = r0 + int(threadIdx.x), rc = r < R ? r : R - 1, i = int(quot(A.by_G, uint32_t(rc)));
+    if (tid < kTile) {
+      const int r = r0 + tid, rc = r < R ? r : R - 1, i = int(quot(A.by_G, uint32_t(rc)));
       const float z = A.lse[size_t(mine.x + i) * (A.G * A.H) + h * A.G + rc - i * A.G];
       const bool any = r < R && z != -INFINITY;
-      bs[buf][threadIdx.x] = any ? -z * 1.4426950408889634f : -INFINITY;   // a row that sees nothing gives nothing
-      lim[buf][threadIdx.x] = first_new + i;
+      bs[buf][tid] = any ? -z * 1.4426950408889634f : -INFINITY;   // a row that sees nothing gives nothing
+      lim[buf][tid] = first_new + i;
     }
   };
-  fetch(0, 0);
-  float total[kX] = {};
+  if (part < n_tiles) fetch(part, 0);
+  float total[kX] = {}, sum[kX] = {};
   const float by = A.c_log2;
-  for (int tile = 0; tile < n_tiles; ++tile) {
+  const int steps = kParts == 1 ? n_tiles : (n_tiles + kRuns - 1) / kRuns;
+  int tile = part;
+  for (int step = 0; step < steps; ++step) {
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    if (tile + 1 < n_tiles) fetch(tile + 1, (tile + 1) & 1);
-    const uint16_t* qt = qs[tile & 1];
+    const bool last = tile + kRuns >= n_tiles;                     // of its run
+    const int next = kParts == 1 && last ? tile % kRuns + 1 : tile + kRuns;
+    if (step + 1 < steps && next < n_tiles) fetch(next, (step + 1) & 1);
+    if (kParts > 1 && tile >= n_tiles) continue;
+    const uint16_t* qt = qs[step & 1];
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
       f32x16 sc[kX] = {};
@@ -524,9 +536,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
 #pragma unroll
         for (int e4 = 0; e4 < 4; ++e4) {
           const int at = blk * 32 + 8 * e4 + 4 * hh;
-          const f32x4 bz = *reinterpret_cast<const f32x4*>(&bs[tile & 1][at]);
+          const f32x4 bz = *reinterpret_cast<const f32x4*>(&bs[step & 1][at]);
           i32x4 lm = {0, 0, 0, 0};
-          if constexpr (checked) lm = *reinterpret_cast<const i32x4*>(&lim[tile & 1][at]);
+          if constexpr (checked) lm = *reinterpret_cast<const i32x4*>(&lim[step & 1][at]);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
@@ -540,11 +552,28 @@ __global__ __launch_bounds__(kThreads, 2) void k_weights_tiles(Args A, FastDiv b
       if (key0 + 32 * kX - 1 <= first_new + int(quot(A.by_G, uint32_t(r_from + tile * kTile)))) add(std::false_type{});
       else add(std::true_type{});
     }
+    if (kParts == 1 && last) {
+#pragma unroll
+      for (int x = 0; x < kX; ++x) sum[x] += total[x], total[x] = 0.0f;
+    }
+    tile = next;
+  }
+  if constexpr (kParts > 1) {
+    float* const sums = reinterpret_cast<float*>(qs_all);   // [part][x][thread]
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kX; ++x) sums[(part * kX + x) * kThreads + tid] = total[x];
+    __syncthreads();
+    if (part > 0) return;
+#pragma unroll
+    for (int x = 0; x < kX; ++x)
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) sum[x] += sums[(i * kX + x) * kThreads + tid];
   }
 #pragma unroll
   for (int x = 0; x < kX; ++x) {
-    total[x] += __shfl_xor(total[x], 32);
-    if (hh == 0 && there[x]) A.c.weight[size_t(n) * A.c.room + key0 + x * 32 + j] += total[x];
+    sum[x] += __shfl_xor(sum[x], 32);
+    if (hh == 0 && there[x]) A.c.weight[size_t(n) * A.c.room + key0 + x * 32 + j] += sum[x];
   }
 }
 
@@ -560,14 +589,14 @@ unsigned deal(Args& A, int slots) {
   return unsigned((int64_t(A.H) * A.parts + kXcds - 1) / kXcds * kXcds * A.per);
 }
 
-template <int D, int kX>
+template <int D, int kX, int kParts>
 void weigh_tiles(const Args& A, hipStream_t s) {
   constexpr int kKeys = kWaves * 32 * kX;
   const int chunks = (A.c.cap + kKeys - 1) / kKeys;
   const int heads = A.c.B * A.H, most = (1 << 23) / chunks;
   for (int n0 = 0; n0 < heads; n0 += most) {   // at most 2^23 workgroups a launch
     const int nh = heads - n0 < most ? heads - n0 : most;
-    k_weights_tiles<D, kX><<<unsigned(nh) * unsigned(chunks), kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);
+    k_weights_tiles<D, kX, kParts><<<unsigned(nh) * unsigned(chunks), kParts * kThreads, 0, s>>>(A, fast_div(uint32_t(chunks)), n0);
   }
 }
 
@@ -581,11 +610,15 @@ void attend_chunks(Args& A, hipStream_t s) {
     k_join_tiles<D><<<dim3(unsigned(tiles) * unsigned(A.H), kRows * D / 1024), kThreads, 0, s>>>(A, fast_div(uint32_t(tiles)));
   }
   if (!A.c.weight) return;
-  // A key's sum is the same either way.  Half as many keys a wave where workgroups of twice
-  // as many do not give every CU two: 2048 new tokens in 4096 slots of 8 heads of 128 307 us
-  // against 364 (128 workgroups); 512 over 16384 242 against 234 (512 of them).
-  if (A.c.B * int64_t(A.H) * ((A.c.cap + 255) / 256) < 512) weigh_tiles<D, 1>(A, s);
-  else weigh_tiles<D, 2>(A, s);
+  // A key's sum is the same in all three.  Half as many keys a wave, and of many rows a
+  // quarter too, where workgroups of 256 keys do not give every CU two (8 heads of 128, 4
+  // rows a token, the whole call, us): 2048 new tokens in 4096 slots, 128 workgroups, 364 : 305 :
+  // 215, 128 tokens 49 : 46 in quarters, 64 40.2 : 40.8; 512 over 16384, 512 workgroups, 234 :
+  // 242 : 259.
+  const bool few = A.c.B * int64_t(A.H) * ((A.c.cap + 255) / 256) < 512;
+  if (!few) weigh_tiles<D, 2, 1>(A, s);
+  else if (int64_t(A.G) * A.k.max_new < 512) weigh_tiles<D, 1, 1>(A, s);
+  else weigh_tiles<D, 1, kRuns>(A, s);
 }
 
 }  // namespace

@@ -354,14 +354,17 @@ def test_many_heads_of_few_pieces(case, weights):
             assert torch.equal(one.weight, g.weight[heads])
 
 
+@pytest.mark.parametrize("n", [40, 100, 300, 700])
 @pytest.mark.parametrize("d", [64, 128])
-def test_weights_of_many_rows_alone_and_in_a_batch(d):
-    """One sequence (few workgroups, of fewer keys each) and twelve of them (many) give the same weights."""
-    H, G, T, n = 4, 2, 4000, 300
+def test_weights_of_many_rows_alone_and_in_a_batch(d, n):
+    """One sequence (few workgroups, of fewer keys and rows each) and twelve of them (many) give the
+    same weights."""
+    H, G, T = 4, 2, 4000
     c = u.random_cache(83, 1, H, d, 16, [T], weights=True)
     q = dev_bf16(random_rows(84, n, G * H, d))
     one = u.to_gpu(c)
     kvc.paged_attend(one, q, u.dev(u.starts_of([n])))
+    u.check_weights(og.attend(c, og.widen(u.bits(q)), u.starts_of([n])), c.weight, one.weight.cpu().numpy(), d, G * n)
     B = 12
     many = kvc.PagedCache(one.k_pool, one.v_pool, one.table.repeat(B, 1), one.seq_len.repeat(B),
                           weight=u.dev(np.tile(c.weight, (B, 1))), pos=u.dev(np.tile(c.pos, (B, 1))))
