@@ -2,7 +2,7 @@
 // tokens over a paged cache.
 //
 // A sequence's n new tokens and the G query heads of a KV head form R = G*n rows (row
-// r: token r / G, head r % G).  A workgroup takes 128 rows, 32 a wave, and streams
+// r: token r / G, head r % G).  A workgroup takes 128 or 256 rows, 32 a wave, and streams
 // their keys and values through LDS in tiles of 64 keys, so that each tile is read
 // once for all of them; with many rows the bound is the matrix cores (4*d flops a
 // row and key) and, beside them, the vector ALU: one FMA, one exp2, one add and half
@@ -22,8 +22,8 @@
 //
 // Tiles go from global memory to LDS without passing registers, one tile ahead, in
 // the order in which the LDS banks serve both kinds of reads: 16-byte piece p of row
-// r sits at place p ^ swizzle(r).  Two workgroups share a CU, so that one's softmax runs
-// beside the other's products.
+// r sits at place p ^ swizzle(r).  Eight waves share a CU, so that one's softmax runs
+// beside another's products.
 //
 // Measured: a 16384-token prompt, 8 KV heads of 128, 4 rows a token, 2040 us (1080 TFLOP/s,
 // matrix cores busy 52 % at 1.9 GHz; a library product of 8192^3 reaches 1232); of 64
@@ -105,7 +105,7 @@ __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
 
 // What a workgroup works on: its sequence, KV head, rows and piece of the keys.
 struct Where {
-  int b, h, slot;
+  int b, h, first;    // first: of the sequence's slots
   int r0, R;          // first row, rows of the sequence
   int token0, n;      // first new token and their count
   int len;            // keys of the sequence
@@ -118,50 +118,53 @@ struct Where {
 // parts-th where the heads do not fill the XCDs evenly), the last rows first: they see
 // most keys.  The row tiles of a piece follow each other on one XCD, whose L2 then reads
 // the keys once.
-template <bool PAGED>
+template <bool PAGED, int kW>
 __device__ __forceinline__ bool find(const Args& A, Where& w) {
+  constexpr int kHere = kW * 32;                         // rows of a workgroup
   const uint32_t x = blockIdx.x % kXcds, i = blockIdx.x / kXcds;
   const uint32_t nth = quot(A.by_per, i);
   const uint32_t unit = nth * kXcds + x;                 // (head, part)
   const uint32_t h = quot(A.by_parts, unit);
   if (h >= uint32_t(A.H)) return false;
   const int at = int(i - nth * A.per) * A.parts + int(unit - h * A.parts);
-  w.slot = A.slots - 1 - at;
-  if (w.slot < 0) return false;
+  const int slot = A.slots - 1 - at;
+  if (slot < 0) return false;
   const int G = A.G;
-  const auto first = [G](int s, int b) { return PAGED ? first_slot(s, b, G) : first_tile(s, b, G); };
-  w.b = last_at_or_below(A.k, w.slot, first);
+  const auto first = [G](int s, int b) { return PAGED ? first_slot(s, b, G) : first_tile(s, b, G, kHere); };
+  w.b = last_at_or_below(A.k, slot, first);
   const int2 mine = chunk_of(A.k, w.b);
   w.h = int(h);
   w.token0 = mine.x;
   w.n = mine.y;
   w.R = mine.y * G;
-  const int s = w.slot - first(mine.x, w.b);
+  w.first = first(mine.x, w.b);
+  const int s = slot - w.first;
   w.tiles = (w.R + kRows - 1) / kRows;
   if (PAGED) {
     if (w.R <= kFewRows || s < 0) return false;
     w.len = paged_len(A.c, w.b);
     w.pieces = tile_pieces(w.len, w.tiles);
-    w.piece = s / w.tiles;
-    if (w.piece >= w.pieces || w.slot - s + w.tiles * w.pieces > A.slots) return false;
-    w.r0 = (s - w.piece * w.tiles) * kRows;
+    const int here = (w.R + kHere - 1) / kHere;
+    w.piece = s / here;
+    if (w.piece >= w.pieces || w.first + w.tiles * w.pieces > A.slots) return false;
+    w.r0 = (s - w.piece * here) * kHere;
     return true;
   }
   w.len = w.n;
   w.piece = 0;
   w.pieces = 1;
-  w.r0 = s * kRows;
+  w.r0 = s * kHere;
   return s >= 0 && w.r0 < w.R;
 }
 
-// GROUP: keys that a look-up in the table covers, of a wave's load all where pages hold
+// kW: waves of a workgroup.  GROUP: keys that a look-up in the table covers, of a wave's load all where pages hold
 // whole loads, or one; 0: no cache.
-template <int D, int GROUP>
-__global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
+template <int D, int GROUP, int kW>
+__global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
   constexpr bool PAGED = GROUP != 0;
   constexpr int kPieces = D / 8;             // 16-byte pieces of a row
   constexpr int kRowsPerLoad = 64 / kPieces; // rows one wave's load covers
-  constexpr int kLoads = kTile / kWaves / kRowsPerLoad;
+  constexpr int kLoads = kTile / kW / kRowsPerLoad;
   constexpr int kSteps = D / 16;             // matrix steps over the head dimension
   constexpr int kDims = D / 32;              // 32-value blocks of the output
   constexpr int kPerTile = PAGED ? kTile / GROUP : 1;    // look-ups of a tile
@@ -171,7 +174,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   __shared__ __align__(16) uint16_t vs[2][kTile * D];
 
   Where w;
-  if (!find<PAGED>(A, w)) return;
+  if (!find<PAGED, kW>(A, w)) return;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int j = lane & 31, hh = lane >> 5;
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   const int low = __builtin_amdgcn_readfirstlane(limit);
   // A wave without rows helps to load.
   const int high = w.r0 + wave * 32 < w.R ? __builtin_amdgcn_readlane(limit, 31) : -1;
-  const int last_row = w.r0 + kRows <= w.R ? w.r0 + kRows - 1 : w.R - 1;
+  const int last_row = w.r0 + kW * 32 <= w.R ? w.r0 + kW * 32 - 1 : w.R - 1;
   // Keys that any row of the tile sees, of these the piece's.
   const int seen = w.len - w.n + int(quot(A.by_G, uint32_t(last_row))) + 1;
   const int span = PAGED ? tile_span(w.len, w.pieces) : 0;
@@ -213,7 +216,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   uint32_t k_off[kLoads], v_off[kLoads];
 #pragma unroll
   for (int x = 0; x < kLoads; ++x) {
-    const int row = wave * (kTile / kWaves) + x * kRowsPerLoad + lane / kPieces;
+    const int row = wave * (kTile / kW) + x * kRowsPerLoad + lane / kPieces;
     const int piece = (lane % kPieces) ^ swizzle<D>(row);
     k_off[x] = PAGED ? uint32_t((lane / kPieces) * D + piece * 8) * 2 : (uint32_t(row) * uint32_t(A.kr.ts) + piece * 8) * 2;
     v_off[x] = PAGED ? k_off[x] : (uint32_t(row) * uint32_t(A.vr.ts) + piece * 8) * 2;
@@ -226,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
         const uint16_t* vp = vb + int64_t(t0) * A.vr.ts;
 #pragma unroll
         for (int x = 0; x < kLoads; ++x) {
-          const int first = wave * (kTile / kWaves) + x * kRowsPerLoad;
+          const int first = wave * (kTile / kW) + x * kRowsPerLoad;
           to_lds(at_off(kp, k_off[x]), ks[buf] + first * D);
           to_lds(at_off(vp, v_off[x]), vs[buf] + first * D);
         }
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
     }
 #pragma unroll
     for (int x = 0; x < kLoads; ++x) {
-      const int first = wave * (kTile / kWaves) + x * kRowsPerLoad, row = first + lane / kPieces;
+      const int first = wave * (kTile / kW) + x * kRowsPerLoad, row = first + lane / kPieces;
       const int piece = (lane % kPieces) ^ swizzle<D>(row);
       if constexpr (!PAGED) {
         const int t = t0 + row < w.n ? t0 + row : w.n - 1;
@@ -380,8 +383,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_tiles(Args A) {
   const float by_l = any ? 1.0f / l : 0.0f;
   const float b_sum = any ? fast_log2(l) - nm : -INFINITY;   // log2 of the row's sum of 2^x
   if (PAGED && w.pieces > 1) {
-    const size_t tile = size_t(w.h) * A.slots + w.slot, row = tile * kRows + (r - w.r0);
-    float* po = A.part + tile * kRows * D + (r - w.r0) * 4;
+    const size_t tile = size_t(w.h) * A.slots + (w.first + w.piece * w.tiles + r / kRows), row = tile * kRows + r % kRows;
+    float* po = A.part + tile * kRows * D + r % kRows * 4;
 #pragma unroll
     for (int d = 0; d < kDims; ++d)
 #pragma unroll
@@ -589,6 +592,27 @@ unsigned deal(Args& A, int slots) {
   return unsigned((int64_t(A.H) * A.parts + kXcds - 1) / kXcds * kXcds * A.per);
 }
 
+// Whether workgroups take 256 rows, eight waves, and so half as many loads of keys for their
+// products (the results are the same bits: a wave's rows are the same ones).  It pays
+// for 128 values (64 are bound by the softmax: 1357 us against 1296 on a 16384-token
+// prompt) where they still fill the chip, waste few rows and run long.  Of prompts (us, eight waves :
+// four; 8 KV heads, 4 rows a token unless said): 16384 tokens 2224 : 2330, 4096 155 : 161, 11 of 2043 on
+// average, 4 heads of 7 rows, 561 : 578, 8 of 2048 342 : 344, 16 of 1024 222 : 209, one of 2048 62 : 57,
+// 16384 tokens of one KV head (256 workgroups) 409 : 392.
+bool eight_waves(int64_t rows, int seqs, int H, int D) {
+  return D == 128 && rows / seqs >= 8192 && rows * H / (2 * kRows) >= 512;
+}
+// Of chunks over a cache, by the rows of a sequence on average and the longest length: 512 tokens over
+// 131072 slots 1149 : 1263, over 16384 162 : 175, over 8192 (pieces of 2048 keys) 91 : 97; 8 of 256
+// over 4096 (of 512) 257 : 242, 8 of 64 over 32768 (of 1024) 443 : 431; 512 over 32768 slots of four
+// heads (128 workgroups) 226 : 200.
+bool eight_waves(const Args& A, int D) {
+  const int64_t rows = int64_t(A.k.n_tokens) * A.G / A.k.B;
+  if (D != 128 || rows <= kRows) return false;
+  const int tiles = int((rows + kRows - 1) / kRows), pieces = tile_pieces(A.c.cap, tiles);
+  return tile_span(A.c.cap, pieces) >= 2048 && A.H * int64_t(A.k.B) * ((tiles + 1) / 2) * pieces >= 256;
+}
+
 template <int D, int kX, int kParts>
 void weigh_tiles(const Args& A, hipStream_t s) {
   constexpr int kKeys = kWaves * 32 * kX;
@@ -603,8 +627,9 @@ void weigh_tiles(const Args& A, hipStream_t s) {
 template <int D>
 void attend_chunks(Args& A, hipStream_t s) {
   const unsigned blocks = deal(A, A.slots);
-  if (A.c.bs % (512 / D) == 0) k_attend_tiles<D, 512 / D><<<blocks, kThreads, 0, s>>>(A);
-  else k_attend_tiles<D, 1><<<blocks, kThreads, 0, s>>>(A);
+  if (A.c.bs % (512 / D) != 0) k_attend_tiles<D, 1, kWaves><<<blocks, kThreads, 0, s>>>(A);
+  else if (eight_waves(A, D)) k_attend_tiles<D, 512 / D, 8><<<blocks, 512, 0, s>>>(A);
+  else k_attend_tiles<D, 512 / D, kWaves><<<blocks, kThreads, 0, s>>>(A);
   if (tile_max_pieces(A.c.cap) > 1) {
     const int tiles = first_tile(A.k.n_tokens, A.k.B, A.G);
     k_join_tiles<D><<<dim3(unsigned(tiles) * unsigned(A.H), kRows * D / 1024), kThreads, 0, s>>>(A, fast_div(uint32_t(tiles)));
@@ -650,9 +675,11 @@ hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_lo
   A.c_log2 = c_log2;
   A.q = q, A.kr = k_rows, A.vr = v_rows, A.out = out;
   A.lse = lse;
-  const unsigned blocks = deal(A, int(int64_t(k.n_tokens) * G / kRows) + k.B);
-  if (D == 128) k_attend_tiles<128, 0><<<blocks, kThreads, 0, s>>>(A);
-  else k_attend_tiles<64, 0><<<blocks, kThreads, 0, s>>>(A);
+  const bool eight = eight_waves(int64_t(k.n_tokens) * G, k.B, H, D);
+  const unsigned blocks = deal(A, first_tile(k.n_tokens, k.B, G, eight ? 2 * kRows : kRows));
+  if (eight) k_attend_tiles<128, 0, 8><<<blocks, 512, 0, s>>>(A);
+  else if (D == 128) k_attend_tiles<128, 0, kWaves><<<blocks, kThreads, 0, s>>>(A);
+  else k_attend_tiles<64, 0, kWaves><<<blocks, kThreads, 0, s>>>(A);
   return hipGetLastError();
 }
 

@@ -144,8 +144,8 @@ inline int tile_max_pieces(int cap) { return tile_pieces(cap, 1); }
 
 // Row tiles of packed sequences, numbered through: those of sequence b start here, and
 // floor((s + n) G / 128) - floor(s G / 128) + 1 leaves room for its ceil(n G / 128).
-__host__ __device__ inline int first_tile(int start, int b, int G) {
-  return int(int64_t(start) * G / kTileRows) + b;
+__host__ __device__ inline int first_tile(int start, int b, int G, int rows = kTileRows) {
+  return int(int64_t(start) * G / rows) + b;
 }
 // (piece, row tile) pairs of a head over a cache, numbered through: tiles * pieces <=
 // max(kTileWork, tiles).  Only a sequence of more than kFewRows rows has any, so b or

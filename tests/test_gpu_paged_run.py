@@ -372,6 +372,34 @@ def test_weights_of_many_rows_alone_and_in_a_batch(d, n):
     assert torch.equal(many.weight, one.weight.repeat(B, 1))
 
 
+def test_workgroups_of_eight_waves_give_the_bits_of_four():
+    """Long prompts and chunks of many heads (256 rows a workgroup), and each KV head of them alone (128)."""
+    d, H, G = 128, 8, 8
+    starts = u.dev(u.starts_of([2048, 37, 1100]))
+    rows = dev_bf16(random_rows(85, 3190, (G + 2) * H, d))
+    q, k, v = rows[:, : G * H], rows[:, G * H: (G + 1) * H], rows[:, (G + 1) * H:]
+    out = torch.full((3190, G * H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = kvc.prompt_attend(q, k, v, starts, out=out, want_lse=True)
+    assert bool((out[3185:] == 7.0).all())
+    for h in range(H):
+        o, z = kvc.prompt_attend(q[:, h * G: (h + 1) * G], k[:, h: h + 1], v[:, h: h + 1], starts, want_lse=True)
+        assert torch.equal(o[:3185].view(torch.int16), out[:3185, h * G: (h + 1) * G].contiguous().view(torch.int16))
+        assert torch.equal(z[:3185], lse[:3185, h * G: (h + 1) * G])
+    H, G = 4, 4
+    c = u.random_cache(86, 2, H, d, 16, [8192, 7001])
+    c.table[1, 200: 210] = -1
+    starts = u.dev(u.starts_of([512, 401]))
+    q = dev_bf16(random_rows(87, 915, G * H, d))
+    out = torch.full((915, G * H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    _, lse = kvc.paged_attend(u.to_gpu(c), q, starts, out=out, want_lse=True)
+    assert bool((out[913:] == 7.0).all())
+    for h in range(H):
+        one = u.to_gpu(og.Cache(c.k[:, h: h + 1], c.v[:, h: h + 1], c.table, c.lens))
+        o, z = kvc.paged_attend(one, q[:, h * G: (h + 1) * G], starts, want_lse=True)
+        assert torch.equal(o[:913].view(torch.int16), out[:913, h * G: (h + 1) * G].contiguous().view(torch.int16))
+        assert torch.equal(z[:913], lse[:913, h * G: (h + 1) * G])
+
+
 def test_max_len_bounds_the_lengths():
     c = u.random_cache(73, 2, 1, 64, 16, [300, 90], weights=True, max_len=200)
     c.lens[0] = 300
