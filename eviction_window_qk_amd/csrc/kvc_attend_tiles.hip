@@ -25,11 +25,11 @@
 // r sits at place p ^ swizzle(r).  Eight waves share a CU, so that one's softmax runs
 // beside another's products.
 //
-// Measured: a 16384-token prompt, 8 KV heads of 128, 4 rows a token, 2040 us (1080 TFLOP/s,
-// matrix cores busy 52 % at 1.9 GHz; a library product of 8192^3 reaches 1232); of 64
-// values 1210 us (909).  512 tokens over 131072 slots 1150 us (955).  In copies of the
-// kernel the 16384-token prompt took 1761 us without the loads to LDS, 1961 without exp2, 1844 without
-// both and half of the LDS reads.
+// Measured: a 16384-token prompt, 8 KV heads of 128, 4 rows a token, 1970 us (1116 TFLOP/s,
+// matrix cores busy 53 % at 1.9 GHz; a library product of 8192^3 reaches 1257 on that machine);
+// of 64 values 1210 us (909).  512 tokens over 131072 slots 1017 us (1080).  With four waves a
+// workgroup the prompt took 2025 us, and in copies of the kernel 1761 without the loads to
+// LDS, 1961 without exp2, 1971 with half of the reads of V.
 #include <type_traits>
 
 #include "kvc_paged.h"
