@@ -17,7 +17,8 @@
 //
 // m is a reference, not the running maximum: any value serves as long as no sum
 // overflows, so a tile is summed against the present one and m moves to the row's maximum
-// only when a lane's sum passes 2^32 (the first tile always does).
+// only when a lane's sum passes 2^32 (the first tile always does).  A wave whose values are
+// so large that their sums pass fp32 takes them a second time, with smaller weights (loud_of).
 //
 // The keys of a head are cut into pieces by its own length (few_chunk); the four
 // waves of a piece take its 32-key tiles in turn, and their sums meet in LDS.  A
@@ -73,6 +74,8 @@ __device__ __forceinline__ T load(const uint16_t* at) {
 
 // Four output values of row r of a head, and log2 of its sum of 2^x.
 __device__ __forceinline__ void finish(const Args& A, int token, int head, int dim, f32x4 out, float b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = within_bf16(out[i]);
   *reinterpret_cast<u32x2*>(A.a.out.p + token * A.a.out.ts + head * A.a.out.hs + dim) =
       u32x2{pack_bf16(out.x, out.y), pack_bf16(out.z, out.w)};
   if (A.a.lse && dim == 0)
@@ -244,13 +247,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
 
   float nm[MT], l[MT];  // -m, sum of this lane's weights
   f32x4 acc[MT][kTiles];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    nm[mt] = kFar;
-    l[mt] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) acc[mt][i] = f32x4{0, 0, 0, 0};
-  }
+  Loud loud{kSumLimit, 0.0f};
   const int low = len - mine.y - t0;  // the first token's last key: all rows see the keys up to it
   const float by = A.a.c_log2;
 
@@ -304,13 +301,13 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
         e[j] = fast_exp2(__builtin_fmaf(y[mt][j], by, nm[mt]));
         sum += e[j];
       }
-      if (__any(!(sum <= 0x1p32f))) {
+      if (__any(!(sum <= loud.limit))) {
         float top = y[mt][0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = fmaxf(top, y[mt][j]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float now = fminf(nm[mt], -top * by);
+        const float now = fminf(nm[mt], -top * by - loud.lift);
         const float f = fast_exp2(now - nm[mt]);
         nm[mt] = now;
         l[mt] *= f;
@@ -337,10 +334,28 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
       for (int mt = 0; mt < MT; ++mt) acc[mt][u] = mfma(vf, w[mt], acc[mt][u]);
     }
   };
-  for (int tile = wave * 32; tile < keys; tile += kWaves * 32) {
-    Tile cur;
-    fetch(tile, cur);
-    work(tile, cur, tile + 31 > low || none_of[tile >> 5] != 0);
+  for (bool again = false;; again = true) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      nm[mt] = kFar;
+      l[mt] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) acc[mt][i] = f32x4{0, 0, 0, 0};
+    }
+    int first = wave;
+    asm volatile("" : "+v"(first));          // or the first tile's addresses stay in registers
+    for (int tile = first * 32; tile < keys; tile += kWaves * 32) {
+      Tile cur;
+      fetch(tile, cur);
+      work(tile, cur, tile + 31 > low || none_of[tile >> 5] != 0);
+    }
+    float over = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i) over += unless_finite(acc[mt][i].x, acc[mt][i].y, acc[mt][i].z, acc[mt][i].w);
+    if (again || !__any(over != over)) break;
+    loud = loud_of(4 * kFewMaxChunk / (32 * kWaves));   // four lanes a row and tile
   }
 
   // The waves' sums meet in LDS (over the look-ups), 16 rows at a time.
@@ -380,7 +395,16 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
         L = __builtin_fmaf(aw[D + 1], f, L);
       }
       const bool any = L > 0.0f;
-      sum = any ? sum * (1.0f / L) : f32x4{0, 0, 0, 0};
+      const float by_L = any ? 1.0f / L : 0.0f;
+      sum *= by_L;
+      if (any && unless_finite(sum.x, sum.y, sum.z, sum.w) != 0.0f) {   // each wave's share first
+        sum = f32x4{0, 0, 0, 0};
+        for (int w = 0; w < kWaves; ++w) {
+          const float* aw = at + w * kept * kRowF;
+          sum += *reinterpret_cast<const f32x4*>(aw + dim) * (fast_exp2(aw[D] - M) * by_L);
+        }
+      }
+      sum = any ? sum : f32x4{0, 0, 0, 0};
       const float bsum = any ? M + fast_log2(L) : -INFINITY;
       if constexpr (WHOLE) {       // over the first wave's, which nobody else reads any more
         *reinterpret_cast<f32x4*>(at + dim) = sum;

@@ -18,7 +18,8 @@
 // The reference m of a row (w = 2^(x - m)) is not the running maximum: any value serves
 // as long as no sum overflows, so a block is summed against the present one and m moves
 // to the row's maximum only when a lane's sum passes 2^32 (the first block always
-// does).
+// does).  Values so large that their sums pass fp32 before that are taken a second
+// time, with smaller weights (loud_of).
 //
 // Tiles go from global memory to LDS without passing registers, one tile ahead, in
 // the order in which the LDS banks serve both kinds of reads: 16-byte piece p of row
@@ -157,10 +158,14 @@ __device__ __forceinline__ bool find(const Args& A, Where& w) {
   return s >= 0 && w.r0 < w.R;
 }
 
+// What a workgroup computes, with threads counted by `thread`.  Returns whether any wave's results
+// are not finite; such waves leave their results to a second call (LOUD), in which the others help to
+// load.  A wave decides for itself: its rows are the same whatever kW.
 // kW: waves of a workgroup.  GROUP: keys that a look-up in the table covers, of a wave's load all where pages hold
 // whole loads, or one; 0: no cache.
-template <int D, int GROUP, int kW>
-__global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
+template <int D, int GROUP, int kW, bool LOUD>
+__device__ __forceinline__ bool attend_tiles(const Args& A, int thread, bool& wanted, uint16_t (&ks)[2][kTile * D],
+                                             uint16_t (&vs)[2][kTile * D], int (&flags)[kW]) {
   constexpr bool PAGED = GROUP != 0;
   constexpr int kPieces = D / 8;             // 16-byte pieces of a row
   constexpr int kRowsPerLoad = 64 / kPieces; // rows one wave's load covers
@@ -170,13 +175,11 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
   constexpr int kPerTile = PAGED ? kTile / GROUP : 1;    // look-ups of a tile
   constexpr int kBatch = PAGED ? 64 / kPerTile : 1;      // tiles that a wave's 64 look-ups cover
   static_assert(GROUP == 0 || GROUP == 1 || GROUP == kRowsPerLoad, "a load's rows, or one");
-  __shared__ __align__(16) uint16_t ks[2][kTile * D];
-  __shared__ __align__(16) uint16_t vs[2][kTile * D];
 
   Where w;
-  if (!find<PAGED, kW>(A, w)) return;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (!find<PAGED, kW>(A, w)) return false;
+  const int lane = thread & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(thread >> 6);
   const int j = lane & 31, hh = lane >> 5;
   const int r = w.r0 + wave * 32 + j;
   const int rc = r < w.R ? r : w.R - 1;      // rows that are none repeat the last one, never written
@@ -273,6 +276,7 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
   const float by = A.c_log2;
 
   const int n_tiles = to > from ? (to - from + kTile - 1) / kTile : 0;
+  const Loud loud = LOUD ? loud_of(2 * n_tiles) : Loud{kSumLimit, 0.0f};   // two lanes a row and tile
   if (PAGED) rows = look_up(from);
   if (n_tiles > 0) fetch(from, 0, rows, 0);
   if (PAGED && n_tiles > kBatch) rows_next = look_up(from + kBatch * kTile);
@@ -345,12 +349,12 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
       sum = s0 + s1;
     };
     weigh();
-    if (__any(!(sum <= 0x1p32f))) {
+    if (__any(!(sum <= loud.limit))) {
       float top = sc[0][0];
 #pragma unroll
       for (int e = 1; e < 32; ++e) top = fmaxf(top, sc[e >> 4][e & 15]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      const float now = fminf(nm, -top * by), f = fast_exp2(now - nm);
+      const float now = fminf(nm, -top * by - loud.lift), f = fast_exp2(now - nm);
       nm = now;
       l *= f;
 #pragma unroll
@@ -378,10 +382,39 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
   }
 
   l += __shfl_xor(l, 32);
-  if (r >= w.R) return;
   const bool any = l > 0.0f;
   const float by_l = any ? 1.0f / l : 0.0f;
   const float b_sum = any ? fast_log2(l) - nm : -INFINITY;   // log2 of the row's sum of 2^x
+  u32x2 out[kDims][4];
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      acc[d][e] *= by_l;
+      if constexpr (LOUD) acc[d][e] = within_bf16(acc[d][e]);
+    }
+#pragma unroll
+  for (int d = 0; d < kDims; ++d)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      out[d][e] = u32x2{pack_bf16(acc[d][4 * e], acc[d][4 * e + 1]), pack_bf16(acc[d][4 * e + 2], acc[d][4 * e + 3])};
+  bool more = false;
+  if constexpr (!LOUD) {
+    // Nothing times infinity or NaN is NaN: a row's two lanes at once, beside the vector ALU, which
+    // would take 64 steps (eleven prompts of 2043 tokens on average +3 %).
+    f32x16 none_of = {};
+#pragma unroll
+    for (int d = 0; d < kDims; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        none_of = mfma(u32x4{0, 0, 0, 0}, u32x4{out[d][e].x, out[d][e].y, out[d][e + 1].x, out[d][e + 1].y}, none_of);
+    wanted = __any(none_of[0] != none_of[0]);
+    if (lane == 0) flags[wave] = wanted;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kW; ++x) more |= flags[x] != 0;
+  }
+  if (r >= w.R || wanted != LOUD) return more;
   if (PAGED && w.pieces > 1) {
     const size_t tile = size_t(w.h) * A.slots + (w.first + w.piece * w.tiles + r / kRows), row = tile * kRows + r % kRows;
     float* po = A.part + tile * kRows * D + r % kRows * 4;
@@ -390,20 +423,31 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<f32x4*>(po + (32 * d + 8 * e + 4 * hh) * kRows) =
-            f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]} * by_l;
+            f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]};
     if (hh == 0) A.stat[row] = b_sum;
-    return;
+    return more;
   }
   uint16_t* po = A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs;
 #pragma unroll
   for (int d = 0; d < kDims; ++d)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<u32x2*>(po + 32 * d + 8 * e + 4 * hh) =
-          u32x2{pack_bf16(acc[d][4 * e] * by_l, acc[d][4 * e + 1] * by_l),
-                pack_bf16(acc[d][4 * e + 2] * by_l, acc[d][4 * e + 3] * by_l)};
+    for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x2*>(po + 32 * d + 8 * e + 4 * hh) = out[d][e];
   if (A.lse && hh == 0)
     A.lse[size_t(w.token0 + i) * (A.G * A.H) + head] = b_sum * 0.6931471805599453f;
+  return more;
+}
+
+template <int D, int GROUP, int kW>
+__global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
+  __shared__ __align__(16) uint16_t ks[2][kTile * D];
+  __shared__ __align__(16) uint16_t vs[2][kTile * D];
+  __shared__ int flags[kW];
+  bool wanted = false;
+  int thread = threadIdx.x;
+  if (attend_tiles<D, GROUP, kW, false>(A, thread, wanted, ks, vs, flags)) {
+    asm volatile("" : "+v"(thread));         // or what the two calls share stays in registers
+    attend_tiles<D, GROUP, kW, true>(A, thread, wanted, ks, vs, flags);
+  }
 }
 
 // Joins the pieces of 1024 / D rows of a row tile, each weighted by its sum, four values
@@ -439,9 +483,18 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
     L += f;
   }
   const float by_l = L > 0.0f ? 1.0f / L : 0.0f;
+  if (unless_finite(sum.x, sum.y, sum.z, sum.w) == 0.0f) {
+    sum *= by_l;
+  } else {                                               // each piece's share first
+    sum = f32x4{0, 0, 0, 0};
+    for (int p = 0; p < pieces; ++p)
+      sum += *reinterpret_cast<const f32x4*>(part + p * step * D) * (fast_exp2(A.stat[row + p * step] - base) * by_l);
+  }
+#pragma unroll
+  for (int x = 0; x < 4; ++x) sum[x] = within_bf16(sum[x]);
   const int i = int(quot(A.by_G, uint32_t(r))), head = h * G + r - i * G;
   *reinterpret_cast<u32x2*>(A.out.p + int64_t(mine.x + i) * A.out.ts + int64_t(head) * A.out.hs + dim) =
-      u32x2{pack_bf16(sum.x * by_l, sum.y * by_l), pack_bf16(sum.z * by_l, sum.w * by_l)};
+      u32x2{pack_bf16(sum.x, sum.y), pack_bf16(sum.z, sum.w)};
   if (A.lse && dim == 0)
     A.lse[size_t(mine.x + i) * (G * A.H) + head] =
         L > 0.0f ? (base + fast_log2(L)) * 0.6931471805599453f : -INFINITY;

@@ -99,6 +99,37 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(a), static_cast<__bf16>(b)});
 }
 
+// Values of any finite size.  Weights relative to a reference that lags behind the row's
+// maximum, or many of them, may take a sum past fp32 though the mean they stand for is
+// finite.  A wave whose sums are not finite takes its keys once more, with weights so
+// small that a row's sum stays below 1.  They start kLoudHead binades below the limit, so
+// that scores may climb by as many before the reference moves.  What they bring below
+// 2^-126 is lost: parts of a result below 2^-85 at most.
+constexpr float kSumLimit = 0x1p32f;   // of a lane's sum of a tile, where the reference moves
+constexpr int kLoudHead = 8;
+struct Loud {
+  float limit, lift;   // lift: binades of a row's maximum below 1
+};
+// For rows whose weights are added up by at most `sums` lanes and tiles, of 2^kLoudKeys keys
+// at most each.
+constexpr int kLoudKeys = 5;
+__device__ __forceinline__ Loud loud_of(int sums) {
+  const int e = 33 - __builtin_clz(sums | 1);   // 2^-e * sums < 1/2
+  return Loud{__uint_as_float(uint32_t(127 - e) << 23), float(e + kLoudKeys + kLoudHead)};
+}
+
+// 0 if all of them are finite, otherwise NaN.
+__device__ __forceinline__ float unless_finite(float x, float y, float z, float w) {
+  return __builtin_fmaf(x, 0.0f, y * 0.0f) + __builtin_fmaf(z, 0.0f, w * 0.0f);
+}
+
+// A mean of values within bf16 that the weights' roundings took past its largest, which
+// would round to infinity.
+constexpr float kMostBf16 = 0x1.fep127f;
+__device__ __forceinline__ float within_bf16(float x) {
+  return fabsf(x) > kMostBf16 && fabsf(x) < INFINITY ? copysignf(kMostBf16, x) : x;
+}
+
 // Keys per workgroup of the attention of few rows, for a sequence of len slots: pieces of at most
 // kFewChunk, doubled to kFewMaxChunk while there are more than 64; equal pieces, in
 // multiples of the workgroup's 128-key stride.  A piece depends on the sequence's own

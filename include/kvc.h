@@ -594,7 +594,8 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
  * exp(scale * <q, k[t]>)).  In a cache with weight and pos, weight[t] of each KV head
  * grows by the softmax weights that slot t receives, summed over the new tokens
  * and the group.  fp32 softmax; weights enter the product with V as bf16, whose
- * step is 2^-8 of each.  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.
+ * step is 2^-8 of each.  Values may have any finite size (beside some past 2^64, what a
+ * result holds below 2^-80 may be lost).  scale 0 => 1/sqrt(d), otherwise positive, at most 2^127.
  * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
  * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
  * (a sequence with more counts its first max_new).  group 1..64.  Where group * max_new is

@@ -1,0 +1,94 @@
+"""Values of any finite size in the attention over bf16 pages and within prompts: a softmax's mean of
+finite values is finite, however its scores climb."""
+import numpy as np
+import pytest
+import torch
+
+from eviction_window_qk_amd import kvc, synth
+from oracle import paged as og
+import paged_utils as u
+from q8_utils import dev_bf16, random_rows, rng_of
+
+pytestmark = pytest.mark.gpu
+
+BIG = np.uint16(0x7F7F)     # the largest bf16
+
+
+def loud(seed, shape, kind):
+    """Values as bits: one column as large as bf16 holds, one of its negatives, one of both signs, the
+    others of one size."""
+    rng = rng_of(seed, *shape)
+    x = rng.standard_normal(shape)
+    x *= {"2^100": 2.0 ** 100, "2^126": 2.0 ** 124, "largest": 2.0 ** 124, "quiet": 2.0 ** -100}[kind]
+    b = synth.f32_to_bf16_bits(x.astype(np.float32))
+    if kind == "largest":
+        b[..., 0], b[..., 1] = BIG, BIG | 0x8000
+        b[..., 2] = np.where(rng.random(shape[:-1]) < 0.5, BIG, BIG | 0x8000)
+    return b
+
+
+def climbing(T, d, step):
+    """Keys whose first value rises to `step` * T, and queries that read it: scores in nats, with scale 1."""
+    k = np.zeros((T, d), np.float32)
+    k[:, 0] = np.arange(T) * step
+    k[:, 1] = np.sin(np.arange(T))
+    return synth.f32_to_bf16_bits(k)
+
+
+# (G, lens, new, bs): alone, in pieces, whole heads, more rows than 16, row tiles, pieces of them
+CHUNKS = [
+    (1, [1], [1], 16), (2, [300], [1], 16), (4, [2100], [1], 16), (4, [700], [6], 16), (1, [600], [3], 5),
+    (4, [300], [60], 16), (2, [1500], [100], 24), (1, [1500], [70], 5), (2, [900, 40, 0, 700], [1, 40, 2, 90], 16),
+]
+
+
+@pytest.mark.parametrize("step", [0.0, 0.1, -0.1, 3.0])
+@pytest.mark.parametrize("kind", ["2^100", "2^126", "largest", "quiet"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_size_over_pages(d, kind, step):
+    for i, (G, lens, new, bs) in enumerate(CHUNKS):
+        print(f"[case] {i} d {d} {kind} {step}", flush=True)
+        c = u.random_cache(90 + i, len(lens), 1, d, bs, lens, weights=i % 2 == 1)
+        keys = climbing(max(lens), d, step)
+        for b, L in enumerate(lens):
+            for t in range(L):
+                p, r = c.at(b, t)
+                c.k[p, 0, r] = keys[t]
+        c.v = np.where(c.v == u.NAN, c.v, loud(91 + i, c.v.shape, kind))
+        starts = u.starts_of(new)
+        q = random_rows(92 + i, int(starts[-1]), G, d)
+        q[..., 0] = synth.f32_to_bf16_bits(np.float32([1.0]))[0]
+        out, lse = kvc.paged_attend(u.to_gpu(c), dev_bf16(q), u.dev(starts), scale=1.0, want_lse=True)
+        assert bool(torch.isfinite(out.float()).all())
+        u.check_attention(og.attend(c, og.widen(q), starts, scale=1.0), u.bits(out), lse, max(lens))
+
+
+@pytest.mark.parametrize("step", [0.0, 0.1, 3.0])
+@pytest.mark.parametrize("kind", ["2^100", "2^126", "largest", "quiet"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_size_within_prompts(d, kind, step):
+    lens, G = [300, 1, 129, 700], 2
+    starts = u.starts_of(lens)
+    n = int(starts[-1])
+    k = np.concatenate([climbing(L, d, step) for L in lens])[:, None]
+    v = loud(95, (n, 1, d), kind)
+    q = random_rows(96, n, G, d)
+    q[..., 0] = synth.f32_to_bf16_bits(np.float32([1.0]))[0]
+    out, lse = kvc.prompt_attend(dev_bf16(q), dev_bf16(k), dev_bf16(v), u.dev(starts), scale=1.0, want_lse=True)
+    assert bool(torch.isfinite(out.float()).all())
+    u.check_attention(og.prompt(og.widen(q), og.widen(k), og.widen(v), starts, scale=1.0), u.bits(out), lse, max(lens))
+
+
+def test_loud_heads_leave_the_others_their_bits():
+    """Heads of one call with values of ordinary size get the bits that they get without loud ones beside them."""
+    H, G, d, lens, new = 2, 4, 128, [1100, 900], [2, 70]
+    c = u.random_cache(97, 2, H, d, 16, lens)
+    starts = u.starts_of(new)
+    q = dev_bf16(random_rows(98, int(starts[-1]), H * G, d))
+    plain = kvc.paged_attend(u.to_gpu(c), q, u.dev(starts))
+    c.v[:, 1] = np.where(c.v[:, 1] == u.NAN, c.v[:, 1], BIG)
+    mixed = kvc.paged_attend(u.to_gpu(c), q, u.dev(starts))
+    assert torch.equal(mixed[:, :G].contiguous().view(torch.int16), plain[:, :G].contiguous().view(torch.int16))
+    # weights in bf16, off by 2^-8 of themselves, and the rounding of what they give
+    big = float(og.widen(BIG))
+    assert float(mixed[:, G:].double().min()) >= big * (1 - 2.0 ** -7) and float(mixed[:, G:].double().max()) <= big
