@@ -14,6 +14,10 @@
 // neighbouring slots, and a sum over the workgroup says where its own begin.  A second
 // kernel moves the rows from these to those, the only bytes that have to move.
 //
+// A page that another entry of the table names too (a fork's) is not written: entries in use
+// are counted page by page, and a sequence that would write to a page counted twice stays as
+// it is.  The counts cost a launch before the plan, which starts them at zero.
+//
 // Positions of a head are distinct, so keys are; should they not be, equal keys stay in
 // the order of their slots, and both lists still have the same length.
 #include "kvc_paged.h"
@@ -39,7 +43,23 @@ struct Evict {
   int32_t* count;              // [heads]
   int32_t* from;               // [heads][most]
   int32_t* to;                 // [heads][most]
+  int32_t* users;              // [n_blocks] entries that name a page, of pages that any names
 };
+
+// f(page) for the pages of sequence b's first `slots` slots, by the threads of a workgroup.
+template <class F>
+__device__ __forceinline__ void each_page(const Paged& c, int b, int slots, F f) {
+  const int n = slots > 0 ? int(quot(c.div, uint32_t(slots - 1))) + 1 : 0;
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int page = paged_page(c, b, j);
+    if (page >= 0) f(page);
+  }
+}
+
+__global__ __launch_bounds__(kMoveThreads) void k_evict_users(Evict E) {
+  const int b = blockIdx.x;
+  each_page(E.c, b, paged_len(E.c, b), [&](int page) { E.users[page] = 0; });
+}
 
 __device__ __forceinline__ uint64_t key_of(float w, int pos, int sinks, int64_t recent_from) {
   const uint32_t p = uint32_t(pos < 0 ? 0 : (pos < kLastPos ? pos : kLastPos)), back = kLastPos - p;
@@ -75,6 +95,7 @@ __global__ __launch_bounds__(NT) void k_evict_plan(Evict E) {
   const Paged& c = E.c;
   const int n = blockIdx.x, b = n / c.H, len = paged_len(c, b);
   const int K = E.K, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  if (n == b * c.H) each_page(c, b, len, [&](int page) { atomicAdd(&E.users[page], 1); });
   if (len <= K) {
     if (tid == 0) E.count[n] = 0;
     return;
@@ -267,7 +288,13 @@ __global__ __launch_bounds__(kMoveThreads) void k_evict_move(Evict E) {
   const Paged& c = E.c;
   const int n = blockIdx.x, b = n / c.H, h = n - b * c.H;
   const int moves = E.count[n], p = threadIdx.x % kPieces;
-  if (blockIdx.y == 0 && h == 0 && threadIdx.x == 0 && paged_len(c, b) > E.K) c.seq_len[b] = E.K;
+  // One workgroup a sequence sets its length, and no other one reads it.
+  const bool sets = blockIdx.y == 0 && h == 0 && paged_len(c, b) > E.K;
+  if (!sets && int(blockIdx.y) * kAtOnce >= moves) return;
+  bool shared = false;
+  each_page(c, b, E.K, [&](int page) { shared |= E.users[page] > 1; });
+  if (__syncthreads_or(shared)) return;
+  if (sets && threadIdx.x == 0) c.seq_len[b] = E.K;
   for (int i = blockIdx.y * kAtOnce + threadIdx.x / kPieces; i < moves; i += gridDim.y * kAtOnce) {
     const int from = E.from[size_t(n) * E.most + i], to = E.to[size_t(n) * E.most + i];
     const int64_t rf = paged_row(c, b, h, from), rt = paged_row(c, b, h, to);
@@ -294,15 +321,17 @@ int most_moves(const Paged& c, int K) {
 
 size_t evict_ws(const Paged& c, int K) {
   const size_t heads = size_t(c.B) * c.H;
-  return (heads * (1 + 2 * size_t(most_moves(c, K))) * 4 + 255) & ~size_t(255);
+  return ((heads * (1 + 2 * size_t(most_moves(c, K))) + c.n_blocks) * 4 + 255) & ~size_t(255);
 }
 
 hipError_t launch_paged_evict(const Paged& c, const int32_t* seen, int K, int sinks, int recent,
                               int32_t* ws, hipStream_t s) {
   const int heads = c.B * c.H;
-  Evict E{c, seen, K, sinks, recent, most_moves(c, K), ws, nullptr, nullptr};
+  Evict E{c, seen, K, sinks, recent, most_moves(c, K), ws, nullptr, nullptr, nullptr};
   E.from = ws + heads;
   E.to = E.from + size_t(heads) * E.most;
+  E.users = E.to + size_t(heads) * E.most;
+  k_evict_users<<<unsigned(c.B), kMoveThreads, 0, s>>>(E);
   // By the longest length there can be: few waves meet sooner.
   const auto lds = [](int slots) { return size_t(place(slots)) * 8; };
   if (c.cap <= 2048) k_evict_plan<256, true><<<unsigned(heads), 256, lds(c.cap), s>>>(E);

@@ -1230,7 +1230,9 @@ def prompt_attend(q, k, v, starts, out=None, lse=None, want_lse: bool = False, s
 def paged_evict(cache: PagedCache, seen, budget: int, sinks: int = 4, recent: int = 64, ws=None,
                 stream=None):
     """Cuts every sequence to `budget` slots a head: positions below sinks, the last
-    `recent` of the seen ones (int32 [n_seqs]), then the largest weights.  Returns the cache."""
+    `recent` of the seen ones (int32 [n_seqs]), then the largest weights.  A sequence that
+    shares one of its pages below the budget (a fork) is left as it is, its length too.
+    Returns the cache."""
     dev = cache.device
     s = _here(dev, stream)
     if s is None:

@@ -519,7 +519,7 @@ size_t kvc_pages_workspace_bytes(const kvc_page_table* t, int32_t n_pairs);
  * positions to each head, in any order).  They belong to the sequence, not to its pages:
  * whoever forks a sequence by kvc_pages_fork copies its rows of them.
  * Preconditions (not checked): the rows of attended slots are finite, and a page
- * that is written belongs to one entry of the table. */
+ * that is appended to belongs to one entry of the table (kvc_pages_fork sees to it). */
 typedef struct kvc_paged_cache {
   int32_t n_seqs;        /* B sequences; 0 = nothing to do                   */
   int32_t kv_heads;      /* H KV heads, n_seqs * kv_heads < 2^24             */
@@ -634,8 +634,11 @@ int kvc_prompt_attend(int32_t n_seqs, int32_t kv_heads, int32_t group, int32_t h
  * Their seq_len becomes budget; shorter sequences are left as they are.  Needs weight
  * and pos.  budget >= 1, sinks, recent >= 0, n_seqs * kv_heads < 2^22.
  * A move from or to a slot in no page carries weight and pos only.
- * Precondition (not checked): a page of a sequence longer than budget belongs to one
- * entry of the table.
+ * A sequence longer than budget one of whose pages below it another entry in use names
+ * too (an entry of the first ceil(seq_len / block_size) ones of any sequence: what a fork
+ * shares) is left as it is, its seq_len too.  To cut both, give one of them pages of its
+ * own first: kvc_pages_free it, set its length again, kvc_pages_alloc, and kvc_pages_copy
+ * from the other's row of the table to its own.  Pages shared with another table are not seen.
  * ws: at least kvc_paged_evict_workspace_bytes(c, budget), 256-byte aligned; calls that
  * share one must not run at once. */
 int kvc_paged_evict(const kvc_paged_cache* c, const int32_t* seen, int32_t budget, int32_t sinks,

@@ -140,9 +140,13 @@ def prompt(q, k, v, starts, scale=0.0):
 
 
 def evict(c: Cache, seen, budget, sinks, recent):
+    used = [int(c.table[b, j]) for b in range(c.B) for j in range(-(-c.length(b) // c.bs))]
     for b in range(c.B):
         L = c.length(b)
         if L <= budget:
+            continue
+        below = [int(p) for p in c.table[b, : -(-budget // c.bs)] if 0 <= p < c.n]
+        if any(used.count(p) > 1 for p in below):          # somebody else's too
             continue
         for h in range(c.H):
             n = b * c.H + h
