@@ -24,7 +24,8 @@ def _cache(**kw):
 
 
 def test_evictions_ask_for_a_count_a_page():
-    a, b = (kvc.lib().kvc_paged_evict_workspace_bytes(ctypes.addressof(_cache(n_blocks=n)), 50) for n in (64, 64 + 4096))
+    few, many = _cache(n_blocks=64), _cache(n_blocks=64 + 4096)
+    a, b = (kvc.lib().kvc_paged_evict_workspace_bytes(ctypes.addressof(c), 50) for c in (few, many))
     assert b - a == 4 * 4096 and a >= 3 * 4 * (1 + 2 * 50) * 4 + 64 * 4
 
 
