@@ -48,13 +48,12 @@ constexpr int kWholePieces = 3;          // pieces of a head that one workgroup 
 
 struct Args {
   AttendCall a;
-  int pieces, rows;  // of the longest length and the longest chunk: the grid's and the partials'
+  int pieces, rows;  // of the longest length and the longest chunk: the grid's
   FastDiv by_G, by_pieces, by_H;
   int units;         // (head, piece) pairs of this launch
   int n0;            // its first head
-  float* part;       // [n][row][piece][D] outputs of a piece
-  float* stat;       // [n][row][piece] log2 of its sum of 2^x
-  float* scores;     // NULL, or [n][row][score_stride] x
+  Partials places;   // of a sequence [row][piece]
+  float* scores;     // NULL, or x: [row][score_stride] from first_score on
   int score_stride;
 };
 
@@ -72,6 +71,16 @@ __device__ __forceinline__ T load(const uint16_t* at) {
   else return *reinterpret_cast<const T*>(at);
 }
 
+// Place of the first piece of a head's first row.
+__device__ __forceinline__ size_t place_of(const Args& A, int start, int b, int h) {
+  return size_t(h) * A.places.total + first_place(A.places, start, b, A.a.G);
+}
+
+// A head's first row of scores.
+__device__ __forceinline__ float* first_score(const Args& A, int start, int b, int h, int R) {
+  return A.scores + (score_rows(start, b, A.a.G, A.rows) * A.a.c.H + h * R) * A.score_stride;
+}
+
 // Four output values of row r of a head, and log2 of its sum of 2^x.
 __device__ __forceinline__ void finish(const Args& A, int token, int head, int dim, f32x4 out, float b) {
 #pragma unroll
@@ -85,9 +94,9 @@ __device__ __forceinline__ void finish(const Args& A, int token, int head, int d
 // What four slots of a head from t on receive from its R rows: the sum down the rows of
 // 2^(x - log2 of the row's sum), less: minus these logarithms.  The scores were kept (4
 // bytes a row and slot; the keys would be 2 * d bytes a slot again).
-__device__ __forceinline__ void weigh_four(const Args& A, int n, int t, int len, int R, const float* less,
-                                           const float* was, float* to) {
-  const float* x = A.scores + size_t(n) * A.rows * A.score_stride + t;
+__device__ __forceinline__ void weigh_four(const Args& A, const float* scores, int t, int len, int R,
+                                           const float* less, const float* was, float* to) {
+  const float* x = scores + t;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 8
   for (int r = 0; r < R; ++r) {
@@ -180,6 +189,8 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
   if (!WHOLE && t0 >= len && piece > 0) return;
   const int left = len > t0 ? len - t0 : 0, keys = left < chunk ? left : chunk;  // of this piece
   const bool alone = len <= chunk;
+  const int pieces = alone ? 1 : (len + chunk - 1) / chunk;
+  const size_t place = WHOLE ? 0 : place_of(A, mine.x, b, h) + piece;   // of the first row
   // Rows of the look-ups, then the waves' sums.
   uint32_t* const where = reinterpret_cast<uint32_t*>(lds_raw) + (WHOLE ? piece * (kFewChunk / GROUP) : 0);
   uint32_t* const none_of = none_all + (WHOLE ? piece * (kFewChunk / 32) : 0);
@@ -248,6 +259,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
   float nm[MT], l[MT];  // -m, sum of this lane's weights
   f32x4 acc[MT][kTiles];
   Loud loud{kSumLimit, 0.0f};
+  float* const scores = A.scores ? first_score(A, mine.x, b, h, R) : nullptr;
   const int low = len - mine.y - t0;  // the first token's last key: all rows see the keys up to it
   const float by = A.a.c_log2;
 
@@ -284,7 +296,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
       for (int mt = 0; mt < MT; ++mt) {
         const int r = mt * 16 + col;
         if (r < R) {
-          float* to = A.scores + (size_t(n) * A.rows + r) * A.score_stride + t0 + tile + 4 * g;
+          float* to = scores + size_t(r) * A.score_stride + t0 + tile + 4 * g;
 #pragma unroll
           for (int half = 0; half < 2; ++half)
             *reinterpret_cast<f32x4*>(to + half * 16) =
@@ -411,14 +423,14 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
         if (dim == 0) at[D + 2] = bsum;
         continue;
       }
-      if (A.scores && dim == 0) A.stat[(size_t(n) * A.rows + r0 + r) * A.pieces + piece] = bsum;
+      const size_t at_piece = place + (r0 + r) * pieces;
+      if (A.scores && dim == 0) A.places.stat[at_piece] = bsum;
       if (alone) {
         const int i = int(quot(A.by_G, uint32_t(r0 + r)));
         finish(A, mine.x + i, h * A.a.G + r0 + r - i * A.a.G, dim, sum, bsum);
       } else {
-        const size_t at_piece = (size_t(n) * A.rows + r0 + r) * A.pieces + piece;
-        *reinterpret_cast<f32x4*>(A.part + at_piece * D + dim) = sum;
-        if (dim == 0) A.stat[at_piece] = bsum;
+        *reinterpret_cast<f32x4*>(A.places.part + at_piece * D + dim) = sum;
+        if (dim == 0) A.places.stat[at_piece] = bsum;
       }
     }
   }
@@ -441,7 +453,7 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
       float was[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) was[i] = t + i < len ? to[i] : 0.0f;
-      weigh_four(A, n, t, len, R, less, was, to);
+      weigh_four(A, scores, t, len, R, less, was, to);
     }
   }
 }
@@ -484,9 +496,9 @@ __device__ __forceinline__ void join_rows(const Args& A, int n, int block, float
   if (!SMALL && by_wave && threadIdx.x >= 64) return;
   const int at_once = (by_wave ? 64 : kThreads) / kLanes, thread = SMALL ? threadIdx.x % 64 : threadIdx.x;
   const int group = thread / kLanes, dim = thread % kLanes * 4;
-  const size_t row = size_t(n) * A.rows + r;
-  const float* st = A.stat + row * A.pieces;
-  const float* part = A.part + row * A.pieces * D + dim;
+  const size_t at = place_of(A, mine.x, b, h) + r * pieces;
+  const float* st = A.places.stat + at;
+  const float* part = A.places.part + at * D + dim;
   float base;
   const float L = by_wave ? whole_sum<kFewPieces>(st, pieces, base) : whole_sum<64>(st, pieces, base);
   const float by_L = L > 0.0f ? 1.0f / L : 0.0f;
@@ -515,8 +527,9 @@ __device__ __forceinline__ void weigh_piece(const Args& A, float* less) {
   int n, piece;
   if (!piece_of(A, n, piece)) return;
   const Paged& c = A.a.c;
-  const int b = int(quot(A.by_H, uint32_t(n)));
-  const int R = chunk_of(A.a.k, b).y * A.a.G, len = paged_len(c, b);
+  const int b = int(quot(A.by_H, uint32_t(n))), h = n - b * c.H;
+  const int2 mine = chunk_of(A.a.k, b);
+  const int R = mine.y * A.a.G, len = paged_len(c, b);
   const int chunk = few_chunk(len), t0 = piece * chunk, end = len - t0 < chunk ? len : t0 + chunk;
   if (R > kFewRows || t0 >= len) return;
   static_assert(kThreads == 8 * kFewRows, "eight lanes a row");
@@ -530,12 +543,13 @@ __device__ __forceinline__ void weigh_piece(const Args& A, float* less) {
   const int first = t0 + int(threadIdx.x) * 4;
   look(first);
   float base;
-  const float L = whole_sum<8>(A.stat + (size_t(n) * A.rows + row) * A.pieces, row < R ? pieces : 0, base);
+  const float L = whole_sum<8>(A.places.stat + place_of(A, mine.x, b, h) + row * pieces, row < R ? pieces : 0, base);
   if (threadIdx.x % 8 == 0) less[row] = L > 0.0f ? -(base + fast_log2(L)) : -INFINITY;   // a row that sees nothing gives nothing
   __syncthreads();
+  const float* scores = first_score(A, mine.x, b, h, R);
   for (int t = first; t < end; t += kThreads * 4) {
     if (t > first) look(t);
-    weigh_four(A, n, t, end, R, less, was, to + t);
+    weigh_four(A, scores, t, end, R, less, was, to + t);
   }
 }
 
@@ -645,15 +659,17 @@ AttendWs attend_ws(const Paged& c, const Chunks& k, int G) {
   };
   w.few_rows = int64_t(G) * k.max_new < kFewRows ? G * k.max_new : kFewRows;
   w.few_pieces = few_max_pieces(c.cap);
-  const size_t n = w.few_pieces > 1 ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : 0;
-  w.few_part = take(n * c.D);
-  w.few_stat = take(c.weight ? size_t(c.B) * c.H * w.few_rows * w.few_pieces : n);
+  const bool many = int64_t(G) * k.max_new > kFewRows;
+  const int most = tile_max_pieces(c.cap), few = w.few_rows * w.few_pieces;
+  w.slots = many ? first_slot(k.n_tokens, c.B, G, most) + 1 : 0;
+  w.places.most = many && most > w.few_pieces ? most : w.few_pieces;
+  w.places.each = many && kTileWork * kTileRows > few ? kTileWork * kTileRows : few;
+  w.places.total = first_place(w.places, k.n_tokens, c.B, G);
+  const size_t n = size_t(w.places.total) * c.H;
+  w.part = take(w.places.most > 1 ? n * c.D : 0);
+  w.stat = take(w.places.most > 1 || c.weight ? n : 0);
   w.score_stride = (c.cap + 31) & ~31;
-  w.scores = take(c.weight ? size_t(c.B) * c.H * w.few_rows * w.score_stride : 0);
-  w.slots = int64_t(G) * k.max_new > kFewRows ? first_slot(k.n_tokens, c.B, G) + 1 : 0;
-  const size_t m = tile_max_pieces(c.cap) > 1 ? size_t(c.H) * w.slots * kTileRows : 0;
-  w.part = take(m * c.D);
-  w.stat = take(m);
+  w.scores = take(c.weight ? size_t(score_rows(k.n_tokens, c.B, G, w.few_rows)) * c.H * w.score_stride : 0);
   w.lse = take(c.weight ? size_t(k.n_tokens) * G * c.H : 0);
   w.total = off;
   return w;
@@ -669,8 +685,9 @@ hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
   A.by_G = fast_div(uint32_t(a.G));
   A.by_pieces = fast_div(uint32_t(A.pieces));
   A.by_H = fast_div(uint32_t(a.c.H));
-  A.part = ws + w.few_part;
-  A.stat = ws + w.few_stat;
+  A.places = w.places;
+  A.places.part = ws + w.part;
+  A.places.stat = ws + w.stat;
   A.scores = a.c.weight ? ws + w.scores : nullptr;
   A.score_stride = w.score_stride;
   if (a.c.D == 128) attend_rows<128>(A, s);
@@ -678,7 +695,7 @@ hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s) {
   if (w.slots > 0) {
     AttendCall t = a;
     t.lse = A.a.lse;
-    const hipError_t e = launch_attend_tiles(t, ws + w.part, ws + w.stat, w.slots, s);
+    const hipError_t e = launch_attend_tiles(t, A.places, w.slots, s);
     if (e != hipSuccess) return e;
   }
   return hipGetLastError();

@@ -64,8 +64,8 @@ struct Args {
   int slots;          // workgroups of a head
   int parts, per;     // ways a head's slots are dealt out to the XCDs, slots in each
   FastDiv by_per, by_parts;
-  float* part;        // [H][slots][D / 4][kRows][4] outputs of a piece
-  float* stat;        // [H][slots][kRows] log2 of its sum of 2^x
+  int most;           // pieces that any sequence is cut into
+  Partials places;    // of a sequence [piece][row], outputs [piece][D / 4][row][4]
 };
 
 // Rows past the end, or in no page, are read from here.
@@ -130,8 +130,8 @@ __device__ __forceinline__ bool find(const Args& A, Where& w) {
   const int at = int(i - nth * A.per) * A.parts + int(unit - h * A.parts);
   const int slot = A.slots - 1 - at;
   if (slot < 0) return false;
-  const int G = A.G;
-  const auto first = [G](int s, int b) { return PAGED ? first_slot(s, b, G) : first_tile(s, b, G, kHere); };
+  const int G = A.G, most = A.most;
+  const auto first = [G, most](int s, int b) { return PAGED ? first_slot(s, b, G, most) : first_tile(s, b, G, kHere); };
   w.b = last_at_or_below(A.k, slot, first);
   const int2 mine = chunk_of(A.k, w.b);
   w.h = int(h);
@@ -416,15 +416,15 @@ __device__ __forceinline__ bool attend_tiles(const Args& A, int thread, bool& wa
   }
   if (r >= w.R || wanted != LOUD) return more;
   if (PAGED && w.pieces > 1) {
-    const size_t tile = size_t(w.h) * A.slots + (w.first + w.piece * w.tiles + r / kRows), row = tile * kRows + r % kRows;
-    float* po = A.part + tile * kRows * D + r % kRows * 4;
+    const size_t at = size_t(w.h) * A.places.total + first_place(A.places, w.token0, w.b, A.G) + w.piece * w.R;
+    float* po = A.places.part + at * D + r * 4;
 #pragma unroll
     for (int d = 0; d < kDims; ++d)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<f32x4*>(po + (32 * d + 8 * e + 4 * hh) * kRows) =
+        *reinterpret_cast<f32x4*>(po + size_t(32 * d + 8 * e + 4 * hh) * w.R) =
             f32x4{acc[d][4 * e], acc[d][4 * e + 1], acc[d][4 * e + 2], acc[d][4 * e + 3]};
-    if (hh == 0) A.stat[row] = b_sum;
+    if (hh == 0) A.places.stat[at + r] = b_sum;
     return more;
   }
   uint16_t* po = A.out.p + int64_t(w.token0 + i) * A.out.ts + int64_t(head) * A.out.hs;
@@ -464,21 +464,21 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
   if (R <= kFewRows || t < 0) return;
   const int tiles = (R + kRows - 1) / kRows, pieces = tile_pieces(paged_len(A.c, b), tiles);
   const int in_tile = int(blockIdx.y) * kAtOnce + int(threadIdx.x) % kAtOnce, r = t * kRows + in_tile;
-  const int slot = first_slot(start, b, G) + t;
-  if (pieces == 1 || r >= R || slot + (pieces - 1) * tiles >= A.slots) return;
+  if (pieces == 1 || r >= R) return;
   const int dim = threadIdx.x / kAtOnce * 4;
-  const size_t row = (size_t(h) * A.slots + slot) * kRows + in_tile;
-  const float* part = A.part + (size_t(h) * A.slots + slot) * kRows * D + (dim * kRows + in_tile * 4);
-  const size_t step = size_t(tiles) * kRows;             // from piece to piece
+  const size_t at = size_t(h) * A.places.total + first_place(A.places, start, b, G);
+  const float* part = A.places.part + at * D + (size_t(dim) * R + r * 4);
+  const float* stat = A.places.stat + at + r;
+  const size_t step = R;                                 // from piece to piece
   float M = -INFINITY;
 #pragma unroll 4
-  for (int p = 0; p < pieces; ++p) M = fmaxf(M, A.stat[row + p * step]);
+  for (int p = 0; p < pieces; ++p) M = fmaxf(M, stat[p * step]);
   const float base = M == -INFINITY ? 0.0f : M;
   float L = 0.0f;
   f32x4 sum = {0, 0, 0, 0};
 #pragma unroll 4
   for (int p = 0; p < pieces; ++p) {
-    const float f = fast_exp2(A.stat[row + p * step] - base);
+    const float f = fast_exp2(stat[p * step] - base);
     sum += *reinterpret_cast<const f32x4*>(part + p * step * D) * f;
     L += f;
   }
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tile
   } else {                                               // each piece's share first
     sum = f32x4{0, 0, 0, 0};
     for (int p = 0; p < pieces; ++p)
-      sum += *reinterpret_cast<const f32x4*>(part + p * step * D) * (fast_exp2(A.stat[row + p * step] - base) * by_l);
+      sum += *reinterpret_cast<const f32x4*>(part + p * step * D) * (fast_exp2(stat[p * step] - base) * by_l);
   }
 #pragma unroll
   for (int x = 0; x < 4; ++x) sum[x] = within_bf16(sum[x]);
@@ -701,7 +701,7 @@ void attend_chunks(Args& A, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attend_tiles(const AttendCall& a, float* part, float* stat, int slots, hipStream_t s) {
+hipError_t launch_attend_tiles(const AttendCall& a, const Partials& places, int slots, hipStream_t s) {
   Args A{};
   A.c = a.c;
   A.k = a.k;
@@ -710,8 +710,8 @@ hipError_t launch_attend_tiles(const AttendCall& a, float* part, float* stat, in
   A.c_log2 = a.c_log2;
   A.q = a.q, A.out = a.out;
   A.lse = a.lse;
-  A.part = part;
-  A.stat = stat;
+  A.most = tile_max_pieces(a.c.cap);
+  A.places = places;
   A.slots = slots;
   if (a.c.D == 128) attend_chunks<128>(A, s);
   else attend_chunks<64>(A, s);

@@ -179,11 +179,37 @@ __host__ __device__ inline int first_tile(int start, int b, int G, int rows = kT
   return int(int64_t(start) * G / rows) + b;
 }
 // (piece, row tile) pairs of a head over a cache, numbered through: tiles * pieces <=
-// max(kTileWork, tiles).  Only a sequence of more than kFewRows rows has any, so b or
-// the count of so many rows before it, whichever is less, bounds those before it.
-__host__ __device__ inline int first_slot(int start, int b, int G) {
-  const int64_t rows = int64_t(start) * G, n = rows / (kFewRows + 1);
-  return int(rows / kTileRows + (kTileWork + 1) * (n < b ? n : int64_t(b)));
+// max(kTileWork, tiles), and pieces <= most, tile_max_pieces of the longest length.  Only a
+// sequence of more than kFewRows rows has any, so b or the count of so many rows before it,
+// whichever is less, bounds those before it.  Either bound alone leaves each sequence
+// enough behind those before it, so the lesser of both does.
+__host__ __device__ inline int first_slot(int start, int b, int G, int most) {
+  const int64_t rows = int64_t(start) * G, some = rows / (kFewRows + 1), n = some < b ? some : b, tiles = rows / kTileRows;
+  const int64_t by_work = tiles + (kTileWork + 1) * n, by_len = most * (tiles + n);
+  return int(by_work < by_len ? by_work : by_len);
+}
+
+// What the pieces of rows leave for their joins, outputs and log2 of the sums of 2^x: a place
+// for each row and piece, [head][sequence][...], in the order that its kernel likes.  A
+// sequence takes at most `most` places a row, and `each` more than it has rows: kTileWork
+// tiles, or kFewRows rows in the pieces of few rows.  Places for kTileRows rows of every
+// sequence that may have many, 64 times, were 2.3 GB for 64 chunks of 64 tokens in
+// tables of 1024 slots (8 heads of 128, 4 rows a token); now 135 MB.
+struct Partials {
+  float* part;        // [place][D]
+  float* stat;        // [place]
+  int64_t total;      // places of a head
+  int most, each;
+};
+__host__ __device__ inline int64_t first_place(const Partials& p, int start, int b, int G) {
+  const int64_t rows = int64_t(start) * G, by_len = rows * p.most, by_work = rows + int64_t(p.each) * b;
+  return by_work < by_len ? by_work : by_len;
+}
+// Rows of a KV head whose scores are kept, before sequence b: a sequence has at most `rows` of
+// them, and no more than its tokens have.
+__host__ __device__ inline int64_t score_rows(int start, int b, int G, int rows) {
+  const int64_t by_token = int64_t(start) * G, by_seq = int64_t(rows) * b;
+  return by_token < by_seq ? by_token : by_seq;
 }
 
 // A call of the attention over the cache.
@@ -198,7 +224,8 @@ struct AttendCall {
 
 // Workspace carve-up, in floats.
 struct AttendWs {
-  size_t few_part, few_stat, scores, part, stat, lse, total;
+  size_t scores, part, stat, lse, total;
+  Partials places;
   int few_rows, few_pieces;  // most rows of a head (at most kFewRows) and pieces
   int slots;                 // first_slot behind the last token, 0: no sequence has many rows
   int score_stride;          // keys of a row of scores
@@ -211,8 +238,7 @@ hipError_t launch_paged_append(const Paged& c, const Chunks& k, const int32_t* p
                                const RopePlan& f, int q_heads, const Rows& q, const Rows& q_out,
                                const Rows& k_new, const Rows& v_new, hipStream_t s);
 hipError_t launch_paged_attend(const AttendCall& a, float* ws, hipStream_t s);
-hipError_t launch_attend_tiles(const AttendCall& a, float* part, float* stat, int slots,
-                               hipStream_t s);
+hipError_t launch_attend_tiles(const AttendCall& a, const Partials& places, int slots, hipStream_t s);
 hipError_t launch_prompt_attend(int H, int G, int D, const Chunks& k, float c_log2, const Rows& q,
                                 const Rows& k_rows, const Rows& v_rows, const Rows& out,
                                 float* lse, hipStream_t s);

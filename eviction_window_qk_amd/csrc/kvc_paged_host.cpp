@@ -132,7 +132,7 @@ int attend_shape(const kvc_paged_cache* c, int32_t group, int32_t n_tokens, int3
     return KVC_EINVAL;
   *k = {nullptr, d->B, n_tokens, max_new > 0 && max_new < n_tokens ? max_new : n_tokens};
   if (int64_t(group) * k->max_new > kFewRows &&   // workgroups of a launch
-      (int64_t(first_slot(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23) ||
+      (int64_t(first_slot(n_tokens, d->B, group, tile_max_pieces(d->cap))) * d->H >= (int64_t(1) << 23) ||
        int64_t(first_tile(n_tokens, d->B, group)) * d->H >= (int64_t(1) << 23)))
     return KVC_EINVAL;
   return KVC_OK;

@@ -599,8 +599,9 @@ int kvc_paged_append(const kvc_paged_cache* c, int32_t n_tokens, const int32_t* 
  * A query that attends to nothing gives zeros and lse = -inf.  max_new: 0
  * (n_tokens), or a bound on the new tokens of a sequence that sizes the launches
  * (a sequence with more counts its first max_new).  group 1..64.  Where group * max_new is
- * past 32: kv_heads * (n_seqs + n_tokens * group / 128) and kv_heads * (65 * n +
- * n_tokens * group / 128) below 2^23, n the lesser of n_seqs and n_tokens * group / 33.
+ * past 32: kv_heads * (n_seqs + t) and kv_heads * min(65 * n + t, p * (n + t)) below 2^23,
+ * with t = n_tokens * group / 128, n the lesser of n_seqs and n_tokens * group / 33, p the
+ * lesser of 64 and the longest length / 512, rounded up.
  * Preconditions (not checked): q is finite, and scores times log2(e) are above -2^63 and
  * finite in fp32.  A head's results depend on its own length, queries and slots alone.
  * ws: at least kvc_paged_attend_workspace_bytes(c, group, n_tokens, max_new), 256-byte
