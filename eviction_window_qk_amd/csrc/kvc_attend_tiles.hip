@@ -97,7 +97,7 @@ __device__ __forceinline__ int swizzle(int row) {
 __device__ __forceinline__ void to_lds(const void* from, const void* to) {
   const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) const void*)to));
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :: "v"(from), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory");
+               :: "v"(from), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory", "m0");
 }
 __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
   return __builtin_bit_cast(
@@ -215,7 +215,7 @@ __device__ __forceinline__ bool attend_tiles(const Args& A, int thread, bool& wa
     return at < 0 ? kNone : uint32_t(at);
   };
   // Bytes of a lane's piece from its tile's (no cache) or its group's first row: below
-  // 2^32, so a load's address is a scalar and these.
+  // 2^32, so a load's address is a scalar base and these, added in 64 bits for each load.
   uint32_t k_off[kLoads], v_off[kLoads];
 #pragma unroll
   for (int x = 0; x < kLoads; ++x) {
