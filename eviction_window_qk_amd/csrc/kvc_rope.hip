@@ -7,9 +7,9 @@
 // 40 rows of 128 values).  What remains is a copy: 2 * d bytes in, 2 * d out a row.
 //
 // Every rotated value is read and written by the one thread that has its pair, so y
-// may be x.  A thread takes eight pairs: 16 bytes of either half of the rotated part
-// (of any alignment: its second half starts anywhere), or two neighbouring 16-byte
-// pieces' worth of interleaved pairs, eight values at a time.
+// may be x.  A thread takes eight pairs, 16 bytes of either half of the rotated part (of
+// any alignment: its second half starts anywhere), or four interleaved pairs, which are 16
+// neighbouring bytes.
 //
 // Measured: 16384 tokens of 32 heads of 128, 38.8 us (134 MB in, 134 out: 6.9 TB/s, part of
 // it out of the last-level cache).  A token a workgroup leaves the few tokens of a decode
@@ -42,7 +42,8 @@ __device__ __forceinline__ void turn_of(const RopePlan& f, int at, int i, float&
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Items of a row that rotates: eight pairs each, then the copied values by eight.
+// Items of a row that rotates: eight pairs each (four when interleaved), then the copied
+// values by eight.
 struct Shape {
   int r, half, turn_items, items;
 };
