@@ -92,12 +92,14 @@ __device__ __forceinline__ int swizzle(int row) {
 // In assembly, as the compiler takes the builtin's store for one that any later read of
 // LDS may want, and waits for the tile on its way before it reads the one that is there
 // (512 tokens over 131072 slots 1220 us for 1147, a 16384-token prompt 2056 for 2025).
+// m0 is a register that the compiler reserves (it warns where it is named as clobbered): it
+// keeps nothing there, and these kernels have no other instruction that reads it.
 // The instruction writes no register; whoever reads the tile waits for it (s_waitcnt) and
 // meets the other waves (barrier) first.
 __device__ __forceinline__ void to_lds(const void* from, const void* to) {
   const uint32_t at = uint32_t(uintptr_t((__attribute__((address_space(3))) const void*)to));
   asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-               :: "v"(from), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory", "m0");
+               :: "v"(from), "s"(__builtin_amdgcn_readfirstlane(at)) : "memory");
 }
 __device__ __forceinline__ u32x2 read_turned(const uint16_t* at) {
   return __builtin_bit_cast(
