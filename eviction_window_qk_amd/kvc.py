@@ -1006,7 +1006,7 @@ def _rows(t, shape, device, name):
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     ts, hs, one = t.stride()
-    if one != 1:
+    if one != 1 and t.numel():
         raise ValueError(f"{name}: rows must be contiguous")
     # a stride that no step is taken by may be anything
     return _pack_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
