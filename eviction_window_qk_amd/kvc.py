@@ -1027,11 +1027,33 @@ def _count(n, name):
     return n if n <= 0x7fffffff else _int(n, name)
 
 
+class _Rotate(torch.autograd.Function):
+    """The rotation of a tensor that requires a gradient: the other way round on its way back."""
+
+    @staticmethod
+    def forward(ctx, x, plan, positions, backward):
+        ctx.plan, ctx.back = plan, backward
+        ctx.save_for_backward(positions)
+        return rope(plan, x, positions, backward=backward)
+
+    @staticmethod
+    def backward(ctx, g):
+        g = g.contiguous()                       # of a sum it is one value, expanded
+        g = g if g.data_ptr() % 16 == 0 else g.clone()
+        return rope(ctx.plan, g, ctx.saved_tensors[0], backward=not ctx.back), None, None, None
+
+
 def rope(plan: Rope, x, positions, y=None, backward: bool = False, stream=None):
     """Rotates x (bf16 [n_tokens, heads, d], rows contiguous) by positions (int32
     [n_tokens]) into y (None: a new tensor; x itself: in place).  backward: by the
-    transposed map.  Returns y."""
+    transposed map.  A new tensor of an x that requires a gradient passes it on; into a
+    given y such an x is refused.  Returns y."""
     dev = plan.device
+    if (x.requires_grad or (y is not None and y.requires_grad)) and torch.is_grad_enabled():
+        if y is not None:
+            raise ValueError("y: no gradient passes through a given tensor; leave it out, or use torch.no_grad()")
+        with _there(dev, stream):
+            return _Rotate.apply(x, plan, positions, bool(backward))
     s = _here(dev, stream)
     if s is None:
         with _there(dev, stream):
