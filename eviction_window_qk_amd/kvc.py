@@ -978,6 +978,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = None, f
     pair = lambda turns: rot_dim * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(base))  # noqa: E731
     first, last = max(math.floor(pair(fast)), 0), min(math.ceil(pair(slow)), rot_dim - 1)
     gone = ((i - first) / max(last - first, 0.001)).clamp(0, 1)
+    if pair(slow) < 0:                  # the fastest pair turns less than slow times already
+        gone = torch.ones_like(i)
     return freq * (1 - gone + gone / factor), 0.1 * math.log(factor) + 1.0
 
 
