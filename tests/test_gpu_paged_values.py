@@ -92,3 +92,60 @@ def test_loud_heads_leave_the_others_their_bits():
     # weights in bf16, off by 2^-8 of themselves, and the rounding of what they give
     big = float(og.widen(BIG))
     assert float(mixed[:, G:].double().min()) >= big * (1 - 2.0 ** -7) and float(mixed[:, G:].double().max()) <= big
+
+
+def test_loud_workgroups_of_eight_waves_give_the_bits_of_four():
+    """Long prompts and chunks (256 rows a workgroup) whose values are loud in one sequence, and for some keys only in the
+    other, against each KV head alone (128 rows)."""
+    d, H, G = 128, 8, 8
+    lens = [2048, 37, 1100]
+    starts = u.dev(u.starts_of(lens))
+    n = sum(lens)
+    bits = random_rows(100, n, (G + 2) * H, d)
+    bits[:2048, (G + 1) * H:] = loud(101, (2048, H, d), "largest")
+    bits[2900:2910, (G + 1) * H + 3] = loud(102, (10, d), "largest")
+    rows = dev_bf16(bits)
+    q, k, v = rows[:, : G * H], rows[:, G * H: (G + 1) * H], rows[:, (G + 1) * H:]
+    out, lse = kvc.prompt_attend(q, k, v, starts, want_lse=True)
+    assert bool(torch.isfinite(out.float()).all())
+    for h in range(H):
+        o, z = kvc.prompt_attend(q[:, h * G: (h + 1) * G], k[:, h: h + 1], v[:, h: h + 1], starts, want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[:, h * G: (h + 1) * G].contiguous().view(torch.int16))
+        assert torch.equal(z, lse[:, h * G: (h + 1) * G])
+    H, G = 4, 4
+    c = u.random_cache(103, 2, H, d, 16, [8192, 7001])
+    c.v[:, 1:3] = np.where(c.v[:, 1:3] == u.NAN, u.NAN, loud(104, c.v[:, 1:3].shape, "largest"))
+    starts = u.dev(u.starts_of([512, 401]))
+    q = dev_bf16(random_rows(105, 913, G * H, d))
+    out, lse = kvc.paged_attend(u.to_gpu(c), q, starts, want_lse=True)
+    assert bool(torch.isfinite(out.float()).all())
+    for h in range(H):
+        one = u.to_gpu(og.Cache(c.k[:, h: h + 1], c.v[:, h: h + 1], c.table, c.lens))
+        o, z = kvc.paged_attend(one, q[:, h * G: (h + 1) * G], starts, want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[:, h * G: (h + 1) * G].contiguous().view(torch.int16))
+        assert torch.equal(z, lse[:, h * G: (h + 1) * G])
+
+
+@pytest.mark.parametrize("weights", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_loud_heads_taken_whole_give_the_bits_of_pieces(d, weights):
+    """Enough heads that a workgroup takes one whole, loud ones among them, and each sequence alone."""
+    B, H, G = 13, 8, 3
+    lens = [1100, 1, 513, 0, 1024, 700, 1536, 20, 1100, 1100, 1300, 999, 512]
+    c = u.random_cache(106, B, H, d, 16, lens, tb=96, weights=weights)
+    v = loud(107, c.v.shape, "largest")
+    v[:, ::3] = random_rows(108, *v[:, ::3].shape)
+    c.v = np.where(c.v == u.NAN, c.v, v)
+    starts = u.starts_of([2] * B)
+    q = dev_bf16(random_rows(109, 2 * B, G * H, d))
+    g = u.to_gpu(c)
+    out, lse = kvc.paged_attend(g, q, u.dev(starts), max_new=2, want_lse=True)
+    u.check_attention(og.attend(c, og.widen(u.bits(q)), starts), u.bits(out), lse, max(lens))
+    for b in range(B):
+        heads = slice(b * H, (b + 1) * H)
+        one = kvc.PagedCache(g.k_pool, g.v_pool, g.table[b: b + 1], g.seq_len[b: b + 1],
+                             weight=u.dev(c.weight[heads]) if weights else None, pos=u.dev(c.pos[heads]) if weights else None)
+        o, z = kvc.paged_attend(one, q[2 * b: 2 * b + 2], u.dev(u.starts_of([2])), want_lse=True)
+        assert torch.equal(o.view(torch.int16), out[2 * b: 2 * b + 2].view(torch.int16)) and torch.equal(z, lse[2 * b: 2 * b + 2])
+        if weights:
+            assert torch.equal(one.weight, g.weight[heads])
