@@ -278,7 +278,9 @@ __device__ __forceinline__ bool attend_tiles(const Args& A, int thread, bool& wa
   const float by = A.c_log2;
 
   const int n_tiles = to > from ? (to - from + kTile - 1) / kTile : 0;
-  const Loud loud = LOUD ? loud_of(2 * n_tiles) : Loud{kSumLimit, 0.0f};   // two lanes a row and tile
+  // Two lanes a row and tile, of the tiles that the wave's own rows see.
+  const int to_here = high + 1 < to ? high + 1 : to;
+  const Loud loud = LOUD ? loud_of(to_here > from ? 2 * ((to_here - from + kTile - 1) / kTile) : 1) : Loud{kSumLimit, 0.0f};
   if (PAGED) rows = look_up(from);
   if (n_tiles > 0) fetch(from, 0, rows, 0);
   if (PAGED && n_tiles > kBatch) rows_next = look_up(from + kBatch * kTile);
