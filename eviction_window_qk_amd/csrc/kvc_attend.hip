@@ -27,9 +27,9 @@
 // piece's keys are is looked up once, into LDS, four keys at a time where the page size
 // is a multiple of four.
 //
-// Measured (128 values, the kernel alone): 4 rows of 131072 slots of 8 heads 83 us (537 MB,
-// 6.5 TB/s), 7 rows of about 1100 slots of 256 heads with their weights, in one launch,
-// 32.6 us (145 MB, 4.5 TB/s): there the start, the join and the weights of a head are a
+// Measured (128 values, the kernel alone): 4 rows of 131072 slots of 8 heads 84 us (537 MB,
+// 6.4 TB/s), 7 rows of about 1100 slots of 256 heads with their weights, in one launch,
+// 33 us (145 MB, 4.4 TB/s): there the start, the join and the weights of a head are a
 // quarter of its time, and the next head's loads do not cover them.
 #include "kvc_paged.h"
 
@@ -609,7 +609,10 @@ void attend_whole(Args A, hipStream_t s) {
 // round of them.  Heads of 1100 slots, 7 rows, us (one launch : two): 64 heads 16.9 : 13.3,
 // 96 heads 17.3 : 18.9, 256 heads 27.4 : 30.8 (with weights 33.1 : 39.6), 288 heads 46.4 :
 // 36.3, 512 heads 53.5 : 56.1, 2048 heads 207 : 228 (with weights the same); 400 slots with
-// weights, 256 heads 16.5 : 19.0.
+// weights, 256 heads 16.5 : 19.0.  The host knows no lengths: `pieces` are those of the
+// longest one that the table, or max_len, has room for.  256 heads of about 1090 slots, 7 rows, in
+// tables of 1536, 2048, 4096, 32768 slots: 27, 35, 38, 45 us, with weights 33, 43, 47, 64; with
+// max_len 1536 27 and 33 in all of them.
 bool whole_heads(int heads, int pieces, int rows, bool weights) {
   if (rows > 16 || pieces > kWholePieces) return false;
   if (pieces == 1) return weights;

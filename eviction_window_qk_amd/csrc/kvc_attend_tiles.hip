@@ -26,10 +26,11 @@
 // r sits at place p ^ swizzle(r).  Eight waves share a CU, so that one's softmax runs
 // beside another's products.
 //
-// Measured: a 16384-token prompt, 8 KV heads of 128, 4 rows a token, 1970 us (1116 TFLOP/s,
-// matrix cores busy 53 % at 1.9 GHz; a library product of 8192^3 reaches 1257 on that machine);
-// of 64 values 1210 us (909).  512 tokens over 131072 slots 1017 us (1080).  With four waves a
-// workgroup the prompt took 2025 us, and in copies of the kernel 1761 without the loads to
+// Measured, machine to machine: a 16384-token prompt, 8 KV heads of 128, 4 rows a token,
+// 1910 to 2000 us (1150 to 1100 TFLOP/s, matrix cores busy 53 % at 1.9 GHz; a library product of
+// 8192^3 reaches 1232 to 1268); of 64 values 1105 to 1210 us (995 to 909).  512 tokens over 131072
+// slots 970 to 1060 us (1130 to 1040).  With four waves a workgroup the prompt took 2025 us
+// where it takes 1970 with eight, and in copies of the kernel 1761 without the loads to
 // LDS, 1961 without exp2, 1971 with half of the reads of V.
 #include <type_traits>
 
@@ -455,7 +456,7 @@ __global__ __launch_bounds__(kW * 64, 2) void k_attend_tiles(Args A) {
 }
 
 // Joins the pieces of 1024 / D rows of a row tile, each weighted by its sum, four values
-// a lane, in the partials' order: 4 D bytes a row and piece, 15 us of the 255 of a mixed
+// a lane, in the partials' order: 4 D bytes a row and piece, 15 us of the 270 of a mixed
 // batch (24 sequences of up to 16384 slots of 8 heads of 64, 1183 new tokens).
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_join_tiles(Args A, FastDiv by_tiles) {

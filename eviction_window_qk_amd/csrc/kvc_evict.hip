@@ -281,7 +281,7 @@ __global__ __launch_bounds__(NT) void k_evict_plan(Evict E) {
 
 // A row's 16-byte pieces by D/8 lanes; the lists' slots are disjoint, so the order does
 // not matter.  Bound by HBM: 32 heads of 16384 slots cut to 4096 move 98000 rows of 512 bytes
-// in 18.3 us (100 MB in and out, 5.5 TB/s).
+// in 18 to 19 us (100 MB in and out, 5.3 to 5.5 TB/s).
 template <int D>
 __global__ __launch_bounds__(kMoveThreads) void k_evict_move(Evict E) {
   constexpr int kPieces = D / 8, kAtOnce = kMoveThreads / kPieces;
