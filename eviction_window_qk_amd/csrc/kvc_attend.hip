@@ -363,9 +363,12 @@ __global__ __launch_bounds__(WHOLE ? kWholePieces * kThreads : kThreads, WHOLE ?
     }
     float over = 0.0f;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int mt = 0; mt < MT; ++mt) {
+      float here = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) over += unless_finite(acc[mt][i].x, acc[mt][i].y, acc[mt][i].z, acc[mt][i].w);
+      for (int i = 0; i < kTiles; ++i) here += unless_finite(acc[mt][i].x, acc[mt][i].y, acc[mt][i].z, acc[mt][i].w);
+      over += mt * 16 + col < R ? here : 0.0f;   // a place without a row weighs all keys alike
+    }
     if (again || !__any(over != over)) break;
     loud = loud_of(4 * kFewMaxChunk / (32 * kWaves));   // four lanes a row and tile
   }

@@ -165,3 +165,31 @@ def test_loud_rows_go_by_their_own_wave():
         o, z = kvc.prompt_attend(q[:, h: h + 1], k[:, h: h + 1], v[:, h: h + 1], starts, want_lse=True)
         same = torch.equal(o.view(torch.int16), out[:, h: h + 1].contiguous().view(torch.int16))
         assert same and torch.equal(z, lse[:, h: h + 1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_places_without_a_row_do_not_make_a_head_loud(d):
+    """16 rows of a head, in a call of 16 rows a head and in one of 32: the places of the other 16 see all keys alike, and
+    what their sums would be does not matter."""
+    T, G = 1500, 16
+    c = u.random_cache(112, 1, 1, d, 16, [T])
+    v = np.abs(og.widen(random_rows(113, *c.v.shape)))
+    c.v = np.where(c.v == u.NAN, c.v, synth.f32_to_bf16_bits((np.minimum(v, 1.9) * 2.0 ** 124).astype(np.float32)))
+    # each wave's first keys hold one far above the others (pieces of 512, tiles of 32 keys): sums of rows stay finite
+    rng = rng_of(114, d)
+    k = rng.standard_normal((T, d)).astype(np.float32)
+    q = rng.standard_normal((2, G, d)).astype(np.float32)
+    q[..., 0] = 1.0
+    t = np.arange(T)
+    k[:, 0] = np.where((t % 512 < 128) & (t % 32 == 3), 100.0, 0.0)
+    kb = synth.f32_to_bf16_bits(k)
+    for t in range(T):
+        p, r = c.at(0, t)
+        c.k[p, 0, r] = kb[t]
+    g = u.to_gpu(c)
+    gq = dev_bf16(synth.f32_to_bf16_bits(q))
+    one, z1 = kvc.paged_attend(g, gq[:1].contiguous(), u.dev(u.starts_of([1])), max_new=1, scale=1.0, want_lse=True)
+    two, z2 = kvc.paged_attend(g, gq, u.dev(np.int32([0, 1])), max_new=2, scale=1.0, want_lse=True)
+    assert bool(torch.isfinite(one.float()).all())
+    same = torch.equal(one.view(torch.int16), two[:1].view(torch.int16)) and torch.equal(z1, z2[:1])
+    assert same
